@@ -35,10 +35,10 @@ CFLAGS = [
 
 
 def source_digest() -> str:
-    """sha256 over the HIP sources and the C header with comments and blank
+    """sha256 over the HIP sources and the C headers with comments and blank
     space removed: edits to comments alone keep it."""
     h = hashlib.sha256()
-    files = sorted(glob.glob(os.path.join(CSRC, "*"))) + [os.path.join(INCLUDE, "q4linear.h")]
+    files = sorted(glob.glob(os.path.join(CSRC, "*"))) + sorted(glob.glob(os.path.join(INCLUDE, "*.h")))
     for f in files:
         with open(f) as fh:
             text = fh.read()

@@ -1,0 +1,375 @@
+// q4_attention_kernels.h -- attention of new tokens over the paged 8-bit
+// cache, few query rows per workgroup.
+//
+//   out[t, h] = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q . k_j - max)
+//
+// Mathematics.  Keys and values are int8 codes with one scale per page, so
+// both contractions run on the integer matrix unit without unpacking a code.
+// A query row is held as X 2^-e with X an integer of ND signed 8-bit digits,
+// X = sum_i d_i 256^i: ND exact int32 dot products q . k per score, joined in
+// fp32.  The probabilities of a tile of 64 tokens are held the same way
+// against the tile's own largest (which is 1 for the largest score): the
+// tile's contribution is an exact integer sum, and running maximum, sum and
+// output are fp32.  Three digits keep 23 bits (fp32 queries), two keep 15
+// (16-bit queries, whose own rounding is 2^-8 or 2^-11).
+//
+// Layout.  A wave holds 16 query rows as the columns of both products:
+// S^T = K Q^T gives lane l the scores of column l % 16 for 4 rows of each of
+// 4 key tiles, O^T = V^T P^T wants from it 16 consecutive tokens.  Reading
+// key row r of tile a from token 16 (r / 4) + 4 a + r % 4 makes these the
+// same 16 tokens (16 g .. 16 g + 15, g = l / 16), so the probabilities go
+// from one product to the next in registers, and a lane's 16 bytes of V lie
+// together because the cache keeps tokens innermost.  A column's maximum
+// and sum need two exchanges between the four lane groups.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "q4_kv.h"
+#include "q4_serve.h"
+#include "q4_serve_device.h"
+
+namespace q4 {
+namespace attn {
+
+constexpr int kTile = 64;   // tokens per step of a wave
+constexpr int kWaves = 4;   // waves of a workgroup, each over its own tiles
+constexpr int kRows = 16;   // query rows of a workgroup
+constexpr int kThreads = 64 * kWaves;
+
+// largest integer that ND digits hold with the offsets of pack_digits
+template <int ND>
+__device__ __forceinline__ constexpr float digit_max() {
+  return ND == 3 ? 8323072.0f : 32512.0f;  // 127 * 256^(ND - 1)
+}
+template <int ND>
+__device__ __forceinline__ constexpr uint32_t digit_bias() {
+  return ND == 3 ? 0x8080u : 0x80u;
+}
+
+// Digits of four integers, each given as X + digit_bias: word i holds digit i
+// of the four.  With the bias added, byte i of the sum is d_i + 128 for all
+// but the top digit, and flipping its top bit gives d_i.
+template <int ND>
+__device__ __forceinline__ void pack_digits(uint32_t b0, uint32_t b1, uint32_t b2, uint32_t b3,
+                                            uint32_t (&w)[ND]) {
+  const uint32_t lo = __builtin_amdgcn_perm(b1, b0, 0x05010400u);
+  const uint32_t hi = __builtin_amdgcn_perm(b3, b2, 0x05010400u);
+  w[0] = __builtin_amdgcn_perm(hi, lo, 0x05040100u) ^ 0x80808080u;
+  w[1] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);
+  if constexpr (ND == 3) {
+    w[1] ^= 0x80808080u;
+    const uint32_t l2 = __builtin_amdgcn_perm(b1, b0, 0x0c0c0602u);
+    const uint32_t h2 = __builtin_amdgcn_perm(b3, b2, 0x0c0c0602u);
+    w[2] = __builtin_amdgcn_perm(h2, l2, 0x05040100u);
+  }
+}
+
+// sum_i acc_i 256^i in fp32.  The digit sums are below 2^22 in magnitude (64
+// or 256 products of at most 2^14), so the two low ones join exactly.
+template <int ND>
+__device__ __forceinline__ float join_digits(const int32_t (&a)[ND]) {
+  const float low = (float)(a[1] * 256 + a[0]);
+  if constexpr (ND == 3) return __builtin_fmaf((float)a[2], 65536.0f, low);
+  return low;
+}
+
+// The maximum over the four lanes that hold a column.
+__device__ __forceinline__ float column_max(float x) {
+  x = fmaxf(x, __shfl_xor(x, 16, 64));
+  return fmaxf(x, __shfl_xor(x, 32, 64));
+}
+__device__ __forceinline__ float column_sum(float x) {
+  x += __shfl_xor(x, 16, 64);
+  return x + __shfl_xor(x, 32, 64);
+}
+__device__ __forceinline__ uint32_t column_umax(uint32_t x) {
+  x = umax(x, (uint32_t)__shfl_xor((int)x, 16, 64));
+  return umax(x, (uint32_t)__shfl_xor((int)x, 32, 64));
+}
+
+__device__ __forceinline__ float load_elem(const void* p, int64_t i, int32_t dtype) {
+  if (dtype == Q4_DTYPE_F32) return ((const float*)p)[i];
+  if (dtype == Q4_DTYPE_F16) return (float)((const _Float16*)p)[i];
+  return (float)((const bf16*)p)[i];
+}
+__device__ __forceinline__ void store_elem(void* p, int64_t i, float v, int32_t dtype) {
+  if (dtype == Q4_DTYPE_F32) ((float*)p)[i] = v;
+  else if (dtype == Q4_DTYPE_F16) ((_Float16*)p)[i] = (_Float16)v;
+  else ((bf16*)p)[i] = (bf16)v;
+}
+
+// What a workgroup works on, the same for the attention and the join kernel.
+struct Block {
+  SeqSpan sp;
+  int b, h;
+  int64_t row0, rows;  // first query row (token * group + head) and rows of the sequence
+  int tile0, tiles;    // tiles of 64 positions that its queries see
+  KeyRange keys;
+};
+
+__device__ __forceinline__ Block block_of(const AttnParams& p, uint32_t id) {
+  Block k;
+  const int rb = id % p.row_blocks;
+  id /= p.row_blocks;
+  k.h = id % p.c.heads;
+  k.b = id / p.c.heads;
+  k.sp = seq_span(p.c.cu_new, p.c.lengths, k.b, p.T);
+  k.rows = (int64_t)k.sp.n * p.group;
+  k.row0 = (int64_t)rb * kRows;
+  const int64_t last = k.row0 + kRows < k.rows ? k.row0 + kRows : k.rows;
+  k.keys = key_range(k.sp.pos0 + k.row0 / p.group, k.sp.pos0 + (last - 1) / p.group, p.window,
+                     p.max_len);
+  k.tile0 = (int)(k.keys.lo / kTile);
+  k.tiles = k.keys.hi > k.keys.lo ? (int)((k.keys.hi + kTile - 1) / kTile) - k.tile0 : 0;
+  return k;
+}
+
+// Where the 16 tokens at token0 (a multiple of 16) of the sequence lie: their
+// page, and whether they are to be read at all.  page < 0: not in the cache.
+__device__ __forceinline__ int32_t segment_page(const AttnParams& p, const int32_t* row,
+                                                const KeyRange& keys, int64_t token0) {
+  if (token0 + 16 <= keys.lo || token0 >= keys.hi) return -2;  // not seen
+  return page_at(row, p.c.max_pages, p.c.pages, token0 >> p.c.page_log2);
+}
+
+template <int DT, int ND>
+__global__ __launch_bounds__(kThreads) void attention_kernel(AttnParams p) {
+  constexpr int NS = (DT + 3) / 4;  // steps of 64 elements of a head
+  extern __shared__ float lds[];
+  const int split = blockIdx.x % p.splits;
+  const Block k = block_of(p, blockIdx.x / p.splits);
+  if (k.row0 >= k.rows) return;
+  // a block whose tiles fit one split writes its output itself
+  const int n_splits = (k.tiles + p.split_tiles - 1) / p.split_tiles;
+  if (split > 0 && split >= n_splits) return;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int col = lane & 15, g = lane >> 4;
+  const KvCache& c = p.c;
+  const int dim = c.dim, d16 = dim >> 4;
+  const int32_t* table = c.table + (int64_t)k.b * c.table_ld;
+
+  // the lane's query row
+  const int64_t r = k.row0 + col;
+  const bool valid = r < k.rows;
+  const int64_t tok = valid ? r / p.group : 0;
+  const int head = k.h * p.group + (int)(valid ? r - tok * p.group : 0);
+  const int64_t pos = valid ? k.sp.pos0 + tok : -1;
+  const int64_t see_lo64 = p.window > 0 ? pos - p.window + 1 : 0;
+  const int32_t see_hi = (int32_t)(pos < k.keys.hi ? pos : k.keys.hi - 1);  // last position seen
+  const int32_t see_lo = (int32_t)(see_lo64 > 0 ? see_lo64 : 0);
+
+  // its digits: elements 64 s + 16 g .. + 15 of the row, zero past the head
+  i32x4 qd[NS][ND];
+  float q_unit;
+  {
+    const int64_t at = (k.sp.t0 + tok) * p.q_ts + (int64_t)head * p.q_hs;
+    uint32_t amax = 0;
+    float x[NS][16];
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int d = 64 * s + 16 * g + e;
+        x[s][e] = valid && d < dim ? load_elem(p.q, at + d, p.dtype) : 0.0f;
+        amax = umax(amax, abs_bits(x[s][e]));
+      }
+    amax = column_umax(amax);
+    // the power of two that takes the largest element below digit_max; a
+    // row with NaN or infinity gets a NaN unit, and so NaN scores
+    const float a = bits_f32(amax);
+    int ex = __builtin_amdgcn_frexp_expf(a);  // a = m 2^ex, m in [1/2, 1)
+    const float m = __builtin_amdgcn_frexp_mantf(a);
+    int up = (ND == 3 ? 23 : 15) - ex - (m > 127.0f / 128.0f ? 1 : 0);
+    if (amax == 0) up = 0;
+    q_unit = amax >= 0x7f800000u ? bits_f32(0x7fc00000u) : __builtin_amdgcn_ldexpf(p.scale_log2, -up);
+#pragma unroll
+    for (int s = 0; s < NS; ++s)
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        uint32_t bits[4], out[ND];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          bits[e] = (uint32_t)(int)__builtin_rintf(__builtin_amdgcn_ldexpf(x[s][4 * w + e], up)) +
+                    digit_bias<ND>();
+        pack_digits<ND>(bits[0], bits[1], bits[2], bits[3], out);
+#pragma unroll
+        for (int i = 0; i < ND; ++i) qd[s][i][w] = (int32_t)out[i];
+      }
+  }
+
+  float o[DT][4];
+#pragma unroll
+  for (int t = 0; t < DT; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[t][i] = 0.0f;
+  float mx = -__builtin_inff(), sum = 0.0f;  // running maximum (log2), the lane's part of the sum
+
+  const int t_end = (split + 1) * p.split_tiles < k.tiles ? (split + 1) * p.split_tiles : k.tiles;
+  for (int t = split * p.split_tiles + wave; t < t_end; t += kWaves) {
+    const int64_t token0 = (int64_t)(k.tile0 + t) * kTile;
+    // pages of the lane's key rows and of its 16 tokens
+    const int32_t pk = segment_page(p, table, k.keys, token0 + 16 * (col >> 2));
+    const int32_t pg = segment_page(p, table, k.keys, token0 + 16 * g);
+    const int page_mask = c.page - 1;
+    i32x4 kd[4][NS], vd[DT];
+    {
+      const int64_t page_row = ((int64_t)(pk > 0 ? pk : 0) * c.heads + k.h) << c.page_log2;
+      const int slot = (int)((token0 + 16 * (col >> 2) + (col & 3)) & page_mask);
+#pragma unroll
+      for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int s = 0; s < NS; ++s) {
+          const int d = 64 * s + 16 * g;
+          kd[a][s] = *(const i32x4*)(c.k + (page_row + slot + 4 * a) * dim + (d < dim ? d : 0));
+        }
+    }
+    const int64_t ph = (int64_t)(pg > 0 ? pg : 0) * c.heads + k.h;
+    {
+      const int8_t* v = c.v + ph * ((int64_t)dim << c.page_log2) + ((token0 + 16 * g) & page_mask);
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt)
+        vd[dt] = *(const i32x4*)(v + ((int64_t)((dt < d16 ? 16 * dt : 0) + col) << c.page_log2));
+    }
+    const float nan = bits_f32(0x7fc00000u);
+    const float ks = pg >= 0 ? c.ks[ph] : nan, vs = pg >= 0 ? c.vs[ph] : nan;
+
+    // scores, in log2 units
+    float sc[4][4];
+    const float unit = q_unit * ks;
+    const int32_t tok0 = (int32_t)token0 + 16 * g;
+    float top = -__builtin_inff();
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      i32x4 acc[ND];
+#pragma unroll
+      for (int i = 0; i < ND; ++i) {
+        acc[i] = i32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+          acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(kd[a][s], qd[s][i], acc[i], 0, 0, 0);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        int32_t part[ND];
+#pragma unroll
+        for (int n = 0; n < ND; ++n) part[n] = acc[n][i];
+        const int32_t j = tok0 + 4 * a + i;
+        const bool seen = j >= see_lo && j <= see_hi;
+        sc[a][i] = seen ? join_digits<ND>(part) * unit : -__builtin_inff();
+        top = fmaxf(top, sc[a][i]);
+      }
+    }
+    top = column_max(top);
+    const bool any = top > -__builtin_inff();
+    const float ref = any ? top : 0.0f;
+
+    // probabilities against the tile's maximum; the values' scale joins them
+    // before they are made digits, as a tile may hold several pages
+    float part_sum = 0.0f;
+    uint32_t wmax = 0;
+    float pw[4][4];
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int32_t j = tok0 + 4 * a + i;
+        const bool seen = j >= see_lo && j <= see_hi;
+        const float e = exp2_fast(sc[a][i] - ref);  // 0 where not seen
+        part_sum += e;
+        pw[a][i] = seen ? e * vs : 0.0f;
+        wmax = umax(wmax, abs_bits(pw[a][i]));
+      }
+    wmax = column_umax(wmax);
+    const float big = fmaxf(bits_f32(wmax), 1e-30f);  // below it, digits run out
+    const float to_digits = digit_max<ND>() / big;
+    i32x4 pd[ND];
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      uint32_t bits[4], out[ND];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        bits[i] = f32_bits(__builtin_fmaf(pw[a][i], to_digits,
+                                          8388608.0f + (float)digit_bias<ND>()));
+      pack_digits<ND>(bits[0], bits[1], bits[2], bits[3], out);
+#pragma unroll
+      for (int i = 0; i < ND; ++i) pd[i][a] = (int32_t)out[i];
+    }
+
+    const float m_new = fmaxf(mx, top);
+    const float m_ref = m_new > -__builtin_inff() ? m_new : 0.0f;
+    const float alpha = exp2_fast(mx - m_ref);           // 0 before the first seen tile
+    const float beta = any ? exp2_fast(top - m_ref) : 0.0f;
+    mx = m_new;
+    // a tile of NaN scores has no maximum: its sum, NaN, still has to show
+    sum = sum * alpha + (any ? beta * part_sum : (part_sum != part_sum ? part_sum : 0.0f));
+    // wmax as bits: NaN and infinity of a page's scale reach the outputs
+    const float w = any ? beta * (wmax >= 0x7f800000u ? bits_f32(wmax) : big) / digit_max<ND>() : 0.0f;
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) {
+      i32x4 acc[ND];
+#pragma unroll
+      for (int i = 0; i < ND; ++i)
+        acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(vd[dt], pd[i], i32x4{0, 0, 0, 0}, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        int32_t part[ND];
+#pragma unroll
+        for (int n = 0; n < ND; ++n) part[n] = acc[n][i];
+        o[dt][i] = __builtin_fmaf(join_digits<ND>(part), w, o[dt][i] * alpha);
+      }
+    }
+  }
+
+  // join the waves' parts: [wave][row][dim] outputs, then maxima and sums
+  sum = column_sum(sum);
+  const int pitch = 16 * DT + 4;
+  float* lo = lds;
+  float* lm = lds + kWaves * kRows * pitch;
+  float* ls = lm + kWaves * kRows;
+#pragma unroll
+  for (int dt = 0; dt < DT; ++dt)
+    *(f32x4*)&lo[(wave * kRows + col) * pitch + 16 * dt + 4 * g] =
+        f32x4{o[dt][0], o[dt][1], o[dt][2], o[dt][3]};
+  if (g == 0) {
+    lm[wave * kRows + col] = mx;
+    ls[wave * kRows + col] = sum;
+  }
+  __syncthreads();
+  const bool last = n_splits <= 1;
+  for (int i = threadIdx.x; i < kRows * dim; i += kThreads) {
+    const int row = i / dim, d = i - row * dim;
+    const int64_t rr = k.row0 + row;
+    if (rr >= k.rows) break;
+    float m = lm[row];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) m = fmaxf(m, lm[w * kRows + row]);
+    const float ref = m > -__builtin_inff() ? m : 0.0f;
+    float acc = 0.0f, den = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+      const float f = exp2_fast(lm[w * kRows + row] - ref);
+      // a wave without a maximum has a sum of 0, or NaN, which has to show
+      const float sw = ls[w * kRows + row];
+      den += sw != sw ? sw : f * sw;
+      acc += f * lo[(w * kRows + row) * pitch + d];
+    }
+    const int64_t tk = rr / p.group;
+    const int64_t tq = k.sp.t0 + tk, hq = k.h * p.group + (rr - tk * p.group);
+    if (last) {
+      const float v = den == 0.0f ? 0.0f : acc / den;  // no key seen: 0
+      store_elem(p.out, tq * p.o_ts + hq * p.o_hs + d, v, p.dtype);
+    } else {
+      const int64_t at = (int64_t)split * p.T * p.heads + tq * p.heads + hq;
+      p.part_o[at * dim + d] = acc;
+      if (d == 0) {
+        p.part_ml[2 * at] = m;
+        p.part_ml[2 * at + 1] = den;
+      }
+    }
+  }
+}
+
+}  // namespace attn
+}  // namespace q4

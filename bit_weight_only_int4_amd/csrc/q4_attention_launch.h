@@ -1,0 +1,36 @@
+// q4_attention_launch.h -- the attention kernel for one number of digits;
+// included by q4_attention_d2.hip and q4_attention_d3.hip.
+#pragma once
+
+#include "q4_attention_kernels.h"
+
+namespace q4 {
+
+template <int DT, int ND>
+static hipError_t launch_attention_dim(const AttnParams& p, hipStream_t s) {
+  using namespace attn;
+  const size_t lds = (size_t)(kWaves * kRows * (16 * DT + 4) + 2 * kWaves * kRows) * sizeof(float);
+  if (lds > 65536) {
+    const hipError_t e =
+        hipFuncSetAttribute((const void*)attention_kernel<DT, ND>,
+                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+  }
+  const dim3 grid((unsigned)((int64_t)p.batch * p.c.heads * p.row_blocks * p.splits));
+  hipLaunchKernelGGL((attention_kernel<DT, ND>), grid, dim3(kThreads), lds, s, p);
+  return hipGetLastError();
+}
+
+// The kernel holds a head in 16-wide tiles; head sizes between the instances
+// run the next one up (past-the-end tiles are computed and not stored).
+template <int ND>
+hipError_t launch_attention_digits(const AttnParams& p, hipStream_t s) {
+  const int d16 = p.c.dim / 16;
+  if (d16 <= 4) return launch_attention_dim<4, ND>(p, s);
+  if (d16 <= 6) return launch_attention_dim<6, ND>(p, s);
+  if (d16 <= 8) return launch_attention_dim<8, ND>(p, s);
+  if (d16 <= 12) return launch_attention_dim<12, ND>(p, s);
+  return launch_attention_dim<16, ND>(p, s);
+}
+
+}  // namespace q4

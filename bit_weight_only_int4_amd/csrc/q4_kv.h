@@ -1,0 +1,64 @@
+// q4_kv.h -- index arithmetic of the paged cache, shared by the append and
+// attention kernels and compiled for the host by the tests: which tokens a
+// sequence has, where a position lies, and the checks that keep every access
+// inside the arrays whatever the device-side tables hold.
+#pragma once
+
+#include <stdint.h>
+
+#if defined(__HIPCC__)
+#define Q4_HD __host__ __device__ __forceinline__
+#else
+#define Q4_HD inline
+#endif
+
+namespace q4 {
+
+// Sequence b's part of a call: new tokens t0 .. t0 + n - 1 of T, at positions
+// pos0 .. len - 1.  A table that decreases or leaves [0, T] gives n = 0, a
+// negative length is 0.  pos0 may be negative (fewer tokens than new ones):
+// those tokens have no place.
+struct SeqSpan {
+  int32_t t0, n, len, pos0;
+};
+
+Q4_HD SeqSpan seq_span(const int32_t* cu_new, const int32_t* lengths, int64_t b, int64_t T) {
+  SeqSpan s;
+  const int64_t lo = cu_new[b], hi = cu_new[b + 1];
+  const bool ok = lo >= 0 && hi >= lo && hi <= T;
+  s.t0 = ok ? (int32_t)lo : 0;
+  s.n = ok ? (int32_t)(hi - lo) : 0;
+  s.len = lengths[b] > 0 ? lengths[b] : 0;
+  s.pos0 = s.len - s.n;
+  return s;
+}
+
+// The page number at entry `index` of a sequence's table row, or -1 if the
+// entry lies past the table or its page outside the cache.
+Q4_HD int32_t page_at(const int32_t* row, int64_t max_pages, int64_t pages, int64_t index) {
+  if (index < 0 || index >= max_pages) return -1;
+  const int32_t p = row[index];
+  return (p >= 0 && p < pages) ? p : -1;
+}
+
+// Pages that `n` consecutive positions can touch.
+Q4_HD int64_t pages_touched(int64_t n, int64_t page) {
+  return n <= 0 ? 0 : (n - 1 + page - 1) / page + 1;
+}
+
+// Positions [lo, hi) that any of the queries at pos_min .. pos_max sees.
+struct KeyRange {
+  int64_t lo, hi;
+};
+
+Q4_HD KeyRange key_range(int64_t pos_min, int64_t pos_max, int64_t window, int64_t max_len) {
+  KeyRange r;
+  r.hi = pos_max + 1 < max_len ? pos_max + 1 : max_len;
+  if (r.hi < 0) r.hi = 0;
+  r.lo = window > 0 ? pos_min - window + 1 : 0;
+  if (r.lo < 0) r.lo = 0;
+  if (r.lo > r.hi) r.lo = r.hi;
+  return r;
+}
+
+}  // namespace q4
