@@ -75,7 +75,7 @@ __device__ __forceinline__ float join_digits(const int32_t (&a)[ND]) {
   return low;
 }
 
-// The maximum over the four lanes that hold a column.
+// Over the four lanes that hold a column.
 __device__ __forceinline__ float column_max(float x) {
   x = fmaxf(x, __shfl_xor(x, 16, 64));
   return fmaxf(x, __shfl_xor(x, 32, 64));
@@ -127,15 +127,228 @@ __device__ __forceinline__ Block block_of(const AttnParams& p, uint32_t id) {
 }
 
 // Where the 16 tokens at token0 (a multiple of 16) of the sequence lie: their
-// page, and whether they are to be read at all.  page < 0: not in the cache.
+// page, -1 if it is not in the cache, -2 if no query sees them.
 __device__ __forceinline__ int32_t segment_page(const AttnParams& p, const int32_t* row,
                                                 const KeyRange& keys, int64_t token0) {
-  if (token0 + 16 <= keys.lo || token0 >= keys.hi) return -2;  // not seen
+  if (token0 + 16 <= keys.lo || token0 >= keys.hi) return -2;
   return page_at(row, p.c.max_pages, p.c.pages, token0 >> p.c.page_log2);
 }
 
+// Elements d0 .. d0 + 15 of a query row as fp32, 16 bytes at a time where the
+// rows allow it.
+__device__ __forceinline__ void load_row16(const AttnParams& p, int64_t at, float (&x)[16]) {
+  if (p.q_vec && p.dtype == Q4_DTYPE_F32) {
+    const f32x4* s = (const f32x4*)((const float*)p.q + at);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const f32x4 v = s[i];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[4 * i + e] = v[e];
+    }
+  } else if (p.q_vec) {
+    const u32x4v* s = (const u32x4v*)((const uint16_t*)p.q + at);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const u32x4v v = s[i];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint16_t b = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
+        x[8 * i + e] = p.dtype == Q4_DTYPE_F16 ? (float)__builtin_bit_cast(_Float16, b)
+                                               : bits_f32((uint32_t)b << 16);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 16; ++e) x[e] = load_elem(p.q, at + e, p.dtype);
+  }
+}
+
+// A query row's digits, elements 64 s + 16 g .. + 15 in the lane (zero past
+// the head and for rows that do not exist), and the factor that takes a
+// digit product to a score in log2 units, >= 0: a negative softmax scale goes
+// into the digits, so that the largest product is the largest score.  A row
+// with NaN or infinity gets a NaN factor.
+template <int NS, int ND>
+__device__ __forceinline__ float row_digits(const AttnParams& p, int64_t at, bool valid, int g,
+                                            i32x4 (&qd)[NS][ND]) {
+  const int dim = p.c.dim;
+  uint32_t amax = 0;
+  float x[NS][16];
+#pragma unroll
+  for (int s = 0; s < NS; ++s) {
+    const int d = 64 * s + 16 * g;
+    if (valid && d < dim) {
+      load_row16(p, at + d, x[s]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) x[s][e] = 0.0f;
+    }
+#pragma unroll
+    for (int e = 0; e < 16; ++e) amax = umax(amax, abs_bits(x[s][e]));
+  }
+  amax = column_umax(amax);
+  // the power of two that takes the largest element below digit_max
+  const float a = bits_f32(amax);
+  const int ex = __builtin_amdgcn_frexp_expf(a);  // a = m 2^ex, m in [1/2, 1)
+  const float m = __builtin_amdgcn_frexp_mantf(a);
+  const int up = amax == 0 ? 0 : (ND == 3 ? 23 : 15) - ex - (m > 127.0f / 128.0f ? 1 : 0);
+  const float sign = p.scale_log2 < 0.0f ? -1.0f : 1.0f;
+#pragma unroll
+  for (int s = 0; s < NS; ++s)
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      uint32_t bits[4], out[ND];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        bits[e] = (uint32_t)(int)__builtin_rintf(
+                      __builtin_amdgcn_ldexpf(sign * x[s][4 * w + e], up)) +
+                  digit_bias<ND>();
+      pack_digits<ND>(bits[0], bits[1], bits[2], bits[3], out);
+#pragma unroll
+      for (int i = 0; i < ND; ++i) qd[s][i][w] = (int32_t)out[i];
+    }
+  return amax >= 0x7f800000u ? bits_f32(0x7fc00000u)
+                             : __builtin_amdgcn_ldexpf(__builtin_fabsf(p.scale_log2), -up);
+}
+
+// Running state of a column (query row): maximum in log2 units, the lane's
+// part of the sum, the lane's part of the outputs (4 of every 16 elements).
+template <int DT>
+struct Column {
+  float mx, sum;
+  float o[DT][4];
+};
+
+template <int DT>
+__device__ __forceinline__ void column_init(Column<DT>& c) {
+  c.mx = -__builtin_inff();
+  c.sum = 0.0f;
+#pragma unroll
+  for (int t = 0; t < DT; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c.o[t][i] = 0.0f;
+}
+
+// Scores of one 64-token tile, as digit products: sc[a][i] is token
+// 16 g + 4 a + i of the tile.
+template <int NS, int ND>
+__device__ __forceinline__ void tile_scores(const i32x4 (&kd)[4][NS], const i32x4 (&qd)[NS][ND],
+                                            float (&sc)[4][4]) {
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    i32x4 acc[ND];
+#pragma unroll
+    for (int i = 0; i < ND; ++i) {
+      acc[i] = i32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+        acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(kd[a][s], qd[s][i], acc[i], 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      int32_t part[ND];
+#pragma unroll
+      for (int n = 0; n < ND; ++n) part[n] = acc[n][i];
+      sc[a][i] = join_digits<ND>(part);
+    }
+  }
+}
+
+// Scores to probability digits.  unit: score per digit product (>= 0, or
+// NaN); lo, hi: first and last of the tile's tokens that the row sees,
+// relative to the lane's first (MASK only); vs: the values' scale.  Updates
+// maximum and sum; alpha is what the outputs so far are multiplied by, w what
+// the tile's digit products are worth.
+// UNIFORM: one page covers the tile.  Else its pages' scales join the
+// probabilities before these become digits.
+template <int ND, bool MASK, bool UNIFORM>
+__device__ __forceinline__ void tile_softmax(float (&sc)[4][4], float unit, float vs, int lo, int hi,
+                                             float& mx, float& sum, i32x4 (&pd)[ND], float& alpha,
+                                             float& w) {
+  const float inf = __builtin_inff();
+  float top = -inf;
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = 4 * a + i;
+      sc[a][i] *= unit;
+      if (MASK) sc[a][i] = j >= lo && j <= hi ? sc[a][i] : -inf;
+      top = fmaxf(top, sc[a][i]);
+    }
+  top = column_max(top);
+  const bool any = top > -inf;  // not: nothing seen, or NaN scores only
+  const float ref = any ? top : 0.0f;
+  float part = 0.0f, big = 1.0f;
+#pragma unroll
+  for (int a = 0; a < 4; ++a)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      sc[a][i] = exp2_fast(sc[a][i] - ref);  // 0 where not seen
+      part += sc[a][i];
+    }
+  uint32_t wmax = 0;
+  if (!UNIFORM) {
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = 4 * a + i;
+        sc[a][i] = !MASK || (j >= lo && j <= hi) ? sc[a][i] * vs : 0.0f;
+        wmax = umax(wmax, abs_bits(sc[a][i]));
+      }
+    wmax = column_umax(wmax);
+    big = fmaxf(bits_f32(wmax), 1e-30f);  // below it, digits run out
+  }
+  const float to_digits = UNIFORM ? digit_max<ND>() : digit_max<ND>() / big;
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    uint32_t bits[4], out[ND];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      bits[i] = f32_bits(__builtin_fmaf(sc[a][i], to_digits, 8388608.0f + (float)digit_bias<ND>()));
+    pack_digits<ND>(bits[0], bits[1], bits[2], bits[3], out);
+#pragma unroll
+    for (int i = 0; i < ND; ++i) pd[i][a] = (int32_t)out[i];
+  }
+  const float m_new = fmaxf(mx, top);
+  const float m_ref = m_new > -inf ? m_new : 0.0f;
+  alpha = exp2_fast(mx - m_ref);  // 0 before the first tile with a maximum
+  const float beta = any ? exp2_fast(top - m_ref) : 0.0f;
+  mx = m_new;
+  // a tile of NaN scores has no maximum: its sum, NaN, still has to show
+  sum = sum * alpha + (any || part == part ? beta * part : part);
+  // a scale that is not finite reaches the rows that see it, and no others
+  const float worth = UNIFORM ? vs : wmax >= 0x7f800000u ? bits_f32(wmax) : big;
+  w = any ? beta * worth * (1.0f / digit_max<ND>()) : 0.0f;
+}
+
+// Adds a tile's values: o = o alpha + w (V^T digits).
 template <int DT, int ND>
-__global__ __launch_bounds__(kThreads) void attention_kernel(AttnParams p) {
+__device__ __forceinline__ void tile_values(const i32x4 (&vd)[DT], const i32x4 (&pd)[ND],
+                                            float alpha, float w, float (&o)[DT][4]) {
+#pragma unroll
+  for (int dt = 0; dt < DT; ++dt) {
+    i32x4 acc[ND];
+#pragma unroll
+    for (int i = 0; i < ND; ++i)
+      acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(vd[dt], pd[i], i32x4{0, 0, 0, 0}, 0, 0, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      int32_t part[ND];
+#pragma unroll
+      for (int n = 0; n < ND; ++n) part[n] = acc[n][i];
+      o[dt][i] = __builtin_fmaf(join_digits<ND>(part), w, o[dt][i] * alpha);
+    }
+  }
+}
+
+// One workgroup: 16 query rows of one kv head, one split of their keys, the
+// tiles dealt to its four waves in turn.  The next tile's keys and page
+// numbers load while this one's scores become probabilities, its values
+// while its scores form; nothing but the final join passes through LDS.
+template <int DT, int ND, bool UNIFORM>
+__global__ __launch_bounds__(kThreads, DT <= 8 ? 2 : 1) void attention_kernel(AttnParams p) {
   constexpr int NS = (DT + 3) / 4;  // steps of 64 elements of a head
   extern __shared__ float lds[];
   const int split = blockIdx.x % p.splits;
@@ -144,230 +357,159 @@ __global__ __launch_bounds__(kThreads) void attention_kernel(AttnParams p) {
   // a block whose tiles fit one split writes its output itself
   const int n_splits = (k.tiles + p.split_tiles - 1) / p.split_tiles;
   if (split > 0 && split >= n_splits) return;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int col = lane & 15, g = lane >> 4;
   const KvCache& c = p.c;
   const int dim = c.dim, d16 = dim >> 4;
   const int32_t* table = c.table + (int64_t)k.b * c.table_ld;
+  const int page_mask = c.page - 1;
+  const float nan = bits_f32(0x7fc00000u);
 
-  // the lane's query row
+  const int t_end = (split + 1) * p.split_tiles < k.tiles ? (split + 1) * p.split_tiles : k.tiles;
+  int t = split * p.split_tiles + wave;
+  // page of the tile's keys that this lane loads, and of its 16 tokens
+  struct Pages {
+    int32_t key, own;
+  };
+  auto pages_of = [&](int tile) {
+    const int64_t token0 = (int64_t)(k.tile0 + tile) * kTile;
+    Pages r;
+    if (UNIFORM) {  // the tile has a token that is seen, and so its page has
+      r.own = r.key = page_at(table, c.max_pages, c.pages, token0 >> c.page_log2);
+    } else {
+      r.own = segment_page(p, table, k.keys, token0 + 16 * g);
+      r.key = segment_page(p, table, k.keys, token0 + 16 * (col >> 2));
+    }
+    return r;
+  };
+  i32x4 kd[4][NS];
+  float ks;
+  auto load_keys = [&](int tile, const Pages& pg) {
+    const int64_t token0 = (int64_t)(k.tile0 + tile) * kTile;
+    const int slot = (int)((token0 + 16 * (col >> 2) + (col & 3)) & page_mask);
+    // what is not seen, or not in the cache, is read from page 0: its scores
+    // are masked, or NaN by their scale
+    const int64_t page_row = ((int64_t)(pg.key > 0 ? pg.key : 0) * c.heads + k.h) << c.page_log2;
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+      for (int s = 0; s < NS; ++s) {
+        const int d = 64 * s + 16 * g;
+        kd[a][s] = *(const i32x4*)(c.k + (page_row + slot + 4 * a) * dim + (d < dim ? d : 0));
+      }
+    ks = pg.own >= 0 ? c.ks[(int64_t)pg.own * c.heads + k.h] : nan;
+  };
+  Pages pg{0, 0}, pg_next{0, 0};
+  if (t < t_end) {
+    pg = pages_of(t);
+    load_keys(t, pg);
+    if (t + kWaves < t_end) pg_next = pages_of(t + kWaves);
+  }
+
+  // the lane's query row and the positions it sees
   const int64_t r = k.row0 + col;
   const bool valid = r < k.rows;
   const int64_t tok = valid ? r / p.group : 0;
   const int head = k.h * p.group + (int)(valid ? r - tok * p.group : 0);
   const int64_t pos = valid ? k.sp.pos0 + tok : -1;
   const int64_t see_lo64 = p.window > 0 ? pos - p.window + 1 : 0;
-  const int32_t see_hi = (int32_t)(pos < k.keys.hi ? pos : k.keys.hi - 1);  // last position seen
-  const int32_t see_lo = (int32_t)(see_lo64 > 0 ? see_lo64 : 0);
+  const int64_t see_hi = pos < k.keys.hi ? pos : k.keys.hi - 1;  // last position seen
+  const int64_t see_lo = see_lo64 > 0 ? see_lo64 : 0;
+  // positions that every row of the block sees
+  const int64_t last_row = (k.row0 + kRows < k.rows ? k.row0 + kRows : k.rows) - 1;
+  const int64_t pos_first = k.sp.pos0 + k.row0 / p.group, pos_last = k.sp.pos0 + last_row / p.group;
+  const int64_t all_hi = pos_first < k.keys.hi ? pos_first : k.keys.hi - 1;
+  const int64_t all_lo = p.window > 0 ? pos_last - p.window + 1 : 0;
 
-  // its digits: elements 64 s + 16 g .. + 15 of the row, zero past the head
   i32x4 qd[NS][ND];
-  float q_unit;
-  {
-    const int64_t at = (k.sp.t0 + tok) * p.q_ts + (int64_t)head * p.q_hs;
-    uint32_t amax = 0;
-    float x[NS][16];
-#pragma unroll
-    for (int s = 0; s < NS; ++s)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int d = 64 * s + 16 * g + e;
-        x[s][e] = valid && d < dim ? load_elem(p.q, at + d, p.dtype) : 0.0f;
-        amax = umax(amax, abs_bits(x[s][e]));
-      }
-    amax = column_umax(amax);
-    // the power of two that takes the largest element below digit_max; a
-    // row with NaN or infinity gets a NaN unit, and so NaN scores
-    const float a = bits_f32(amax);
-    int ex = __builtin_amdgcn_frexp_expf(a);  // a = m 2^ex, m in [1/2, 1)
-    const float m = __builtin_amdgcn_frexp_mantf(a);
-    int up = (ND == 3 ? 23 : 15) - ex - (m > 127.0f / 128.0f ? 1 : 0);
-    if (amax == 0) up = 0;
-    q_unit = amax >= 0x7f800000u ? bits_f32(0x7fc00000u) : __builtin_amdgcn_ldexpf(p.scale_log2, -up);
-#pragma unroll
-    for (int s = 0; s < NS; ++s)
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        uint32_t bits[4], out[ND];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          bits[e] = (uint32_t)(int)__builtin_rintf(__builtin_amdgcn_ldexpf(x[s][4 * w + e], up)) +
-                    digit_bias<ND>();
-        pack_digits<ND>(bits[0], bits[1], bits[2], bits[3], out);
-#pragma unroll
-        for (int i = 0; i < ND; ++i) qd[s][i][w] = (int32_t)out[i];
-      }
-  }
+  const float q_unit = row_digits<NS, ND>(
+      p, (k.sp.t0 + tok) * p.q_ts + (int64_t)head * p.q_hs, valid, g, qd);
 
-  float o[DT][4];
-#pragma unroll
-  for (int t = 0; t < DT; ++t)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[t][i] = 0.0f;
-  float mx = -__builtin_inff(), sum = 0.0f;  // running maximum (log2), the lane's part of the sum
-
-  const int t_end = (split + 1) * p.split_tiles < k.tiles ? (split + 1) * p.split_tiles : k.tiles;
-  for (int t = split * p.split_tiles + wave; t < t_end; t += kWaves) {
+  Column<DT> st;
+  column_init(st);
+  for (; t < t_end; t += kWaves) {
     const int64_t token0 = (int64_t)(k.tile0 + t) * kTile;
-    // pages of the lane's key rows and of its 16 tokens
-    const int32_t pk = segment_page(p, table, k.keys, token0 + 16 * (col >> 2));
-    const int32_t pg = segment_page(p, table, k.keys, token0 + 16 * g);
-    const int page_mask = c.page - 1;
-    i32x4 kd[4][NS], vd[DT];
-    {
-      const int64_t page_row = ((int64_t)(pk > 0 ? pk : 0) * c.heads + k.h) << c.page_log2;
-      const int slot = (int)((token0 + 16 * (col >> 2) + (col & 3)) & page_mask);
-#pragma unroll
-      for (int a = 0; a < 4; ++a)
-#pragma unroll
-        for (int s = 0; s < NS; ++s) {
-          const int d = 64 * s + 16 * g;
-          kd[a][s] = *(const i32x4*)(c.k + (page_row + slot + 4 * a) * dim + (d < dim ? d : 0));
-        }
-    }
-    const int64_t ph = (int64_t)(pg > 0 ? pg : 0) * c.heads + k.h;
+    const int64_t ph = (int64_t)(pg.own > 0 ? pg.own : 0) * c.heads + k.h;
+    i32x4 vd[DT];
     {
       const int8_t* v = c.v + ph * ((int64_t)dim << c.page_log2) + ((token0 + 16 * g) & page_mask);
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt)
         vd[dt] = *(const i32x4*)(v + ((int64_t)((dt < d16 ? 16 * dt : 0) + col) << c.page_log2));
     }
-    const float nan = bits_f32(0x7fc00000u);
-    const float ks = pg >= 0 ? c.ks[ph] : nan, vs = pg >= 0 ? c.vs[ph] : nan;
-
-    // scores, in log2 units
+    const float vs = pg.own >= 0 ? c.vs[ph] : nan;
     float sc[4][4];
+    tile_scores<NS, ND>(kd, qd, sc);
     const float unit = q_unit * ks;
-    const int32_t tok0 = (int32_t)token0 + 16 * g;
-    float top = -__builtin_inff();
-#pragma unroll
-    for (int a = 0; a < 4; ++a) {
-      i32x4 acc[ND];
-#pragma unroll
-      for (int i = 0; i < ND; ++i) {
-        acc[i] = i32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int s = 0; s < NS; ++s)
-          acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(kd[a][s], qd[s][i], acc[i], 0, 0, 0);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        int32_t part[ND];
-#pragma unroll
-        for (int n = 0; n < ND; ++n) part[n] = acc[n][i];
-        const int32_t j = tok0 + 4 * a + i;
-        const bool seen = j >= see_lo && j <= see_hi;
-        sc[a][i] = seen ? join_digits<ND>(part) * unit : -__builtin_inff();
-        top = fmaxf(top, sc[a][i]);
-      }
+    if (t + kWaves < t_end) {
+      load_keys(t + kWaves, pg_next);
+      pg = pg_next;
+      if (t + 2 * kWaves < t_end) pg_next = pages_of(t + 2 * kWaves);
     }
-    top = column_max(top);
-    const bool any = top > -__builtin_inff();
-    const float ref = any ? top : 0.0f;
-
-    // probabilities against the tile's maximum; the values' scale joins them
-    // before they are made digits, as a tile may hold several pages
-    float part_sum = 0.0f;
-    uint32_t wmax = 0;
-    float pw[4][4];
-#pragma unroll
-    for (int a = 0; a < 4; ++a)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int32_t j = tok0 + 4 * a + i;
-        const bool seen = j >= see_lo && j <= see_hi;
-        const float e = exp2_fast(sc[a][i] - ref);  // 0 where not seen
-        part_sum += e;
-        pw[a][i] = seen ? e * vs : 0.0f;
-        wmax = umax(wmax, abs_bits(pw[a][i]));
-      }
-    wmax = column_umax(wmax);
-    const float big = fmaxf(bits_f32(wmax), 1e-30f);  // below it, digits run out
-    const float to_digits = digit_max<ND>() / big;
     i32x4 pd[ND];
-#pragma unroll
-    for (int a = 0; a < 4; ++a) {
-      uint32_t bits[4], out[ND];
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        bits[i] = f32_bits(__builtin_fmaf(pw[a][i], to_digits,
-                                          8388608.0f + (float)digit_bias<ND>()));
-      pack_digits<ND>(bits[0], bits[1], bits[2], bits[3], out);
-#pragma unroll
-      for (int i = 0; i < ND; ++i) pd[i][a] = (int32_t)out[i];
+    float alpha, w;
+    if (token0 >= all_lo && token0 + kTile - 1 <= all_hi) {
+      tile_softmax<ND, false, UNIFORM>(sc, unit, vs, 0, 0, st.mx, st.sum, pd, alpha, w);
+    } else {
+      const int64_t base = token0 + 16 * g;
+      const int lo = (int)(see_lo - base > 16 ? 16 : see_lo - base < 0 ? 0 : see_lo - base);
+      const int hi = (int)(see_hi - base < -1 ? -1 : see_hi - base > 15 ? 15 : see_hi - base);
+      tile_softmax<ND, true, UNIFORM>(sc, unit, vs, lo, hi, st.mx, st.sum, pd, alpha, w);
     }
-
-    const float m_new = fmaxf(mx, top);
-    const float m_ref = m_new > -__builtin_inff() ? m_new : 0.0f;
-    const float alpha = exp2_fast(mx - m_ref);           // 0 before the first seen tile
-    const float beta = any ? exp2_fast(top - m_ref) : 0.0f;
-    mx = m_new;
-    // a tile of NaN scores has no maximum: its sum, NaN, still has to show
-    sum = sum * alpha + (any ? beta * part_sum : (part_sum != part_sum ? part_sum : 0.0f));
-    // wmax as bits: NaN and infinity of a page's scale reach the outputs
-    const float w = any ? beta * (wmax >= 0x7f800000u ? bits_f32(wmax) : big) / digit_max<ND>() : 0.0f;
-#pragma unroll
-    for (int dt = 0; dt < DT; ++dt) {
-      i32x4 acc[ND];
-#pragma unroll
-      for (int i = 0; i < ND; ++i)
-        acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(vd[dt], pd[i], i32x4{0, 0, 0, 0}, 0, 0, 0);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        int32_t part[ND];
-#pragma unroll
-        for (int n = 0; n < ND; ++n) part[n] = acc[n][i];
-        o[dt][i] = __builtin_fmaf(join_digits<ND>(part), w, o[dt][i] * alpha);
-      }
-    }
+    tile_values<DT, ND>(vd, pd, alpha, w, st.o);
   }
 
   // join the waves' parts: [wave][row][dim] outputs, then maxima and sums
-  sum = column_sum(sum);
-  const int pitch = 16 * DT + 4;
+  const float sum = column_sum(st.sum);
+  constexpr int pitch = 16 * DT + 4;
   float* lo = lds;
   float* lm = lds + kWaves * kRows * pitch;
   float* ls = lm + kWaves * kRows;
 #pragma unroll
   for (int dt = 0; dt < DT; ++dt)
     *(f32x4*)&lo[(wave * kRows + col) * pitch + 16 * dt + 4 * g] =
-        f32x4{o[dt][0], o[dt][1], o[dt][2], o[dt][3]};
+        f32x4{st.o[dt][0], st.o[dt][1], st.o[dt][2], st.o[dt][3]};
   if (g == 0) {
-    lm[wave * kRows + col] = mx;
+    lm[wave * kRows + col] = st.mx;
     ls[wave * kRows + col] = sum;
   }
   __syncthreads();
-  const bool last = n_splits <= 1;
-  for (int i = threadIdx.x; i < kRows * dim; i += kThreads) {
-    const int row = i / dim, d = i - row * dim;
-    const int64_t rr = k.row0 + row;
-    if (rr >= k.rows) break;
-    float m = lm[row];
+  // 16 threads a row, 4 elements a step
+  const int row = threadIdx.x >> 4, sub = threadIdx.x & 15;
+  const int64_t rr = k.row0 + row;
+  if (rr >= k.rows) return;
+  float m = lm[row];
 #pragma unroll
-    for (int w = 1; w < kWaves; ++w) m = fmaxf(m, lm[w * kRows + row]);
-    const float ref = m > -__builtin_inff() ? m : 0.0f;
-    float acc = 0.0f, den = 0.0f;
+  for (int i = 1; i < kWaves; ++i) m = fmaxf(m, lm[i * kRows + row]);
+  const float ref = m > -__builtin_inff() ? m : 0.0f;
+  float f[kWaves], den = 0.0f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-      const float f = exp2_fast(lm[w * kRows + row] - ref);
-      // a wave without a maximum has a sum of 0, or NaN, which has to show
-      const float sw = ls[w * kRows + row];
-      den += sw != sw ? sw : f * sw;
-      acc += f * lo[(w * kRows + row) * pitch + d];
-    }
-    const int64_t tk = rr / p.group;
-    const int64_t tq = k.sp.t0 + tk, hq = k.h * p.group + (rr - tk * p.group);
-    if (last) {
-      const float v = den == 0.0f ? 0.0f : acc / den;  // no key seen: 0
-      store_elem(p.out, tq * p.o_ts + hq * p.o_hs + d, v, p.dtype);
+  for (int i = 0; i < kWaves; ++i) {
+    f[i] = exp2_fast(lm[i * kRows + row] - ref);
+    // a wave without a maximum has a sum of 0, or NaN, which has to show
+    const float si = ls[i * kRows + row];
+    den += si != si ? si : f[i] * si;
+  }
+  const int64_t tk = rr / p.group;
+  const int64_t tq = k.sp.t0 + tk, hq = k.h * p.group + (rr - tk * p.group);
+  const int64_t at = (int64_t)split * p.T * p.heads + tq * p.heads + hq;
+  const float inv = den == 0.0f ? 0.0f : 1.0f / den;  // no key seen: 0
+  for (int d = 4 * sub; d < dim; d += 64) {
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < kWaves; ++i)
+      acc += f[i] * *(const f32x4*)&lo[(i * kRows + row) * pitch + d];
+    if (n_splits <= 1) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        store_elem(p.out, tq * p.o_ts + hq * p.o_hs + d + e, acc[e] * inv, p.dtype);
     } else {
-      const int64_t at = (int64_t)split * p.T * p.heads + tq * p.heads + hq;
-      p.part_o[at * dim + d] = acc;
-      if (d == 0) {
-        p.part_ml[2 * at] = m;
-        p.part_ml[2 * at + 1] = den;
-      }
+      *(f32x4*)&p.part_o[at * dim + d] = acc;
     }
+  }
+  if (n_splits > 1 && sub == 0) {
+    p.part_ml[2 * at] = m;
+    p.part_ml[2 * at + 1] = den;
   }
 }
 

@@ -6,19 +6,25 @@
 
 namespace q4 {
 
-template <int DT, int ND>
-static hipError_t launch_attention_dim(const AttnParams& p, hipStream_t s) {
+template <int DT, int ND, bool UNIFORM>
+static hipError_t launch_attention_pages(const AttnParams& p, hipStream_t s) {
   using namespace attn;
   const size_t lds = (size_t)(kWaves * kRows * (16 * DT + 4) + 2 * kWaves * kRows) * sizeof(float);
   if (lds > 65536) {
     const hipError_t e =
-        hipFuncSetAttribute((const void*)attention_kernel<DT, ND>,
+        hipFuncSetAttribute((const void*)attention_kernel<DT, ND, UNIFORM>,
                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
   }
   const dim3 grid((unsigned)((int64_t)p.batch * p.c.heads * p.row_blocks * p.splits));
-  hipLaunchKernelGGL((attention_kernel<DT, ND>), grid, dim3(kThreads), lds, s, p);
+  hipLaunchKernelGGL((attention_kernel<DT, ND, UNIFORM>), grid, dim3(kThreads), lds, s, p);
   return hipGetLastError();
+}
+
+template <int DT, int ND>
+static hipError_t launch_attention_dim(const AttnParams& p, hipStream_t s) {
+  return p.c.page >= attn::kTile ? launch_attention_pages<DT, ND, true>(p, s)
+                                 : launch_attention_pages<DT, ND, false>(p, s);
 }
 
 // The kernel holds a head in 16-wide tiles; head sizes between the instances

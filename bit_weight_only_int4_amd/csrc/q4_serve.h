@@ -51,6 +51,8 @@ struct AttnParams {
   int32_t dtype, batch, heads, group;  // group = heads / kv heads
   int64_t max_len, window;
   float scale_log2;             // scale * log2(e)
+  int32_t q_vec;                // 16-byte aligned query rows
+  int32_t max_rows;             // per sequence and kv head
   int32_t row_blocks;           // per sequence and kv head
   int32_t splits;               // workgroups along the keys (grid)
   int32_t split_tiles;          // tiles of 64 keys each of them takes
@@ -59,7 +61,7 @@ struct AttnParams {
 };
 
 struct AttnPlan {
-  int32_t row_blocks, splits, split_tiles;
+  int32_t max_rows, row_blocks, splits, split_tiles;
   size_t workspace;
 };
 AttnPlan plan_attention(int32_t dtype, int64_t T, int64_t batch, int64_t heads, int64_t kv_heads,

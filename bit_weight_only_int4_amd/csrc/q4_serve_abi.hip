@@ -251,7 +251,8 @@ q4_status q4_attention(const void* q, int64_t q_ts, int64_t q_hs, void* out, int
   max_new = rows_bound(max_new, T);
   const q4::AttnPlan pl = q4::plan_attention(dtype, T, batch, heads, kv_heads, head_dim, page,
                                              max_new, max_len, window);
-  if (!grid_ok((double)batch * (double)kv_heads * (double)pl.row_blocks * (double)pl.splits))
+  if (!grid_ok((double)batch * (double)kv_heads * (double)pl.row_blocks * (double)pl.splits) ||
+      !grid_ok((double)batch * (double)heads * (double)max_new))
     return Q4_ERR_INVALID_ARG;
 
   const int64_t cache_n = pages * kv_heads * page * head_dim;
@@ -285,6 +286,8 @@ q4_status q4_attention(const void* q, int64_t q_ts, int64_t q_hs, void* out, int
   p.max_len = max_len;
   p.window = window;
   p.scale_log2 = scale * 1.4426950408889634f;
+  p.q_vec = aligned(q, 16) && q_ts * e % 16 == 0 && q_hs * e % 16 == 0;
+  p.max_rows = pl.max_rows;
   p.row_blocks = pl.row_blocks;
   p.splits = pl.splits;
   p.split_tiles = pl.split_tiles;
