@@ -5,49 +5,96 @@ namespace q4 {
 
 namespace attn {
 
-// Joins the splits of one query row: the weights of its parts first, a lane
-// each, then their outputs, a wave every fourth part.
-__global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnParams p, int32_t max_rows) {
-  __shared__ float acc_s[kWaves][256];
-  __shared__ float den_s[kWaves];
-  // rows of a sequence and kv head are consecutive
-  const int64_t rr = blockIdx.x % max_rows;
-  const uint32_t bh = blockIdx.x / max_rows;
-  const Block k = block_of(p, bh * p.row_blocks + (uint32_t)(rr / kRows));
+// Adds the parts of one query row, n of them, part s at rows at + s * stride of
+// part_o and part_ml, and writes the output.  The parts' weights come first,
+// a thread each, so that their outputs then load without waiting for one
+// another: 4 elements a thread, dim / 4 threads a part, four parts a step.
+__device__ __forceinline__ void join_row(const AttnParams& p, int n, int64_t at, int64_t stride,
+                                         int64_t out, int32_t max_parts) {
+  extern __shared__ float lds[];  // weights [max_parts], then [parts at once][dim]
+  __shared__ float red[2 * kWaves];
+  const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, dim = p.c.dim;
+  float* weight = lds;
+  float m = -__builtin_inff();
+  for (int s = tid; s < n; s += kThreads) m = fmaxf(m, p.part_ml[2 * (at + s * stride)]);
+#pragma unroll
+  for (int i = 32; i >= 1; i >>= 1) m = fmaxf(m, __shfl_xor(m, i, 64));
+  if (lane == 0) red[wave] = m;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) m = fmaxf(m, red[w]);
+  const float ref = m > -__builtin_inff() ? m : 0.0f;
+  float den = 0.0f;
+  for (int s = tid; s < n; s += kThreads) {
+    const int64_t a = at + s * stride;
+    const float f = exp2_fast(p.part_ml[2 * a] - ref), d = p.part_ml[2 * a + 1];
+    weight[s] = f;
+    den += d != d ? d : f * d;  // a part without a maximum: 0, or NaN
+  }
+#pragma unroll
+  for (int i = 32; i >= 1; i >>= 1) den += __shfl_xor(den, i, 64);
+  if (lane == 0) red[kWaves + wave] = den;
+  __syncthreads();
+  const int quads = dim >> 2, at_once = kThreads / quads;
+  const int part = tid / quads, d = 4 * (tid - part * quads);
+  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (part < at_once) {
+    const float* src = p.part_o + at * dim + d;
+    int s = part;
+    for (; s + 3 * at_once < n; s += 4 * at_once) {
+      f32x4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = *(const f32x4*)(src + (s + i * at_once) * stride * dim);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc += weight[s + i * at_once] * v[i];
+    }
+    for (; s < n; s += at_once) acc += weight[s] * *(const f32x4*)(src + s * stride * dim);
+    float* o = lds + max_parts + part * dim + d;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o[e] = acc[e];
+  }
+  __syncthreads();
+  if (tid >= dim) return;
+  float o = 0.0f, total = 0.0f;
+  for (int i = 0; i < at_once; ++i) o += lds[max_parts + i * dim + tid];
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) total += red[kWaves + w];
+  store_elem(p.out, out + tid, total == 0.0f ? 0.0f : o / total, p.dtype);
+}
+
+// One query row of the blocks that have more than one split.
+__global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnParams p) {
+  const int64_t rr = blockIdx.x % p.max_rows;
+  const uint32_t bh = blockIdx.x / p.max_rows;
+  const Block k = block_of(p, bh / p.c.heads, bh % p.c.heads, (int)(rr / kRows));
   if (rr >= k.rows) return;
   const int n = (k.tiles + p.split_tiles - 1) / p.split_tiles;
   if (n <= 1) return;
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, dim = p.c.dim;
   const int64_t tk = rr / p.group;
   const int64_t tq = k.sp.t0 + tk, hq = k.h * p.group + (rr - tk * p.group);
-  const int64_t stride = p.T * p.heads, at = tq * p.heads + hq;
-  float m = -__builtin_inff();
-  for (int s = lane; s < n; s += 64) m = fmaxf(m, p.part_ml[2 * (at + s * stride)]);
-#pragma unroll
-  for (int i = 32; i >= 1; i >>= 1) m = fmaxf(m, __shfl_xor(m, i, 64));
-  const float ref = m > -__builtin_inff() ? m : 0.0f;
-  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f}, den = 0.0f;
-  for (int s = wave; s < n; s += kWaves) {
-    const int64_t a = at + s * stride;
-    const float f = exp2_fast(p.part_ml[2 * a] - ref), d = p.part_ml[2 * a + 1];
-    den += d != d ? d : f * d;  // a part without a maximum: 0, or NaN
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (lane + 64 * i < dim) acc[i] += f * p.part_o[a * dim + lane + 64 * i];
+  join_row(p, n, tq * p.heads + hq, p.T * p.heads, tq * p.o_ts + hq * p.o_hs, p.splits);
+}
+
+// One query row of the units whose tiles several waves had; zeros for those
+// without a tile.
+__global__ __launch_bounds__(kThreads) void attention_stream_join_kernel(AttnParams p) {
+  const int64_t rr = blockIdx.x % p.max_rows;
+  const uint32_t bh = blockIdx.x / p.max_rows;
+  const int b = bh / p.c.heads, h = bh % p.c.heads, rb = (int)(rr / kRows);
+  const Block k = block_of(p, b, h, rb);
+  if (rr >= k.rows) return;
+  const int64_t tk = rr / p.group;
+  const int64_t tq = k.sp.t0 + tk, hq = k.h * p.group + (rr - tk * p.group);
+  const int64_t out = tq * p.o_ts + hq * p.o_hs;
+  if (k.tiles == 0) {
+    if ((int)threadIdx.x < p.c.dim) store_elem(p.out, out + threadIdx.x, 0.0f, p.dtype);
+    return;
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) acc_s[wave][lane + 64 * i] = acc[i];
-  if (lane == 0) den_s[wave] = den;
-  __syncthreads();
-  const int d = threadIdx.x;
-  if (d >= dim) return;
-  float o = 0.0f, total = 0.0f;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    o += acc_s[w][d];
-    total += den_s[w];
-  }
-  store_elem(p.out, tq * p.o_ts + hq * p.o_hs + d, total == 0.0f ? 0.0f : o / total, p.dtype);
+  const int unit = (h * p.batch + b) * p.row_blocks + rb;
+  const int32_t piece = p.stream_info[0], start = p.stream_info[1 + unit];
+  const int32_t first = start / piece, n = (start + k.tiles - 1) / piece - first + 1;
+  if (n <= 1) return;
+  join_row(p, n, ((int64_t)first + unit) * kRows + (rr - k.row0), kRows, out, p.stream_waves);
 }
 
 }  // namespace attn
@@ -58,44 +105,65 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
-// The keys of a row block go to several workgroups, for two reasons: row
-// blocks alone may leave CUs without work, and sequences differ in length,
-// so that the longest would run alone at the end.  A split of kMinTiles tiles
-// already costs little beside them (its part of the output is 1 / 32 of the
-// keys it reads at 4 rows of 128).  max_len and the window bound the tiles:
+// Which kernel, and how much of it.
+//
+// Rows of many keys run the stream kernel, whose waves share all keys evenly:
+// where a unit has at least kStreamTiles tiles by max_len, units are few enough
+// for their running sum in LDS, and the line's length fits 32 bits.  Below,
+// one workgroup per unit needs no second launch.
+//
+// Otherwise the keys of a row block go to several workgroups while row blocks
+// alone leave CUs without work.  max_len and the window bound the tiles:
 // neither the grid nor the workspace depends on device-side lengths.
 AttnPlan plan_attention(int32_t dtype, int64_t T, int64_t batch, int64_t heads, int64_t kv_heads,
                         int64_t dim, int64_t page, int64_t max_new, int64_t max_len,
                         int64_t window) {
   (void)dtype;
   (void)page;
-  constexpr int64_t kTargetBlocks = 4096, kMinTiles = 16;
-  AttnPlan pl;
+  constexpr int64_t kTargetBlocks = 1024, kMinTiles = 16, kStreamTiles = 32;
+  constexpr int64_t kStreamUnits = 8192, kStreamWaves = 2048;
+  AttnPlan pl{};
   const int64_t group = heads / kv_heads;
   pl.max_rows = (int32_t)(max_new * group);
   pl.row_blocks = (int32_t)ceil_div(max_new * group, attn::kRows);
   // a block's queries span at most kRows positions
   int64_t span = max_len;
   if (window > 0 && window + attn::kRows < span) span = window + attn::kRows;
-  const int64_t tiles = ceil_div(span, attn::kTile) + (window > 0 ? 1 : 0);
-  const int64_t blocks = batch * kv_heads * pl.row_blocks;
+  int64_t tiles = ceil_div(span, attn::kTile) + (window > 0 ? 1 : 0);
+  if (tiles < 1) tiles = 1;
+  const int64_t units = batch * pl.row_blocks, blocks = units * kv_heads;
+  pl.splits = 1;
+  pl.split_tiles = (int32_t)tiles;
+  if (tiles >= kStreamTiles && pl.row_blocks <= 2 && units <= kStreamUnits &&
+      (double)tiles * (double)blocks < 1073741824.0) {
+    int64_t waves = ceil_div(tiles * blocks, attn::kMinPiece);
+    if (waves > kStreamWaves) waves = kStreamWaves;
+    pl.stream_waves = (int32_t)(ceil_div(waves, attn::kWaves) * attn::kWaves);
+    pl.parts = (size_t)(pl.stream_waves + blocks) * attn::kRows;
+    pl.workspace = pl.parts * (size_t)(dim + 2) * sizeof(float) + (size_t)(1 + blocks) * sizeof(int32_t);
+    return pl;
+  }
   int64_t splits = ceil_div(kTargetBlocks, blocks > 0 ? blocks : 1);
   if (splits > tiles / kMinTiles) splits = tiles / kMinTiles;
   if (splits < 1) splits = 1;
-  pl.split_tiles = (int32_t)ceil_div(tiles > 0 ? tiles : 1, splits);
-  pl.splits = (int32_t)ceil_div(tiles > 0 ? tiles : 1, pl.split_tiles);
-  pl.workspace = pl.splits > 1
-                     ? (size_t)pl.splits * (size_t)(T * heads) * (size_t)(dim + 2) * sizeof(float)
-                     : 0;
+  pl.split_tiles = (int32_t)ceil_div(tiles, splits);
+  pl.splits = (int32_t)ceil_div(tiles, pl.split_tiles);
+  pl.parts = pl.splits > 1 ? (size_t)pl.splits * (size_t)(T * heads) : 0;
+  pl.workspace = pl.parts * (size_t)(dim + 2) * sizeof(float);
   return pl;
 }
 
 hipError_t launch_attention(const AttnParams& p, hipStream_t s) {
   const hipError_t e = p.dtype == Q4_DTYPE_F32 ? launch_attention_digits<3>(p, s)
                                                : launch_attention_digits<2>(p, s);
-  if (e != hipSuccess || p.splits <= 1) return e;
+  if (e != hipSuccess || (p.splits <= 1 && !p.stream_waves)) return e;
   const dim3 grid((unsigned)((int64_t)p.batch * p.c.heads * p.max_rows));
-  hipLaunchKernelGGL(attn::attention_join_kernel, grid, dim3(attn::kThreads), 0, s, p, p.max_rows);
+  const int32_t most = p.stream_waves ? p.stream_waves : p.splits;
+  const size_t lds = (most + (size_t)(attn::kThreads / (p.c.dim / 4)) * p.c.dim) * sizeof(float);
+  if (p.stream_waves)
+    hipLaunchKernelGGL(attn::attention_stream_join_kernel, grid, dim3(attn::kThreads), lds, s, p);
+  else
+    hipLaunchKernelGGL(attn::attention_join_kernel, grid, dim3(attn::kThreads), lds, s, p);
   return hipGetLastError();
 }
 

@@ -37,6 +37,7 @@ constexpr int kTile = 64;   // tokens per step of a wave
 constexpr int kWaves = 4;   // waves of a workgroup, each over its own tiles
 constexpr int kRows = 16;   // query rows of a workgroup
 constexpr int kThreads = 64 * kWaves;
+constexpr int kMinPiece = 2;  // tiles of a wave in attention_stream_kernel
 
 // largest integer that ND digits hold with the offsets of pack_digits
 template <int ND>
@@ -109,12 +110,10 @@ struct Block {
   KeyRange keys;
 };
 
-__device__ __forceinline__ Block block_of(const AttnParams& p, uint32_t id) {
+__device__ __forceinline__ Block block_of(const AttnParams& p, int b, int h, int rb) {
   Block k;
-  const int rb = id % p.row_blocks;
-  id /= p.row_blocks;
-  k.h = id % p.c.heads;
-  k.b = id / p.c.heads;
+  k.h = h;
+  k.b = b;
   k.sp = seq_span(p.c.cu_new, p.c.lengths, k.b, p.T);
   k.rows = (int64_t)k.sp.n * p.group;
   k.row0 = (int64_t)rb * kRows;
@@ -124,6 +123,12 @@ __device__ __forceinline__ Block block_of(const AttnParams& p, uint32_t id) {
   k.tile0 = (int)(k.keys.lo / kTile);
   k.tiles = k.keys.hi > k.keys.lo ? (int)((k.keys.hi + kTile - 1) / kTile) - k.tile0 : 0;
   return k;
+}
+
+// Tiles of one wave's piece of a line of `total`, dealt to `waves` of them.
+__device__ __forceinline__ int32_t stream_piece(int32_t total, int32_t waves) {
+  const int32_t piece = (total + waves - 1) / waves;
+  return piece > kMinPiece ? piece : kMinPiece;
 }
 
 // Where the 16 tokens at token0 (a multiple of 16) of the sequence lie: their
@@ -343,30 +348,29 @@ __device__ __forceinline__ void tile_values(const i32x4 (&vd)[DT], const i32x4 (
   }
 }
 
-// One workgroup: 16 query rows of one kv head, one split of their keys, the
-// tiles dealt to its four waves in turn.  The next tile's keys and page
-// numbers load while this one's scores become probabilities, its values
-// while its scores form; nothing but the final join passes through LDS.
+// A tile's operands: keys, values, the lane's scales and page.
+template <int NS, int DT>
+struct Tile {
+  i32x4 kd[4][NS], vd[DT];
+  float ks, vs;
+};
+
+// A wave's tiles t, t + step, ... below t_end of a block's keys, into the
+// lane's column state.  The next tile's keys and page numbers load while this
+// one's scores become probabilities, its values while its scores form.  Two or
+// three waves share a SIMD.  One wave per SIMD with whole tiles in two register
+// buffers took 93 us where this takes 84 (64 sequences of 500 to 8000 tokens,
+// 8 kv heads of 128).
 template <int DT, int ND, bool UNIFORM>
-__global__ __launch_bounds__(kThreads, DT <= 8 ? 2 : 1) void attention_kernel(AttnParams p) {
+__device__ __forceinline__ void attend(const AttnParams& p, const Block& k, int t, int t_end,
+                                       int step, Column<DT>& st) {
   constexpr int NS = (DT + 3) / 4;  // steps of 64 elements of a head
-  extern __shared__ float lds[];
-  const int split = blockIdx.x % p.splits;
-  const Block k = block_of(p, blockIdx.x / p.splits);
-  if (k.row0 >= k.rows) return;
-  // a block whose tiles fit one split writes its output itself
-  const int n_splits = (k.tiles + p.split_tiles - 1) / p.split_tiles;
-  if (split > 0 && split >= n_splits) return;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int col = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
   const KvCache& c = p.c;
   const int dim = c.dim, d16 = dim >> 4;
   const int32_t* table = c.table + (int64_t)k.b * c.table_ld;
   const int page_mask = c.page - 1;
   const float nan = bits_f32(0x7fc00000u);
-
-  const int t_end = (split + 1) * p.split_tiles < k.tiles ? (split + 1) * p.split_tiles : k.tiles;
-  int t = split * p.split_tiles + wave;
   // page of the tile's keys that this lane loads, and of its 16 tokens
   struct Pages {
     int32_t key, own;
@@ -375,36 +379,53 @@ __global__ __launch_bounds__(kThreads, DT <= 8 ? 2 : 1) void attention_kernel(At
     const int64_t token0 = (int64_t)(k.tile0 + tile) * kTile;
     Pages r;
     if (UNIFORM) {  // the tile has a token that is seen, and so its page has
-      r.own = r.key = page_at(table, c.max_pages, c.pages, token0 >> c.page_log2);
+      r.own = r.key = __builtin_amdgcn_readfirstlane(
+          page_at(table, c.max_pages, c.pages, token0 >> c.page_log2));
     } else {
       r.own = segment_page(p, table, k.keys, token0 + 16 * g);
       r.key = segment_page(p, table, k.keys, token0 + 16 * (col >> 2));
     }
     return r;
   };
-  i32x4 kd[4][NS];
-  float ks;
-  auto load_keys = [&](int tile, const Pages& pg) {
+  // Addresses are a 64-bit base of the page, of the wave where one page covers
+  // the tile, and 32-bit offsets of the lane in it that do not change.
+  uint32_t k_off[NS];
+#pragma unroll
+  for (int s = 0; s < NS; ++s) {
+    const int d = 64 * s + 16 * g;
+    k_off[s] = (uint32_t)(((UNIFORM ? 16 * (col >> 2) : 0) + (col & 3)) * dim + (d < dim ? d : 0));
+  }
+  const uint32_t v_off = (uint32_t)((col << c.page_log2) + (UNIFORM ? 16 * g : 0));
+  // what is not seen, or not in the cache, is read from page 0: its scores
+  // are masked, or NaN by their scale
+  auto load_keys = [&](int tile, const Pages& pg, Tile<NS, DT>& o) {
     const int64_t token0 = (int64_t)(k.tile0 + tile) * kTile;
-    const int slot = (int)((token0 + 16 * (col >> 2) + (col & 3)) & page_mask);
-    // what is not seen, or not in the cache, is read from page 0: its scores
-    // are masked, or NaN by their scale
-    const int64_t page_row = ((int64_t)(pg.key > 0 ? pg.key : 0) * c.heads + k.h) << c.page_log2;
+    const int slot = (int)((token0 + (UNIFORM ? 0 : 16 * (col >> 2))) & page_mask);
+    const int8_t* base =
+        c.k + ((((int64_t)(pg.key > 0 ? pg.key : 0) * c.heads + k.h) << c.page_log2) + slot) * dim;
 #pragma unroll
     for (int a = 0; a < 4; ++a)
 #pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        const int d = 64 * s + 16 * g;
-        kd[a][s] = *(const i32x4*)(c.k + (page_row + slot + 4 * a) * dim + (d < dim ? d : 0));
-      }
-    ks = pg.own >= 0 ? c.ks[(int64_t)pg.own * c.heads + k.h] : nan;
+      for (int s = 0; s < NS; ++s) o.kd[a][s] = *(const i32x4*)(base + 4 * a * dim + k_off[s]);
+    o.ks = pg.own >= 0 ? c.ks[(int64_t)pg.own * c.heads + k.h] : nan;
   };
-  Pages pg{0, 0}, pg_next{0, 0};
-  if (t < t_end) {
-    pg = pages_of(t);
-    load_keys(t, pg);
-    if (t + kWaves < t_end) pg_next = pages_of(t + kWaves);
-  }
+  auto load_values = [&](int tile, const Pages& pg, Tile<NS, DT>& o) {
+    const int64_t token0 = (int64_t)(k.tile0 + tile) * kTile;
+    const int64_t ph = (int64_t)(pg.own > 0 ? pg.own : 0) * c.heads + k.h;
+    const int8_t* v = c.v + ph * ((int64_t)dim << c.page_log2) +
+                      ((token0 + (UNIFORM ? 0 : 16 * g)) & page_mask);
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+      o.vd[dt] = *(const i32x4*)(v + ((dt < d16 ? 16 * dt : 0) << c.page_log2) + v_off);
+    o.vs = pg.own >= 0 ? c.vs[ph] : nan;
+  };
+  Tile<NS, DT> cur;
+  Pages pg{0, 0}, pg_next{0, 0};  // of the tile at hand and the next
+  column_init(st);
+  if (t >= t_end) return;
+  pg = pages_of(t);
+  load_keys(t, pg, cur);
+  if (t + step < t_end) pg_next = pages_of(t + step);
 
   // the lane's query row and the positions it sees
   const int64_t r = k.row0 + col;
@@ -425,39 +446,57 @@ __global__ __launch_bounds__(kThreads, DT <= 8 ? 2 : 1) void attention_kernel(At
   const float q_unit = row_digits<NS, ND>(
       p, (k.sp.t0 + tok) * p.q_ts + (int64_t)head * p.q_hs, valid, g, qd);
 
-  Column<DT> st;
-  column_init(st);
-  for (; t < t_end; t += kWaves) {
+  for (; t < t_end; t += step) {
     const int64_t token0 = (int64_t)(k.tile0 + t) * kTile;
-    const int64_t ph = (int64_t)(pg.own > 0 ? pg.own : 0) * c.heads + k.h;
-    i32x4 vd[DT];
-    {
-      const int8_t* v = c.v + ph * ((int64_t)dim << c.page_log2) + ((token0 + 16 * g) & page_mask);
-#pragma unroll
-      for (int dt = 0; dt < DT; ++dt)
-        vd[dt] = *(const i32x4*)(v + ((int64_t)((dt < d16 ? 16 * dt : 0) + col) << c.page_log2));
-    }
-    const float vs = pg.own >= 0 ? c.vs[ph] : nan;
+    load_values(t, pg, cur);
     float sc[4][4];
-    tile_scores<NS, ND>(kd, qd, sc);
-    const float unit = q_unit * ks;
-    if (t + kWaves < t_end) {
-      load_keys(t + kWaves, pg_next);
+    tile_scores<NS, ND>(cur.kd, qd, sc);
+    const float unit = q_unit * cur.ks;
+    if (t + step < t_end) {
+      load_keys(t + step, pg_next, cur);
       pg = pg_next;
-      if (t + 2 * kWaves < t_end) pg_next = pages_of(t + 2 * kWaves);
+      if (t + 2 * step < t_end) pg_next = pages_of(t + 2 * step);
     }
     i32x4 pd[ND];
     float alpha, w;
     if (token0 >= all_lo && token0 + kTile - 1 <= all_hi) {
-      tile_softmax<ND, false, UNIFORM>(sc, unit, vs, 0, 0, st.mx, st.sum, pd, alpha, w);
+      tile_softmax<ND, false, UNIFORM>(sc, unit, cur.vs, 0, 0, st.mx, st.sum, pd, alpha, w);
     } else {
       const int64_t base = token0 + 16 * g;
       const int lo = (int)(see_lo - base > 16 ? 16 : see_lo - base < 0 ? 0 : see_lo - base);
       const int hi = (int)(see_hi - base < -1 ? -1 : see_hi - base > 15 ? 15 : see_hi - base);
-      tile_softmax<ND, true, UNIFORM>(sc, unit, vs, lo, hi, st.mx, st.sum, pd, alpha, w);
+      tile_softmax<ND, true, UNIFORM>(sc, unit, cur.vs, lo, hi, st.mx, st.sum, pd, alpha, w);
     }
-    tile_values<DT, ND>(vd, pd, alpha, w, st.o);
+    tile_values<DT, ND>(cur.vd, pd, alpha, w, st.o);
   }
+}
+
+// One workgroup: 16 query rows of one kv head, one split of their keys, the
+// tiles dealt to its four waves in turn and joined through LDS.
+template <int DT, int ND, bool UNIFORM>
+__global__ __launch_bounds__(kThreads, DT <= 4 ? 3 : DT <= 8 ? 2 : 1) void attention_kernel(AttnParams p) {
+  extern __shared__ float lds[];
+  // Heads vary fastest, then sequences, row blocks and splits: consecutive
+  // workgroups go to the 8 XCDs in turn, so that neither the sequences' lengths
+  // nor the splits that the short ones do not need load one XCD more than
+  // another, and the row blocks of a head share an L2 where there are 8 heads.
+  uint32_t id = blockIdx.x;
+  const int h = id % p.c.heads;
+  id /= p.c.heads;
+  const int b = id % p.batch;
+  id /= p.batch;
+  const int rb = id % p.row_blocks, split = id / p.row_blocks;
+  const Block k = block_of(p, b, h, rb);
+  if (k.row0 >= k.rows) return;
+  // a block whose tiles fit one split writes its output itself
+  const int n_splits = (k.tiles + p.split_tiles - 1) / p.split_tiles;
+  if (split > 0 && split >= n_splits) return;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int col = lane & 15, g = lane >> 4;
+  const int dim = p.c.dim;
+  const int t_end = (split + 1) * p.split_tiles < k.tiles ? (split + 1) * p.split_tiles : k.tiles;
+  Column<DT> st;
+  attend<DT, ND, UNIFORM>(p, k, split * p.split_tiles + wave, t_end, kWaves, st);
 
   // join the waves' parts: [wave][row][dim] outputs, then maxima and sums
   const float sum = column_sum(st.sum);
@@ -510,6 +549,113 @@ __global__ __launch_bounds__(kThreads, DT <= 8 ? 2 : 1) void attention_kernel(At
   if (n_splits > 1 && sub == 0) {
     p.part_ml[2 * at] = m;
     p.part_ml[2 * at + 1] = den;
+  }
+}
+
+// Many keys for few rows: the tiles of all units, a unit being the 16 rows of
+// one sequence, row block and kv head, lie on one line, head after head, and
+// every wave takes an equal piece of it, whatever the sequences' lengths.
+// Waves work alone: a unit that lies in one wave's piece is finished there,
+// the parts of the others go to the workspace and attention_stream_join_kernel
+// adds them.  Walking along the line, either the wave or the unit number grows
+// by one from part to part, so their sum numbers the parts.
+//
+// Measured against the workgroup kernel's splits at 64 sequences of 500 to
+// 8000 tokens (8 kv heads of 128): its workgroups last four tiles per wave,
+// most of it the start-up chain table -> page -> keys, and the sequences'
+// lengths leave a tail.
+template <int DT, int ND, bool UNIFORM>
+__global__ __launch_bounds__(kThreads, DT <= 4 ? 3 : DT <= 8 ? 2 : 1) void attention_stream_kernel(
+    AttnParams p) {
+  extern __shared__ int32_t ends[];  // [units of a head]: tiles up to and with each
+  __shared__ int32_t wave_total[kWaves];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int col = lane & 15, g = lane >> 4;
+  const int units = p.batch * p.row_blocks;
+  // running sum of the units' tiles: a thread's share, then over threads
+  const int per = (units + kThreads - 1) / kThreads;
+  int32_t mine = 0;
+  for (int i = 0; i < per; ++i) {
+    const int u = threadIdx.x * per + i;
+    if (u >= units) break;
+    const Block k = block_of(p, u / p.row_blocks, 0, u % p.row_blocks);
+    mine += k.row0 < k.rows ? k.tiles : 0;
+    ends[u] = mine;
+  }
+  int32_t before = mine;
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1) {
+    const int32_t o = __shfl_up(before, m, 64);
+    before += lane >= m ? o : 0;
+  }
+  if (lane == 63) wave_total[wave] = before;
+  __syncthreads();
+  int32_t line = 0;
+  before -= mine;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    before += w < wave ? wave_total[w] : 0;
+    line += wave_total[w];
+  }
+  for (int i = 0; i < per; ++i) {
+    const int u = threadIdx.x * per + i;
+    if (u >= units) break;
+    ends[u] += before;
+  }
+  __syncthreads();
+  line = __builtin_amdgcn_readfirstlane(line);
+  const int32_t total = line * p.c.heads;
+  const int32_t piece = stream_piece(total, p.stream_waves);
+  if (blockIdx.x == 0 && threadIdx.x == 0) p.stream_info[0] = piece;
+  const int32_t me = (int32_t)blockIdx.x * kWaves + wave;
+  int32_t at = me * piece;
+  const int32_t end = at + piece < total ? at + piece : total;
+  while (at < end) {
+    const int h = at / line;
+    const int32_t rem = at - h * line;
+    // the unit that holds `rem`: the first whose end is past it
+    int lo = 0, hi = units - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (ends[mid] > rem) hi = mid; else lo = mid + 1;
+    }
+    const int u = __builtin_amdgcn_readfirstlane(lo);
+    const Block k = block_of(p, u / p.row_blocks, h, u % p.row_blocks);
+    const int32_t start = h * line + __builtin_amdgcn_readfirstlane(ends[u]) - k.tiles;
+    const int t = at - start;
+    const int t_end = end - start < k.tiles ? end - start : k.tiles;
+    Column<DT> st;
+    attend<DT, ND, UNIFORM>(p, k, t, t_end, 1, st);
+    const float sum = column_sum(st.sum);
+    const int unit = h * units + u;
+    if (t == 0 && lane == 0) p.stream_info[1 + unit] = start;
+    const int64_t r = k.row0 + col;
+    if (r < k.rows) {
+      const int dim = p.c.dim;
+      if (t == 0 && t_end == k.tiles) {
+        const int64_t tok = r / p.group;
+        const int64_t o = (k.sp.t0 + tok) * p.o_ts + (h * p.group + (r - tok * p.group)) * p.o_hs;
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt)
+          if (16 * dt < dim)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              store_elem(p.out, o + 16 * dt + 4 * g + i, st.o[dt][i] * inv, p.dtype);
+      } else {
+        const int64_t slot = ((int64_t)me + unit) * kRows + col;
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt)
+          if (16 * dt < dim)
+            *(f32x4*)&p.part_o[slot * dim + 16 * dt + 4 * g] =
+                f32x4{st.o[dt][0], st.o[dt][1], st.o[dt][2], st.o[dt][3]};
+        if (g == 0) {
+          p.part_ml[2 * slot] = st.mx;
+          p.part_ml[2 * slot + 1] = sum;
+        }
+      }
+    }
+    at = start + t_end;
   }
 }
 

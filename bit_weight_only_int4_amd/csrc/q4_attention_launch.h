@@ -9,6 +9,12 @@ namespace q4 {
 template <int DT, int ND, bool UNIFORM>
 static hipError_t launch_attention_pages(const AttnParams& p, hipStream_t s) {
   using namespace attn;
+  if (p.stream_waves) {
+    const size_t bytes = (size_t)p.batch * p.row_blocks * sizeof(int32_t);
+    hipLaunchKernelGGL((attention_stream_kernel<DT, ND, UNIFORM>),
+                       dim3((unsigned)(p.stream_waves / kWaves)), dim3(kThreads), bytes, s, p);
+    return hipGetLastError();
+  }
   const size_t lds = (size_t)(kWaves * kRows * (16 * DT + 4) + 2 * kWaves * kRows) * sizeof(float);
   if (lds > 65536) {
     const hipError_t e =

@@ -56,12 +56,17 @@ struct AttnParams {
   int32_t row_blocks;           // per sequence and kv head
   int32_t splits;               // workgroups along the keys (grid)
   int32_t split_tiles;          // tiles of 64 keys each of them takes
-  float* part_o;                // [splits][T * heads][dim]
-  float* part_ml;               // [splits][T * heads][2]: max (log2), sum
+  // parts of outputs, and their rows' maximum (log2) and sum: [splits][T *
+  // heads][dim] and [2], or [waves + units][16 rows][dim] and [2]
+  float* part_o;
+  float* part_ml;
+  int32_t stream_waves;         // > 0: attention_stream_kernel
+  int32_t* stream_info;         // piece, then the first tile of each unit on the line
 };
 
 struct AttnPlan {
-  int32_t max_rows, row_blocks, splits, split_tiles;
+  int32_t max_rows, row_blocks, splits, split_tiles, stream_waves;
+  size_t parts;  // rows of partial outputs in the workspace
   size_t workspace;
 };
 AttnPlan plan_attention(int32_t dtype, int64_t T, int64_t batch, int64_t heads, int64_t kv_heads,

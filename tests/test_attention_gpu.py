@@ -38,7 +38,7 @@ def tolerance(out, bound, dtype, scale, max_len, page, spread):
 
 
 def run(new, lengths, heads, kv_heads, dim, page, dtype, *, window=0, seed=0, layout="packed",
-        scale=None, spread=1.0, q_gain=1.5, bounds=True, edit=None):
+        scale=None, spread=1.0, q_gain=1.5, bounds=True, edit=None, max_len=None):
     need_gpu()
     b = Batch(new, lengths, page, seed)
     k, v, ks, vs = random_cache(b, kv_heads, dim, seed + 1, spread)
@@ -51,7 +51,7 @@ def run(new, lengths, heads, kv_heads, dim, page, dtype, *, window=0, seed=0, la
     table, cu, ln = b.device()
     out = strided(torch.full((b.T, heads, dim), float("nan"), dtype=TORCH[dtype]), layout)
     caches = [torch.from_numpy(x).cuda() for x in (k, v, ks, vs)]
-    kw = dict(max_new=max(b.new + [1]), max_len=max(b.lengths + [0])) if bounds else {}
+    kw = dict(max_new=max(b.new + [1]), max_len=max_len or max(b.lengths + [0])) if bounds else {}
     got = q4.attention(strided(qt, layout), *caches, table, cu, ln, softmax_scale=scale,
                        window=window, out=out, **kw)
     torch.cuda.synchronize()
@@ -128,6 +128,35 @@ def test_nothing_to_do():
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_long_axis_split_over_workgroups(lengths, kv_heads, dtype):
     check([1] * len(lengths), lengths, 4 * kv_heads, kv_heads, 64, 64, dtype, seed=3)
+
+
+# a generous max_len: the kernel for long contexts on short ones too
+@pytest.mark.parametrize("page", [16, 32, 64, 128])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_short_contexts_among_long_ones(page, dtype):
+    lengths = [0, 1, 2, 63, 64, 65, 0, 127, 128, 129, 300, 700, 2100, 17]
+    check([1] * len(lengths), lengths, 8, 2, 64, page, dtype, seed=page, max_len=4096)
+    check([0, 1, 1, 0], [70, 0, 400, 90], 4, 4, 128, page, dtype, seed=page, max_len=1 << 20)
+
+
+@pytest.mark.parametrize("heads,kv_heads,new", [(16, 1, [1, 2, 2, 1]), (6, 2, [5, 1, 10, 0]), (32, 1, [1, 1, 1, 1]),
+                                                (7, 1, [3, 4, 2, 1])])
+@pytest.mark.parametrize("window", [0, 100, 2500])
+def test_several_rows_over_long_contexts(heads, kv_heads, new, window):
+    check(new, [2300, 4, 130, 900], heads, kv_heads, 96, 32, "f32", window=window, seed=heads, max_len=9000)
+
+
+@pytest.mark.parametrize("dim", [16, 48, 80, 128, 176, 256])
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_head_sizes_over_long_contexts(dim, dtype):
+    check([1, 1], [2500, 200], 4, 2, dim, 64, dtype, seed=dim)
+
+
+def test_many_sequences():
+    g = np.random.default_rng(0)
+    lengths = [int(x) for x in g.integers(0, 150, 600)]
+    lengths[77] = 2200
+    check([1] * 600, lengths, 2, 1, 32, 16, "f32", seed=1)
 
 
 def test_default_bounds_match_exact_ones():
