@@ -1,20 +1,28 @@
 // q4_logprobs.hip -- token log probabilities, entropy and top alternatives of
 // a row of logits in one pass, and their gradient.
 //
-// With m the running maximum, y = x - m:  S = sum e^y,  W = sum e^y y.  When m
-// grows by d, S and W become  S e^-d  and  (W - d S) e^-d.  Then
-//   lse = m + log S,  logprob = (x_t - m) - log S,  entropy = log S - W / S
+// With m the running maximum, y = (x - m) log2 e:  S = sum 2^y,  W = sum 2^y y.
+// When m grows, so that every y falls by d, they become 2^-d S and
+// 2^-d (W - d S).  Then, with ln 2 for the base,
+//   lse = m + ln S,  logprob = (x_t - m) - ln S,  entropy = ln S - ln 2 W / S
 // (all of W's terms are <= 0, so nothing cancels).  Each thread keeps its own
 // (m, S, W), joined by the same rule.
 //
-// The top_k largest are kept per wave as a sorted list, entry i in lane i.  A
-// value enters only if it beats the last entry, which few do: for values in
-// random order the expected number is top_k (1 + log(n / top_k)).
+// The top_k largest: the lanes' largest so far, in 64 groups, give a bar, their
+// top_k-th largest, that the top_k-th of the row cannot be below.  Every wave
+// collects in LDS what reaches the bar, in any order; it is raised after 1, 2,
+// 4, ... steps, between which about 1.2 top_k more values pass in all for
+// values in random order.  What reaches the last bar is ranked by counting.  A
+// full buffer is cut to its top_k best.  (A sorted list in the lanes, an entry
+// inserted at a time through ballots, took 75 us for 512 rows of 128257 and
+// top_k 5, where this takes 61 us and none at all 54 us.)
 //
 // Bound by HBM reads for many rows; for a few rows, whose parts go to several
 // workgroups and are joined by a second launch, by latency.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "q4_serve.h"
 #include "q4_serve_device.h"
@@ -23,24 +31,22 @@ namespace q4 {
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWaves = kThreads / 64;
 constexpr int kMaxTop = 32;
+constexpr int kChunk = 16;             // elements of a thread's step
 constexpr int32_t kNone = 0x7fffffff;  // index of an empty list entry
 constexpr int kPartStats = 4;          // m, S, W of a part (padded)
+constexpr int kMaxParts = 64;          // of a row: a lane each in the join
 
 struct Stats {
   float m, s, w;
 };
 
-__device__ __forceinline__ Stats stats_empty() { return Stats{-__builtin_inff(), 0.0f, 0.0f}; }
-
 // Joins two; an empty side (m = -inf) leaves the other as it is.
 __device__ __forceinline__ Stats stats_join(const Stats& a, const Stats& b) {
   const float m = fmaxf(a.m, b.m);
   if (m == -__builtin_inff()) return Stats{m, a.s + b.s, a.w + b.w};
-  const float da = a.m - m, db = b.m - m;  // <= 0
-  const float fa = exp2_fast(da * kLog2e), fb = exp2_fast(db * kLog2e);
+  const float da = (a.m - m) * kLog2e, db = (b.m - m) * kLog2e;  // <= 0
+  const float fa = exp2_fast(da), fb = exp2_fast(db);
   // a side too far below to count may overflow in d S (a NaN shows in its S)
   const float wa = fa > 0.0f ? fa * (a.w + da * a.s) : 0.0f;
   const float wb = fb > 0.0f ? fb * (b.w + db * b.s) : 0.0f;
@@ -48,52 +54,173 @@ __device__ __forceinline__ Stats stats_join(const Stats& a, const Stats& b) {
   return Stats{m, sa + sb, wa + wb};
 }
 
-__device__ __forceinline__ Stats stats_shfl(const Stats& a, int mask) {
-  return Stats{__shfl_xor(a.m, mask, 64), __shfl_xor(a.s, mask, 64), __shfl_xor(a.w, mask, 64)};
+__device__ __forceinline__ Stats stats_wave(Stats a) {
+#pragma unroll
+  for (int m = 1; m < 64; m <<= 1)
+    a = stats_join(a, Stats{__shfl_xor(a.m, m, 64), __shfl_xor(a.s, m, 64), __shfl_xor(a.w, m, 64)});
+  return a;
 }
 
 // (value, index) before (v, i) in the order of alternatives
 __device__ __forceinline__ bool before(float value, int32_t index, float v, int32_t i) {
-  return value > v || (value == v && index < i);
+  return (value > v) | ((value == v) & (index < i));
 }
 
-// A wave's sorted list: entry i in lane i (lanes past top_k hold nothing of
-// use), the last entry's value and index known to every lane.
-struct TopList {
-  float value, last_value;
-  int32_t index, last_index;
+// Bits of a number as an integer that orders like it (NaN below all, 0).
+__device__ __forceinline__ uint32_t order_key(float v) {
+  const uint32_t b = f32_bits(v);
+  return v != v ? 0u : (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float key_value(uint32_t key) {
+  return bits_f32((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
+}
+
+// Other lanes' LDS accesses of the same wave are done and seen.
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
+// The key of group i's largest value, different for every group: the low bits
+// give way to its number.
+__device__ __forceinline__ uint32_t group_key(float v, int i) {
+  return (order_key(v) & ~63u) | (uint32_t)i;
+}
+
+// A number that the k-th largest of 64 groups' values is not below, and not
+// more than 2^-17 of it less (-inf if fewer are numbers): every lane counts
+// the groups above its own.  Groups are different elements, and a group's key
+// only grows, so the result stands whatever mix of old and new keys is read.
+__device__ __forceinline__ float kth_of_groups(const uint32_t* keys, int k, int lane) {
+  const uint32_t key = keys[lane];
+  int above = 0;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const u32x4v q = ((const u32x4v*)keys)[i];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) above += q[e] > key ? 1 : 0;
+  }
+  // a key that grows meanwhile can leave no lane at k - 1: no bar this time
+  const uint64_t at = __ballot(above == k - 1);
+  if (at == 0) return -__builtin_inff();
+  const uint32_t kth = (uint32_t)__builtin_amdgcn_readlane((int)key, __builtin_ctzll(at)) & ~63u;
+  return kth < 0x00800000u ? -__builtin_inff() : key_value(kth);  // -inf's key and below
+}
+
+// The largest of each W neighbouring lanes (W = 4 or 16), in every one of them.
+template <int W>
+__device__ __forceinline__ float group_max(float v) {
+  auto dpp = [&](auto ctrl) {
+    return bits_f32((uint32_t)__builtin_amdgcn_update_dpp(0, (int)f32_bits(v), decltype(ctrl)::value,
+                                                          0xf, 0xf, true));
+  };
+  v = fmaxf(v, dpp(std::integral_constant<int, 0xb1>{}));   // quad_perm 1 0 3 2
+  v = fmaxf(v, dpp(std::integral_constant<int, 0x4e>{}));   // quad_perm 2 3 0 1
+  if (W == 16) {
+    v = fmaxf(v, dpp(std::integral_constant<int, 0x124>{}));  // row_ror 4
+    v = fmaxf(v, dpp(std::integral_constant<int, 0x128>{}));  // row_ror 8
+  }
+  return v;
+}
+
+constexpr int kBuffer = 256;  // of a wave's candidates, a multiple of 64
+constexpr int kFinal = 64;    // of them at the end
+
+// A wave's candidates: values and indices in LDS, how many, and what the next
+// ones have to be before.
+struct Best {
+  float* val;
+  int32_t* id;
+  int count;
+  float bar;
+  int32_t bar_id;
 };
 
-__device__ __forceinline__ TopList top_empty() {
-  return TopList{-__builtin_inff(), -__builtin_inff(), kNone, kNone};
+// Leaves the k best of more than k candidates, and raises the bar to the last.
+__device__ __forceinline__ void best_cut(Best& t, int k, int lane) {
+  constexpr int J = kBuffer / 64;
+  float v[J];
+  uint32_t key[J];
+  int32_t id[J];
+  wave_lds_fence();
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const int e = 64 * j + lane;
+    const bool on = e < t.count;
+    v[j] = on ? t.val[e] : 0.0f;
+    id[j] = on ? t.id[e] : kNone;
+    key[j] = on ? order_key(v[j] + 0.0f) : 0u;  // -0 and 0 are equal: both 0
+  }
+  wave_lds_fence();
+  uint32_t at = 0;
+#pragma unroll 1
+  for (int bit = 31; bit >= 0; --bit) {
+    const uint32_t next = at | (1u << bit);
+    int c = 0;
+#pragma unroll
+    for (int j = 0; j < J; ++j) c += __popcll(__ballot(key[j] >= next));
+    if (c >= k) at = next;
+  }
+  int above = 0, ties = 0;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    above += __popcll(__ballot(key[j] > at));
+    ties += __popcll(__ballot(key[j] == at));
+  }
+  int32_t last = kNone;  // of equal ones, the lowest indices stay
+  if (above + ties > k) {
+    last = 0;
+#pragma unroll 1
+    for (int bit = 30; bit >= 0; --bit) {
+      const int32_t next = last | (1 << bit);
+      int c = above;
+#pragma unroll
+      for (int j = 0; j < J; ++j) c += __popcll(__ballot(key[j] == at && id[j] < next));
+      if (c < k) last = next;
+    }
+  }
+  t.count = 0;
+#pragma unroll
+  for (int j = 0; j < J; ++j) {
+    const bool keep = key[j] > at || (key[j] == at && id[j] <= last);
+    const uint64_t mask = __ballot(keep);
+    if (keep) {
+      const int to = t.count + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
+                                                         __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+      t.val[to] = v[j];
+      t.id[to] = id[j];
+    }
+    t.count += __popcll(mask);
+  }
+  wave_lds_fence();
+  t.bar = key_value(at);
+  t.bar_id = last;
 }
 
-// Every lane passes the same (v, i).
-__device__ __forceinline__ void top_insert(TopList& t, float v, int32_t i, int k, int lane) {
-  const uint64_t ahead = __ballot(before(t.value, t.index, v, i));
-  const int at = __popcll(ahead);
-  if (at >= k) return;
-  const float pv = __shfl_up(t.value, 1, 64);
-  const int32_t pi = __shfl_up(t.index, 1, 64);
-  if (lane > at) {
-    t.value = pv;
-    t.index = pi;
-  } else if (lane == at) {
-    t.value = v;
-    t.index = i;
+// The lanes' values x (number i), each kept if it is before the bar.
+__device__ __forceinline__ void best_offer(Best& t, float x, int32_t i, bool on, int k, int lane) {
+  const bool keep = on && before(x, i, t.bar, t.bar_id);
+  const uint64_t mask = __ballot(keep);
+  if (!mask) return;
+  if (t.count > kBuffer - 64) best_cut(t, k, lane);
+  if (keep) {
+    const int to = t.count + __builtin_amdgcn_mbcnt_hi((uint32_t)(mask >> 32),
+                                                       __builtin_amdgcn_mbcnt_lo((uint32_t)mask, 0));
+    t.val[to] = x;
+    t.id[to] = i;
   }
-  t.last_value = __shfl(t.value, k - 1, 64);
-  t.last_index = __shfl(t.index, k - 1, 64);
+  t.count += __popcll(mask);
 }
 
-// The lanes' values x (index i), each entering if it belongs.
-__device__ __forceinline__ void top_offer(TopList& t, float x, int32_t i, bool on, int k, int lane) {
-  uint64_t todo = __ballot(on && before(x, i, t.last_value, t.last_index));
-  while (todo) {
-    const int from = __builtin_ctzll(todo);
-    todo &= todo - 1;
-    top_insert(t, __shfl(x, from, 64), __shfl(i, from, 64), k, lane);
-  }
+// Sum over the lanes up to and with this one.
+__device__ __forceinline__ int lane_scan(int x) {
+  x += __builtin_amdgcn_update_dpp(0, x, 0x111, 0xf, 0xf, true);  // row_shr 1, 2, 4, 8
+  x += __builtin_amdgcn_update_dpp(0, x, 0x112, 0xf, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x114, 0xf, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x118, 0xf, 0xf, true);
+  x += __builtin_amdgcn_update_dpp(0, x, 0x142, 0xa, 0xf, false);  // row_bcast 15, 31
+  x += __builtin_amdgcn_update_dpp(0, x, 0x143, 0xc, 0xf, false);
+  return x;
 }
 
 struct Result {
@@ -103,7 +230,7 @@ struct Result {
 __device__ __forceinline__ Result finish(const Stats& a) {
   if (a.s == 0.0f) return Result{-__builtin_inff(), 0.0f};  // nothing but -inf
   const float log_s = log2_fast(a.s) * kLn2;
-  return Result{a.m + log_s, log_s - a.w / a.s};
+  return Result{a.m + log_s, log_s - kLn2 * (a.w / a.s)};
 }
 
 // Log probability of x given the statistics: x - m first, as both may be large.
@@ -112,36 +239,56 @@ __device__ __forceinline__ float logprob_of(float x, const Stats& a) {
   return (x - a.m) - log2_fast(a.s) * kLn2;
 }
 
+// The target's logit, loaded before the sums are known: 0 and no target, NaN
+// where it is past the row.
+struct Target {
+  float x;
+  bool is;
+};
+
 template <typename T>
-__device__ __forceinline__ void write_row(const LogprobParams& p, int64_t row, const Stats& a) {
+__device__ __forceinline__ Target target_of(const LogprobParams& p, int64_t row) {
+  const int64_t t = p.targets ? p.targets[row] : -1;
+  Target r{bits_f32(0x7fc00000u), t >= 0};
+  if (t >= 0 && t < p.V) r.x = to_f32(((const T*)p.x)[row * p.ld + t]);
+  return r;
+}
+
+__device__ __forceinline__ void write_row(const LogprobParams& p, int64_t row, const Stats& a,
+                                          const Target& t) {
   const Result r = finish(a);
   p.lse[row] = r.lse;
   p.entropy[row] = r.entropy;
-  if (p.targets) {
-    const int64_t t = p.targets[row];
-    float lp = 0.0f;
-    if (t >= p.V) lp = bits_f32(0x7fc00000u);
-    else if (t >= 0) lp = logprob_of(to_f32(((const T*)p.x)[row * p.ld + t]), a);
-    p.logprob[row] = lp;
-  }
+  if (p.targets) p.logprob[row] = !t.is ? 0.0f : t.x != t.x ? t.x : logprob_of(t.x, a);
 }
 
-// Ranks the n entries of (vals, ids) in LDS and gives the first k to `out`
-// (called with the entry's rank, value and index).  Indices differ, but for
-// empty entries, which come last in any order.
+// A candidate as one integer: larger for one that is before another.  -0 and 0
+// are equal, and both become 0.
+__device__ __forceinline__ uint64_t entry_of(float v, int32_t i) {
+  return (uint64_t)order_key(v + 0.0f) << 32 | (uint32_t)~i;
+}
+__device__ __forceinline__ float entry_value(uint64_t e) { return key_value((uint32_t)(e >> 32)); }
+__device__ __forceinline__ int32_t entry_index(uint64_t e) { return (int32_t)~(uint32_t)e; }
+
+// Ranks the n entries in LDS, all different and 16-byte aligned with a spare
+// one at the end, and gives the first k to `out` (called with the rank, value
+// and index); the ranks past n are empty.
 template <typename F>
-__device__ __forceinline__ void rank_entries(const float* vals, const int32_t* ids, int n, int k,
-                                             F out) {
-  for (int e = threadIdx.x; e < n; e += kThreads) {
-    const float v = vals[e];
-    const int32_t i = ids[e];
+__device__ __forceinline__ void rank_entries(uint64_t* entries, int n, int k, F out) {
+  typedef uint64_t u64x2 __attribute__((ext_vector_type(2)));
+  if (threadIdx.x == 0) entries[n] = 0;
+  __syncthreads();
+  for (int e = threadIdx.x; e < n; e += blockDim.x) {
+    const uint64_t mine = entries[e];
     int rank = 0;
-    for (int o = 0; o < n; ++o) {
-      const bool b = before(vals[o], ids[o], v, i) || (ids[o] == i && vals[o] == v && o < e);
-      rank += b ? 1 : 0;
+#pragma unroll 8
+    for (int o = 0; o < n; o += 2) {
+      const u64x2 q = *(const u64x2*)(entries + o);
+      rank += (q[0] > mine ? 1 : 0) + (q[1] > mine ? 1 : 0);
     }
-    if (rank < k) out(rank, v, i);
+    if (rank < k) out(rank, entry_value(mine), entry_index(mine));
   }
+  for (int e = n + threadIdx.x; e < k; e += blockDim.x) out(e, -__builtin_inff(), kNone);
 }
 
 __device__ __forceinline__ void write_top(const LogprobParams& p, int64_t row, int rank, float v,
@@ -151,45 +298,99 @@ __device__ __forceinline__ void write_top(const LogprobParams& p, int64_t row, i
   p.top_lp[at] = i == kNone ? bits_f32(0x7fc00000u) : logprob_of(v, a);
 }
 
-// One part (or all) of a row per workgroup.
-template <typename T>
-__global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobParams p) {
-  constexpr int N = 16 / sizeof(T);
-  __shared__ Stats wave_stats[kWaves];
-  __shared__ float top_vals[kWaves * kMaxTop];
-  __shared__ int32_t top_ids[kWaves * kMaxTop];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t row = blockIdx.x / p.splits;
-  const int split = (int)(blockIdx.x - row * p.splits);
+// One part (or all) of a row per workgroup of W waves.  The next step's
+// elements load while this one's are summed.
+template <typename T, int W>
+__global__ __launch_bounds__(64 * W) void logprobs_kernel(LogprobParams p) {
+  constexpr int N = 16 / sizeof(T), C = kChunk / N, kThreads = 64 * W;
+  __shared__ Stats wave_stats[W];
+  __shared__ float best_val[W][kBuffer];
+  __shared__ int32_t best_id[W][kBuffer];
+  __shared__ __attribute__((aligned(16))) uint32_t keys[64];
+  __shared__ __attribute__((aligned(16))) uint64_t entries[W * kFinal + 2];
+  __shared__ int32_t top_count;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const uint32_t row32 = blockIdx.x / (uint32_t)p.splits;
+  const int split = (int)(blockIdx.x - row32 * (uint32_t)p.splits);
+  const int64_t row = row32;
   const int64_t from = split * p.split_len;
   const int64_t to = from + p.split_len < p.V ? from + p.split_len : p.V;
   const T* x = (const T*)p.x + row * p.ld;
   const int k = p.top_k;
+  const float inf = __builtin_inff();
 
-  Stats st = stats_empty();
-  TopList top = top_empty();
-  auto take = [&](const float (&v)[N], int n, int64_t at) {
+  Target target{0.0f, false};
+  if (p.splits == 1 && tid == 0) target = target_of<T>(p, row);
+  Stats st{-inf, 0.0f, 0.0f};
+  Best best{best_val[wave], best_id[wave], 0, -inf, kNone};
+  int step = 0;
+  if (tid == 0) top_count = 0;
+  // element e of v is number at + (e / N) * stride + e % N of the row, if that
+  // is below limit; the first `count` are offered as alternatives
+  auto take = [&](const float (&v)[kChunk], int32_t at, int32_t stride, int32_t limit, int count) {
     float vm = v[0];
 #pragma unroll
-    for (int e = 1; e < N; ++e) vm = fmaxf(vm, v[e]);
+    for (int e = 1; e < kChunk; ++e) vm = fmaxf(vm, v[e]);
     const float m = fmaxf(st.m, vm);
-    const float ref = m > -__builtin_inff() ? m : 0.0f;
-    const float d = st.m - ref;
-    const float f = exp2_fast(d * kLog2e);
+    const float ref = m > -inf ? m : 0.0f;
+    const float d = (st.m - ref) * kLog2e;
+    const float f = exp2_fast(d);
     // an empty sum stays 0 (d is -inf), one too far below may overflow in d S
     st.w = f > 0.0f ? f * (st.w + d * st.s) : 0.0f;
     st.s = f * st.s;
     st.m = m;
+    float s = 0.0f, w = 0.0f;
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
-      const float y = v[e] - ref;
-      const float ex = exp2_fast(y * kLog2e);
-      st.s += ex;
-      st.w += ex == 0.0f ? 0.0f : ex * y;  // y may be -inf
+    for (int e = 0; e < kChunk; ++e) {
+      const float y = (v[e] - ref) * kLog2e;
+      const float ex = exp2_fast(y);
+      s += ex;
+      w = __builtin_fmaf(ex, fmaxf(y, -1e5f), w);  // y may be -inf; a NaN shows in s
     }
-    if (k > 0 && __any(vm >= top.last_value)) {
+    st.s += s;
+    st.w += w;
+    if (k > 0) {
+      if ((step & (step - 1)) == 0) {  // steps 0, 1, 2, 4, ...
+        const float gm = group_max<W>(st.m);
+        if (lane % W == 0) keys[tid / W] = group_key(gm, tid / W);
+        if (step == 0) __syncthreads();
+        else wave_lds_fence();
+        const float bar = kth_of_groups(keys, k, lane);
+        if (bar > best.bar) {
+          best.bar = bar;
+          best.bar_id = kNone;
+        }
+      }
+      ++step;
+      if (__any(vm >= best.bar)) {
+        // after a cut, equal values of later steps have higher indices
+        const float least =
+            best.bar_id == kNone ? best.bar : key_value(order_key(best.bar + 0.0f) + 1);
+        int n = 0;
 #pragma unroll
-      for (int e = 0; e < N; ++e) top_offer(top, v[e], (int32_t)(at + e), e < n, k, lane);
+        for (int e = 0; e < kChunk; ++e) n += v[e] >= least ? 1 : 0;
+        const int upto = lane_scan(n);
+        const int total = __builtin_amdgcn_readlane(upto, 63);
+        // (places past the row hold -inf)
+        if (count == kChunk && best.bar > -inf && best.count + total <= kBuffer) {
+          int to = best.count + upto - n;
+#pragma unroll
+          for (int e = 0; e < kChunk; ++e)
+            if (v[e] >= least) {
+              best.val[to] = v[e];
+              best.id[to] = at + (e / N) * stride + e % N;
+              ++to;
+            }
+          best.count += total;
+        } else {
+#pragma unroll 1
+          for (int e = 0; e < count; ++e) {
+            const int32_t i = at + (e / N) * stride + e % N;
+            best_offer(best, v[e], i, i < limit, k, lane);
+          }
+        }
+      }
     }
   };
   // elements up to the first 16-byte boundary, whole vectors, the rest
@@ -198,86 +399,133 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobParams p) {
   if (head > to - from) head = to - from;
   const int64_t vecs = (to - from - head) / N;
   const int64_t tail = from + head + vecs * N;
+  const u32x4v* body = (const u32x4v*)(x + from + head);
+  u32x4v next[C];
+  u32x4v none;  // -inf in every element
   {
-    float v[N];
+    T t[N];
 #pragma unroll
-    for (int e = 0; e < N; ++e) v[e] = -__builtin_inff();
-    // lane l of wave 0 takes element l of the head, then of the tail
-    if (wave == 0) {
-      if (lane < head) v[0] = to_f32(x[from + lane]);
-      take(v, lane < head ? 1 : 0, from + lane);
-      v[0] = tail + lane < to ? to_f32(x[tail + lane]) : -__builtin_inff();
-      take(v, tail + lane < to ? 1 : 0, tail + lane);
-    }
+    for (int e = 0; e < N; ++e) t[e] = (T)-inf;
+    __builtin_memcpy(&none, t, 16);
   }
-  const T* body = x + from + head;
-  // whole waves step together: a lane past the end offers nothing
-  for (int64_t i0 = (int64_t)wave * 64; i0 < vecs; i0 += kThreads) {
-    const int64_t i = i0 + lane;
-    float v[N];
-    if (i < vecs) {
-      const u32x4v w = *(const u32x4v*)(body + i * N);
-      const T* t = (const T*)&w;
+  auto load = [&](int64_t i0) {
 #pragma unroll
-      for (int e = 0; e < N; ++e) v[e] = to_f32(t[e]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < N; ++e) v[e] = -__builtin_inff();
+    for (int c = 0; c < C; ++c) {
+      const int64_t i = i0 + c * kThreads + tid;
+      next[c] = i < vecs ? body[i] : none;
     }
-    take(v, i < vecs ? N : 0, from + head + i * N);
-  }
+  };
+  load(0);
+  // the elements before the first and after the last whole vector are one
+  // more step of the first wave: one a lane, the tail's from lane N on
+  const int64_t edge = lane < N ? from + lane : tail + lane - N;
+  const bool on_edge = lane < N ? lane < head : lane < 2 * N && tail + lane - N < to;
+  const bool edges = wave == 0 && (head > 0 || tail < to);
+  const float edge_x = edges && on_edge ? to_f32(x[edge]) : -inf;
+  // (at least one, the same for all waves: the first has a barrier)
+  const int64_t steps = vecs > 0 ? (vecs + C * kThreads - 1) / (C * kThreads) : 1;
+  for (int64_t it = 0; it < steps + (edges ? 1 : 0); ++it) {
+    const bool last = it == steps;
+    float v[kChunk];
 #pragma unroll
-  for (int m = 1; m < 64; m <<= 1) st = stats_join(st, stats_shfl(st, m));
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        T t[N];
+        __builtin_memcpy(t, &next[c], 16);
+        v[c * N + e] = last ? -inf : to_f32(t[e]);
+      }
+    if (last) v[0] = edge_x;
+    if (it + 1 < steps) load((it + 1) * C * kThreads);
+    const int32_t at = (int32_t)(last ? (on_edge ? edge : to) : from + head + (it * C * kThreads + tid) * N);
+    take(v, at, kThreads * N, (int32_t)(last ? to : tail), last ? 1 : kChunk);
+  }
+  if (k > 0) {
+    const float gm = group_max<W>(st.m);
+    if (lane % W == 0) keys[tid / W] = group_key(gm, tid / W);
+  }
+  st = stats_wave(st);
   if (lane == 0) wave_stats[wave] = st;
-  if (lane < k) {
-    top_vals[wave * k + lane] = top.value;
-    top_ids[wave * k + lane] = top.index;
-  }
   __syncthreads();
   st = wave_stats[0];
 #pragma unroll
-  for (int w = 1; w < kWaves; ++w) st = stats_join(st, wave_stats[w]);
+  for (int w = 1; w < W; ++w) st = stats_join(st, wave_stats[w]);
+  if (k > 0) {
+    const float bar = kth_of_groups(keys, k, lane);
+    int n = 0;
+    wave_lds_fence();
+    for (int e = lane; e < best.count; e += 64) n += best.val[e] >= bar ? 1 : 0;
+    if (__builtin_amdgcn_readlane(lane_scan(n), 63) > kFinal) best_cut(best, k, lane);
+    for (int e = lane; e < best.count; e += 64)
+      if (best.val[e] >= bar) {
+        const int to = atomicAdd(&top_count, 1);  // any order: they are ranked
+        entries[to] = entry_of(best.val[e], best.id[e]);
+      }
+    __syncthreads();
+  }
+  const int found = k > 0 ? top_count : 0;
   if (p.splits == 1) {
-    if (threadIdx.x == 0) write_row<T>(p, row, st);
-    rank_entries(top_vals, top_ids, kWaves * k, k,
+    if (tid == 0) write_row(p, row, st, target);
+    rank_entries(entries, found, k,
                  [&](int rank, float v, int32_t i) { write_top(p, row, rank, v, i, st); });
   } else {
     const int64_t part = blockIdx.x;
-    if (threadIdx.x == 0) {
+    if (tid == 0) {
       p.part[part * kPartStats] = st.m;
       p.part[part * kPartStats + 1] = st.s;
       p.part[part * kPartStats + 2] = st.w;
     }
-    rank_entries(top_vals, top_ids, kWaves * k, k, [&](int rank, float v, int32_t i) {
+    rank_entries(entries, found, k, [&](int rank, float v, int32_t i) {
       p.part_val[part * k + rank] = v;
       p.part_id[part * k + rank] = i;
     });
   }
 }
 
-// Joins the parts of a row.
+// Joins the parts of a row.  The parts' alternatives that can be the row's
+// are ranked.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void logprobs_join_kernel(LogprobParams p) {
-  extern __shared__ float vals[];  // [splits * k], then the indices
+__global__ __launch_bounds__(256) void logprobs_join_kernel(LogprobParams p) {
+  __shared__ __attribute__((aligned(16))) uint64_t entries[kMaxParts * kMaxTop + 2];
+  __shared__ __attribute__((aligned(16))) uint32_t keys[64];
+  __shared__ int32_t count;
   const int64_t row = blockIdx.x;
-  const int k = p.top_k, n = p.splits * k;
-  int32_t* ids = (int32_t*)(vals + n);
-  for (int e = threadIdx.x; e < n; e += kThreads) {
-    vals[e] = p.part_val[row * n + e];
-    ids[e] = p.part_id[row * n + e];
+  const int k = p.top_k, n = p.splits * k, tid = threadIdx.x, lane = tid & 63;
+  if (tid == 0) count = 0;
+  Target target{0.0f, false};
+  if (tid == 0) target = target_of<T>(p, row);
+  Stats st{-__builtin_inff(), 0.0f, 0.0f};
+  if (lane < p.splits) {
+    const float* q = p.part + (row * p.splits + lane) * kPartStats;
+    st = Stats{q[0], q[1], q[2]};
   }
-  Stats st = stats_empty();
-  for (int s = 0; s < p.splits; ++s) {
-    const float* q = p.part + (row * p.splits + s) * kPartStats;
-    st = stats_join(st, Stats{q[0], q[1], q[2]});
-  }
+  // a group is a part's best depth + 1, and its value the least of them: k of
+  // the row are no less than that of the need-th group
+  const int depth = k > 0 ? (k - 1) / p.splits : 0, need = (k + depth) / (depth + 1);
+  if (tid < 64)
+    keys[tid] = group_key(k > 0 && tid < p.splits ? p.part_val[(row * p.splits + tid) * k + depth]
+                                                  : bits_f32(0x7fc00000u), tid);
   __syncthreads();
-  if (threadIdx.x == 0) write_row<T>(p, row, st);
-  rank_entries(vals, ids, n, k,
+  const float bar = k > 0 ? kth_of_groups(keys, need, lane) : 0.0f;
+  for (int e = tid; e < n; e += 256) {
+    const float v = p.part_val[row * n + e];
+    const int32_t i = p.part_id[row * n + e];
+    if (v >= bar && i != kNone) {
+      const int at = atomicAdd(&count, 1);  // any order: they are ranked
+      entries[at] = entry_of(v, i);
+    }
+  }
+  st = stats_wave(st);
+  __syncthreads();
+  const int found = count;
+  if (tid == 0) write_row(p, row, st, target);
+  rank_entries(entries, found, k,
                [&](int rank, float v, int32_t i) { write_top(p, row, rank, v, i, st); });
 }
 
 // dx_v = g (1[v = t] - p_v) - h p_v (log p_v + H), 16 bytes a thread.
+constexpr int kThreads = 256;  // of the gradient
+
 template <typename T>
 __global__ __launch_bounds__(kThreads) void logprobs_backward_kernel(LogprobBwdParams p,
                                                                      int64_t blocks_per_row) {
@@ -325,16 +573,16 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 }  // namespace
 
-// Rows go to several workgroups while rows alone leave the chip without work.
+// Rows go to several workgroups, each at least a step of a workgroup of four
+// waves, while rows alone leave CUs without work.
 LogprobPlan plan_logprobs(int64_t M, int64_t V, int64_t top_k, int32_t dtype) {
   (void)dtype;
-  constexpr int64_t kTargetBlocks = 1024, kMinLen = 4096;
+  constexpr int64_t kTargetBlocks = 512, kMinLen = 4 * 64 * kChunk;
   LogprobPlan pl;
-  int64_t splits = ceil_div(kTargetBlocks, M > 0 ? M : 1);
+  int64_t splits = kTargetBlocks / (M > 0 ? M : 1);
   if (splits > ceil_div(V, kMinLen)) splits = ceil_div(V, kMinLen);
-  if (M >= 256) splits = 1;
-  if (splits < 1) splits = 1;
-  if (splits > 64) splits = 64;
+  if (splits > kMaxParts) splits = kMaxParts;
+  if (splits < 2) splits = 1;
   pl.split_len = ceil_div(ceil_div(V, splits), 64) * 64;
   pl.splits = (int32_t)ceil_div(V, pl.split_len);
   const size_t n = pl.splits > 1 ? (size_t)M * pl.splits : 0;
@@ -344,13 +592,16 @@ LogprobPlan plan_logprobs(int64_t M, int64_t V, int64_t top_k, int32_t dtype) {
 
 hipError_t launch_logprobs(const LogprobParams& p, int32_t dtype, hipStream_t s) {
   const dim3 grid((unsigned)(p.M * p.splits));
-  const size_t lds = (size_t)p.splits * p.top_k * (sizeof(float) + sizeof(int32_t));
-#define Q4_LOGPROBS(T)                                                                       \
-  do {                                                                                       \
-    hipLaunchKernelGGL((logprobs_kernel<T>), grid, dim3(kThreads), 0, s, p);                 \
-    if (p.splits > 1)                                                                        \
-      hipLaunchKernelGGL((logprobs_join_kernel<T>), dim3((unsigned)p.M), dim3(kThreads), lds, \
-                         s, p);                                                              \
+  // a long row of its own workgroup is shared by 16 waves
+  const bool wide = p.splits == 1 && p.V >= 16 * 64 * kChunk;
+#define Q4_LOGPROBS(T)                                                                         \
+  do {                                                                                         \
+    if (wide)                                                                                  \
+      hipLaunchKernelGGL((logprobs_kernel<T, 16>), grid, dim3(1024), 0, s, p);                 \
+    else                                                                                       \
+      hipLaunchKernelGGL((logprobs_kernel<T, 4>), grid, dim3(256), 0, s, p);                   \
+    if (p.splits > 1)                                                                          \
+      hipLaunchKernelGGL((logprobs_join_kernel<T>), dim3((unsigned)p.M), dim3(256), 0, s, p);  \
   } while (0)
   if (dtype == Q4_DTYPE_F32) Q4_LOGPROBS(float);
   else if (dtype == Q4_DTYPE_F16) Q4_LOGPROBS(_Float16);

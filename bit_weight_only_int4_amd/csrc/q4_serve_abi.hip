@@ -298,8 +298,11 @@ q4_status q4_attention(const void* q, int64_t q_ts, int64_t q_hs, void* out, int
   return status_of(q4::launch_attention(p, (hipStream_t)stream));
 }
 
+// indices within a row, a step past its end included, are 32-bit
+constexpr int64_t kMaxVocab = (int64_t)1 << 30;
+
 static bool logprob_sizes_ok(int64_t M, int64_t vocab, int64_t top_k, int32_t dtype) {
-  return dtype_ok(dtype) && size_ok(M) && vocab >= 1 && vocab < kMaxDim && top_k >= 0 &&
+  return dtype_ok(dtype) && size_ok(M) && vocab >= 1 && vocab <= kMaxVocab && top_k >= 0 &&
          top_k <= 32 && top_k <= vocab;
 }
 

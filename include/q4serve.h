@@ -156,7 +156,7 @@ size_t q4_attention_workspace_bytes(int32_t dtype, int64_t T, int64_t batch,
  *   entropy  = -sum_v p_v log p_v,  p_v = exp(x_v - lse)
  *   top_ids, top_logprobs [M, top_k]: the top_k largest logits in descending
  *              order, equal ones by ascending index, and their x - lse
- * in fp32, sums in fp32, one pass over the logits.
+ * in fp32, sums in fp32, one pass over the logits.  vocab is at most 2^30.
  *   targets  int64 [M] or NULL (then logprob is not written).  A negative
  *            target stands for none: logprob 0.  One >= vocab gives NaN.
  *   top_k    0 .. 32, at most vocab
