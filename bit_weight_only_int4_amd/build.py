@@ -1,11 +1,13 @@
-"""Build the gfx950 HIP library ``libq4linear.so`` in-tree.
+"""Build the gfx950 HIP library ``libq4linear.so`` in-tree, and the native
+half of the Python binding ``serve`` (``_serve_native.so``: host code, against
+torch's headers) beside it.
 
 Every source under ``csrc/`` is compiled with hipcc for gfx950 only, in
 parallel, then linked into one shared library beside this file.  No
 fast-math flags: fp32 denormals are kept and every operation rounds as IEEE
 specifies.  Packed fp32 instructions are disabled for the device code.
 
-Beside the library the build writes ``libq4linear.so.sha256``: a digest of
+Beside each of them the build writes a stamp, ``libq4linear.so.sha256``: a digest of
 the sources it was built from (comments and blank space removed), which the
 binding compares with the sources in the tree before it loads the library.
 """
@@ -22,7 +24,9 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libq4linear.so")
+NATIVE = os.path.join(HERE, "_serve_native.so")
 TREE_LIB = LIB  # the in-tree library, whose stamp the binding checks
+CXX = os.environ.get("CXX", "g++")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
@@ -82,10 +86,43 @@ def _compile(src: str, verbose: bool) -> str:
     return obj
 
 
+def _compile_native(verbose: bool) -> str:
+    """The C++ half of ``serve``, as an object file."""
+    import sysconfig
+
+    import torch
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    obj = os.path.join(BUILD_DIR, "q4_serve_py.o")
+    cmd = [CXX, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall", f"-I{INCLUDE}",
+           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"],
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-c",
+           os.path.join(CSRC, "q4_serve_py.cpp"), "-o", obj]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{CXX} failed for q4_serve_py.cpp:\n{r.stdout}{r.stderr}")
+    return obj
+
+
+def _link_native(obj: str, digest: str) -> None:
+    """Links it to the library beside it."""
+    import torch
+    tmp = NATIVE + ".tmp"
+    subprocess.run([CXX, "-shared", obj, "-o", tmp, f"-L{HERE}", "-lq4linear",
+                    f"-L{os.path.join(os.path.dirname(torch.__file__), 'lib')}", "-ltorch_python",
+                    "-ltorch", "-ltorch_cpu", "-lc10", "-Wl,-rpath,$ORIGIN"], check=True)
+    os.replace(tmp, NATIVE)
+    with open(stamp_path(NATIVE), "w") as f:
+        f.write(digest + "\n")
+
+
 def build(verbose: bool = False, jobs: int = 8) -> str:
     os.makedirs(BUILD_DIR, exist_ok=True)
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.hip")))
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+        native = ex.submit(_compile_native, verbose)
         objs = list(ex.map(lambda s: _compile(s, verbose), srcs))
     tmp = LIB + ".tmp"
     cmd = [HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, "-o", tmp]
@@ -96,6 +133,7 @@ def build(verbose: bool = False, jobs: int = 8) -> str:
     os.replace(tmp, LIB)
     with open(stamp_path(LIB), "w") as f:
         f.write(digest + "\n")
+    _link_native(native.result(), digest)
     return LIB
 
 

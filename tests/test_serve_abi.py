@@ -140,31 +140,85 @@ def test_dequant_refusals():
     assert call("q4_kv_dequant", base, pages=0) == OK
 
 
-def test_the_binding_refuses_host_tensors_and_wrong_shapes():
-    cache = q4.new_cache(4, 2, 64, 16, device="cpu")
-    i = lambda *v: torch.tensor(v, dtype=torch.int32)  # noqa: E731
-    x = torch.zeros((1, 2, 64))
-    with pytest.raises(ValueError, match="device tensor"):
-        q4.kv_append(x, x, *cache, i(0)[None], i(0, 1), i(1))
-    with pytest.raises(ValueError, match="device tensor"):
-        q4.attention(x, *cache, i(0)[None], i(0, 1), i(1))
-    with pytest.raises(ValueError, match="device tensor"):
-        q4.token_logprobs(torch.zeros((2, 5)))
-    with pytest.raises(ValueError, match="device tensor"):
-        q4.token_logprobs_backward(torch.zeros((2, 5)), None, torch.zeros(2), torch.zeros(2), None, torch.zeros(2))
-    with pytest.raises(ValueError, match="device tensor"):
-        q4.kv_dequant(*cache)
+def i32(*v):
+    return torch.tensor(v, dtype=torch.int32)
+
+
+def binding_args(op, **kw):
+    """Arguments that pass every check but the last, that they are on a GPU."""
+    c = dict(zip(("k_cache", "v_cache", "k_scale", "v_scale"), q4.new_cache(4, 2, 64, 16, device="cpu")))
+    tables = dict(page_table=i32(0, 1)[None], cu_new=i32(0, 3), lengths=i32(5))
+    x = torch.zeros((2, 9))
+    a = {"kv_append": dict(k=torch.zeros((3, 2, 64)), v=torch.zeros((3, 2, 64)), **c, **tables,
+                           q=torch.zeros((3, 4, 64)), inv_freq=torch.ones(32)),
+         "attention": dict(q=torch.zeros((3, 4, 64)), **c, **tables),
+         "kv_dequant": c,
+         "token_logprobs": dict(logits=x, targets=torch.zeros(2, dtype=torch.int64), top_k=3),
+         "token_logprobs_backward": dict(logits=x, targets=torch.zeros(2, dtype=torch.int64), lse=torch.zeros(2),
+                                         entropy=torch.zeros(2), g_logprob=torch.zeros(2))}[op]
+    return {**a, **kw}
+
+
+@pytest.mark.parametrize("op", ["kv_append", "attention", "kv_dequant", "token_logprobs", "token_logprobs_backward"])
+def test_the_binding_refuses_host_tensors(op):
+    with pytest.raises(ValueError, match="must be a device tensor"):
+        getattr(q4, op)(**binding_args(op))
+
+
+CACHE = [("k_cache", torch.zeros((4, 2, 8, 64), dtype=torch.int8)), ("k_cache", torch.zeros((4, 2, 16, 64))),
+         ("k_cache", torch.zeros((2, 16, 64), dtype=torch.int8)), ("v_cache", torch.zeros((4, 2, 16, 64), dtype=torch.int8)),
+         ("v_cache", torch.zeros((4, 2, 16, 64), dtype=torch.int8).transpose(2, 3)),
+         ("v_cache", torch.zeros((5, 2, 64, 16), dtype=torch.int8)), ("k_scale", torch.zeros((4, 2), dtype=torch.float64)),
+         ("v_scale", torch.zeros((4, 1))), ("v_scale", torch.zeros((2, 4)).t())]
+TABLES = [("page_table", i32(0, 1)), ("page_table", torch.zeros((1, 2), dtype=torch.int64)),
+          ("page_table", torch.zeros((4, 1), dtype=torch.int32).t()[:, ::2]), ("page_table", torch.zeros((2, 2), dtype=torch.int32)),
+          ("cu_new", i32(0)), ("cu_new", torch.tensor([0, 3])), ("lengths", i32(5, 5)), ("lengths", torch.tensor([5.0])),
+          ("lengths", [5])]
+
+
+@pytest.mark.parametrize("op,name,value", [
+    *(("kv_append", *b) for b in CACHE + TABLES), *(("attention", *b) for b in CACHE + TABLES),
+    *(("kv_dequant", *b) for b in CACHE), ("kv_dequant", "dtype", torch.int8),
+    ("kv_append", "k", torch.zeros((3, 3, 64))), ("kv_append", "k", torch.zeros((3, 2, 64), dtype=torch.float64)),
+    ("kv_append", "v", torch.zeros((2, 2, 64))), ("kv_append", "v", torch.zeros((3, 2, 64), dtype=torch.float16)),
+    ("kv_append", "k", torch.zeros((3, 64, 2)).transpose(1, 2)), ("kv_append", "q", torch.zeros((3, 5, 64))),
+    ("kv_append", "q", torch.zeros((2, 4, 64))), ("kv_append", "q_out", torch.zeros((3, 2, 64))),
+    ("kv_append", "inv_freq", torch.ones(33)), ("kv_append", "inv_freq", torch.ones(32, dtype=torch.float64)),
+    ("kv_append", "inv_freq", torch.ones(64)[::2]),
+    ("attention", "q", torch.zeros((3, 3, 64))), ("attention", "q", torch.zeros((3, 4, 32))),
+    ("attention", "q", torch.zeros((3, 4, 64), dtype=torch.int32)), ("attention", "q", torch.zeros((3, 256))),
+    ("attention", "out", torch.zeros((3, 4, 64), dtype=torch.float16)), ("attention", "out", torch.zeros((2, 4, 64))),
+    ("token_logprobs", "logits", torch.zeros(9)), ("token_logprobs", "logits", torch.zeros((9, 2)).t()),
+    ("token_logprobs", "logits", torch.zeros((2, 0))), ("token_logprobs", "logits", torch.zeros((2, 9), dtype=torch.int32)),
+    ("token_logprobs", "targets", torch.zeros(3, dtype=torch.int64)), ("token_logprobs", "targets", i32(0, 0)),
+    ("token_logprobs", "top_k", 10), ("token_logprobs", "top_k", -1), ("token_logprobs", "top_k", 33),
+    ("token_logprobs_backward", "lse", torch.zeros(3)), ("token_logprobs_backward", "entropy", torch.zeros(2).double()),
+    ("token_logprobs_backward", "g_logprob", torch.zeros((2, 1))), ("token_logprobs_backward", "g_entropy", torch.zeros(1)),
+    ("token_logprobs_backward", "dlogits", torch.zeros((2, 8))),
+    ("token_logprobs_backward", "dlogits", torch.zeros((2, 9), dtype=torch.float16))])
+def test_the_binding_refuses(op, name, value):
+    with pytest.raises(ValueError) as e:
+        getattr(q4, op)(**binding_args(op, **{name: value}))
+    assert "device tensor" not in str(e.value)
+
+
+def test_the_binding_refuses_q_out_without_q_and_cache_sizes():
+    with pytest.raises(ValueError, match="without q"):
+        q4.kv_append(**binding_args("kv_append", q=None, q_out=torch.zeros((3, 4, 64))))
     for page, dim in ((8, 64), (16, 40), (256, 64), (16, 272)):
         with pytest.raises(ValueError):
             q4.new_cache(4, 2, dim, page, device="cpu")
-    dev = torch.device("cpu")
-    for bad in ((cache[0][:, :, :8], *cache[1:]), (cache[0], cache[1].transpose(2, 3), *cache[2:]),
-                (cache[0].float(), *cache[1:]), (*cache[:2], cache[2].double(), cache[3]), (*cache[:3], cache[3][:2])):
-        with pytest.raises(ValueError):
-            serve._cache_sizes(*bad, dev)
-    for table, cu, ln in ((i(0), i(0, 1), i(1)), (i(0)[None], i(0, 1, 2), i(1)), (i(0)[None], i(0, 1), i(1, 2)),
-                          (i(0)[None].long(), i(0, 1), i(1)), (i(0)[None], i(0, 1).long(), i(1))):
-        with pytest.raises(ValueError):
-            serve._tables(table, cu, ln, dev)
-    with pytest.raises(ValueError):
-        serve._rows3(torch.zeros((2, 4, 64)).transpose(1, 2), "x", torch.float32, dev)
+
+
+def test_a_status_becomes_q4error():
+    """What the library refuses and the binding does not look at."""
+    with pytest.raises(q4.Q4Error) as e:
+        raise q4.Q4Error(3, "q4_attention")
+    assert e.value.status == 3
+
+
+def test_native_half_and_sources_have_to_match(monkeypatch):
+    monkeypatch.setattr(serve, "_module", None)
+    monkeypatch.setattr(serve._build, "source_digest", lambda: "0" * 64)
+    with pytest.raises(RuntimeError, match="does not match the sources"):
+        serve._native()
