@@ -2,12 +2,15 @@
 // keys and queries, and the export of a cache's values.
 //
 // One workgroup owns one page of one head for K or for V, since the page's
-// scale covers all of its tokens: it reads the new rows once (turning keys),
-// keeps them in LDS as fp32, takes their largest magnitude, and codes them
-// under the page's new scale, together with what the page held if the scale
-// grew.  The rest of the grid turns queries, one token each.  Bound by HBM
-// for prompts (each element is read once and written once), by the chain
-// table -> row -> maximum -> store for decode steps.
+// scale covers all of its tokens: it reads the new rows once into registers
+// (turning keys), takes their largest magnitude, and codes them under the
+// page's new scale, together with what the page held if the scale grew.  A
+// thread's share of K is 4 pairs of a token (dword stores of codes), of V 16
+// tokens of a column, so that neither passes through LDS: with the rows kept
+// there a prompt of 6000 tokens took 103 us, the turning of its queries, in
+// the rest of the grid, being held to the same 34 KB of LDS a workgroup.
+// Bound by HBM for prompts (each element is read and written once), by the
+// chain table -> row -> maximum -> store for decode steps.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -30,57 +33,156 @@ __device__ __forceinline__ void turn(int32_t pos, float inv_freq, float* c, floa
   sincospif(2.0f * frac, s, c);
 }
 
-// Elements of unit u (0 <= u < dim / 2): the pair that turns together, or
-// two neighbours past the turning part.
-__device__ __forceinline__ void unit_elems(int u, int half, bool interleaved, int* a, int* b) {
-  if (u < half && !interleaved) {
-    *a = u;
-    *b = u + half;
-  } else {
-    *a = 2 * u;
-    *b = 2 * u + 1;
-  }
+// Unit u of a row: pairs 4 u .. 4 u + 3.  Pair i < half turns: elements (i,
+// i + half), or (2 i, 2 i + 1) if interleaved; past half (2 i, 2 i + 1) stay.
+__device__ __forceinline__ void pair_elems(int i, int half, bool interleaved, int* a, int* b) {
+  const bool split = i < half && !interleaved;
+  *a = split ? i : 2 * i;
+  *b = split ? i + half : 2 * i + 1;
 }
 
+template <typename T, int N>
+__device__ __forceinline__ void load_vec(const T* p, T (&x)[N]) {
+  typedef uint32_t vec __attribute__((ext_vector_type(N * sizeof(T) / 4)));
+  const vec v = *(const vec*)p;
+  __builtin_memcpy(x, &v, sizeof v);
+}
+template <typename T, int N>
+__device__ __forceinline__ void store_vec(T* p, const T (&x)[N]) {
+  typedef uint32_t vec __attribute__((ext_vector_type(N * sizeof(T) / 4)));
+  vec v;
+  __builtin_memcpy(&v, x, sizeof v);
+  *(vec*)p = v;
+}
+
+// A unit's elements, x[2 i] and x[2 i + 1] of pair i.  vec: rows are 16-byte
+// aligned and rot a multiple of 8, so that a unit is 4 + 4 or 8 neighbours.
 template <typename T>
-__device__ __forceinline__ void turn_queries(const AppendParams& p, int32_t t) {
-  __shared__ float cs[256];  // cosines of the token, then sines
-  const KvCache& c = p.c;
-  // the sequence of token t: the last b with cu_new[b] <= t
-  int32_t lo = 0, hi = p.batch - 1;
-  while (lo < hi) {
-    const int32_t mid = (lo + hi + 1) >> 1;
-    if (c.cu_new[mid] <= t) lo = mid; else hi = mid - 1;
-  }
-  const SeqSpan sp = seq_span(c.cu_new, c.lengths, lo, p.T);
-  const int32_t pos = sp.pos0 + (t - sp.t0);
-  const int half = p.rot >> 1;
-  for (int i = threadIdx.x; i < half; i += kThreads) turn(pos, p.inv_freq[i], &cs[i], &cs[128 + i]);
-  __syncthreads();
-  const T* q = (const T*)p.q + (int64_t)t * p.q_ts;
-  T* o = (T*)p.q_out + (int64_t)t * p.qo_ts;
-  const int units = c.dim >> 1;
-  for (int i = threadIdx.x; i < p.heads * units; i += kThreads) {
-    const int h = i / units, u = i - h * units;
-    int ea, eb;
-    unit_elems(u, half, p.interleaved, &ea, &eb);
-    const T* src = q + h * p.q_hs;
-    T* dst = o + h * p.qo_hs;
-    const float a = to_f32(src[ea]), b = to_f32(src[eb]);
-    if (u < half) {
-      const float cc = cs[u], ss = cs[128 + u];
-      dst[ea] = from_f32<T>(a * cc - b * ss);
-      dst[eb] = from_f32<T>(b * cc + a * ss);
+__device__ __forceinline__ void load_unit(const T* row, int u, int half, bool interleaved, bool vec,
+                                          float (&x)[8]) {
+  if (vec && 4 * u < half && !interleaved) {
+    T a[4], b[4];
+    load_vec(row + 4 * u, a);
+    load_vec(row + 4 * u + half, b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[2 * i] = to_f32(a[i]);
+      x[2 * i + 1] = to_f32(b[i]);
+    }
+  } else if (vec) {
+    T a[8];
+    if constexpr (sizeof(T) == 2) {
+      load_vec(row + 8 * u, a);
     } else {
-      dst[ea] = src[ea];
-      dst[eb] = src[eb];
+      T lo[4], hi[4];
+      load_vec(row + 8 * u, lo);
+      load_vec(row + 8 * u + 4, hi);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a[i] = lo[i];
+        a[i + 4] = hi[i];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = to_f32(a[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      int ea, eb;
+      pair_elems(4 * u + i, half, interleaved, &ea, &eb);
+      x[2 * i] = to_f32(row[ea]);
+      x[2 * i + 1] = to_f32(row[eb]);
     }
   }
 }
 
-__device__ __forceinline__ int code_of(float x, float scale) {
+template <typename T>
+__device__ __forceinline__ void store_unit(T* row, int u, int half, bool interleaved, bool vec,
+                                           const float (&x)[8]) {
+  if (vec && 4 * u < half && !interleaved) {
+    T a[4], b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a[i] = from_f32<T>(x[2 * i]);
+      b[i] = from_f32<T>(x[2 * i + 1]);
+    }
+    store_vec(row + 4 * u, a);
+    store_vec(row + 4 * u + half, b);
+  } else if (vec) {
+    T lo[4], hi[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      lo[i] = from_f32<T>(x[i]);
+      hi[i] = from_f32<T>(x[i + 4]);
+    }
+    store_vec(row + 8 * u, lo);
+    store_vec(row + 8 * u + 4, hi);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      int ea, eb;
+      pair_elems(4 * u + i, half, interleaved, &ea, &eb);
+      row[ea] = from_f32<T>(x[2 * i]);
+      row[eb] = from_f32<T>(x[2 * i + 1]);
+    }
+  }
+}
+
+// Turns a unit; cs, sn: cosines and sines of its four pairs.
+__device__ __forceinline__ void turn_unit(float (&x)[8], const float* cs, const float* sn, int n) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i >= n) break;  // the turning part may end inside a unit
+    const float a = x[2 * i], b = x[2 * i + 1];
+    x[2 * i] = a * cs[i] - b * sn[i];
+    x[2 * i + 1] = b * cs[i] + a * sn[i];
+  }
+}
+
+// Queries of tokens t0 .. t0 + kTurn - 1, all heads.
+constexpr int kTurn = 4;
+
+template <typename T>
+__device__ __forceinline__ void turn_queries(const AppendParams& p, int64_t t0, int n) {
+  __shared__ float cs[kTurn][128], sn[kTurn][128];
+  __shared__ int32_t at[kTurn];
+  const KvCache& c = p.c;
+  const int half = p.rot >> 1;
+  if ((int)threadIdx.x < n) {
+    // the sequence of the token: the last b with cu_new[b] <= t
+    const int32_t t = (int32_t)t0 + threadIdx.x;
+    int32_t lo = 0, hi = p.batch - 1;
+    while (lo < hi) {
+      const int32_t mid = (lo + hi + 1) >> 1;
+      if (c.cu_new[mid] <= t) lo = mid; else hi = mid - 1;
+    }
+    const SeqSpan sp = seq_span(c.cu_new, c.lengths, lo, p.T);
+    at[threadIdx.x] = sp.pos0 + (t - sp.t0);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n * half; i += kThreads) {
+    const int k = i / half, f = i - k * half;
+    turn(at[k], p.inv_freq[f], &cs[k][f], &sn[k][f]);
+  }
+  __syncthreads();
+  const int units = c.dim >> 3, per_token = p.heads * units;
+  const T* q = (const T*)p.q;
+  T* o = (T*)p.q_out;
+  for (int k = 0; k < n; ++k) {
+#pragma unroll 2
+    for (int i = threadIdx.x; i < per_token; i += kThreads) {
+      const int h = i / units, u = i - h * units;
+      float x[8];
+      load_unit(q + (t0 + k) * p.q_ts + h * p.q_hs, u, half, p.interleaved, p.q_vec, x);
+      if (4 * u < half) turn_unit(x, &cs[k][4 * u], &sn[k][4 * u], half - 4 * u);
+      store_unit(o + (t0 + k) * p.qo_ts + h * p.qo_hs, u, half, p.interleaved, p.q_vec, x);
+    }
+  }
+}
+
+__device__ __forceinline__ uint32_t code_of(float x, float scale) {
   const float r = __builtin_rintf(x / scale);
-  return (int)fminf(fmaxf(r, -127.0f), 127.0f);
+  return (uint32_t)(int)fminf(fmaxf(r, -127.0f), 127.0f) & 0xffu;
 }
 
 // Four codes of a dword under a scale that grew by 1 / ratio.
@@ -94,14 +196,36 @@ __device__ __forceinline__ uint32_t recode(uint32_t w, float ratio) {
   return r;
 }
 
-template <typename T>
+// The page's scale, old and new, from the threads' largest magnitudes.
+struct Scale {
+  float now, ratio;
+  bool grew, zero;
+};
+
+__device__ __forceinline__ Scale grow_scale(float* at, uint32_t amax, bool fresh) {
+  __shared__ uint32_t wave_max[kThreads / 64];
+  const float old = fresh ? 0.0f : *at;
+  amax = wave_umax(amax);
+  if ((threadIdx.x & 63) == 0) wave_max[threadIdx.x >> 6] = amax;
+  __syncthreads();  // and every thread has read the old scale
+  amax = umax(umax(wave_max[0], wave_max[1]), umax(wave_max[2], wave_max[3]));
+  Scale s;
+  s.now = bits_f32(umax(f32_bits(old), f32_bits(bits_f32(amax) / 127.0f)));
+  s.grew = f32_bits(s.now) != f32_bits(old);
+  s.ratio = s.now > 0.0f ? old / s.now : 0.0f;
+  s.zero = s.now == 0.0f;
+  if (threadIdx.x == 0 && (s.grew || fresh)) *at = s.now;
+  return s;
+}
+
+// U: a thread's units of K, and half of its 16-token columns of V.
+template <typename T, int U>
 __global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendParams p) {
   if (blockIdx.x >= (uint32_t)p.cache_blocks) {
-    turn_queries<T>(p, (int32_t)(blockIdx.x - p.cache_blocks));
+    const int64_t t0 = (int64_t)(blockIdx.x - p.cache_blocks) * p.turn;
+    turn_queries<T>(p, t0, p.T - t0 < p.turn ? (int)(p.T - t0) : p.turn);
     return;
   }
-  extern __shared__ float rows[];  // new rows, fp32 [tokens][pitch]
-  __shared__ uint32_t wave_max[kThreads / 64];
   const KvCache& c = p.c;
   // workgroup -> (sequence, page, head, K or V)
   uint32_t id = blockIdx.x;
@@ -117,100 +241,149 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendParams p) {
   const int32_t pi = (first >> c.page_log2) + j;
   const int64_t base = (int64_t)pi << c.page_log2;
   const int o0 = first > base ? (int)(first - base) : 0;
-  // the rows in LDS are sized for max_new tokens
+  // of a sequence the first max_new are stored, as the launch is sized
   const int64_t end = (int64_t)first + p.max_new < sp.len ? (int64_t)first + p.max_new : sp.len;
   const int64_t left = end - base;
   const int o1 = left < c.page ? (int)left : c.page;
   if (sp.n <= 0 || o1 <= o0) return;
   const int32_t pid = page_at(c.table + b * c.table_ld, c.max_pages, c.pages, pi);
   if (pid < 0) return;
-  const int dim = c.dim, nt = o1 - o0;
-  // V is read from LDS along tokens: the odd pitch spreads those over banks
-  const int pitch = is_v ? dim + 1 : dim + 4;
-  const int32_t t0 = sp.t0 + (int32_t)(base + o0 - sp.pos0);  // token of slot o0
-  const T* src = is_v ? (const T*)p.v + h * p.v_hs : (const T*)p.k + h * p.k_hs;
-  const int64_t ts = is_v ? p.v_ts : p.k_ts;
-  const int half = is_v ? 0 : p.rot >> 1;
-  const int units = dim >> 1;
-  uint32_t amax = 0;
-  for (int i = threadIdx.x; i < nt * units; i += kThreads) {
-    const int t = i / units, u = i - t * units;
-    int ea, eb;
-    unit_elems(u, half, p.interleaved, &ea, &eb);
-    const T* row = src + (t0 + t) * ts;
-    float a = to_f32(row[ea]), bb = to_f32(row[eb]);
-    if (u < half) {
-      float cc, ss;
-      turn((int32_t)(base + o0 + t), p.inv_freq[u], &cc, &ss);
-      const float x = a * cc - bb * ss;
-      bb = bb * cc + a * ss;
-      a = x;
-    }
-    rows[t * pitch + ea] = a;
-    rows[t * pitch + eb] = bb;
-    amax = umax(amax, umax(abs_bits(a), abs_bits(bb)));
-  }
-  amax = wave_umax(amax);
-  if ((threadIdx.x & 63) == 0) wave_max[threadIdx.x >> 6] = amax;
-  __syncthreads();
-  amax = umax(umax(wave_max[0], wave_max[1]), umax(wave_max[2], wave_max[3]));
-  float* sc = (is_v ? c.vs : c.ks) + (int64_t)pid * c.heads + h;
+  const int dim = c.dim, tid = threadIdx.x;
+  const int64_t t0 = sp.t0 + (base + o0 - sp.pos0);  // token of slot o0
   const bool fresh = o0 == 0;
-  const float s_old = fresh ? 0.0f : *sc;
-  const float s_new = bits_f32(umax(f32_bits(s_old), f32_bits(bits_f32(amax) / 127.0f)));
-  const bool grew = f32_bits(s_new) != f32_bits(s_old);
-  const float ratio = s_new > 0.0f ? s_old / s_new : 0.0f;
-  const bool zero = s_new == 0.0f;
-  // every thread has read the old scale before one writes the new one
-  __syncthreads();
-  if (threadIdx.x == 0 && (grew || fresh)) *sc = s_new;
-  int8_t* cache = (is_v ? c.v : c.k) + ((int64_t)pid * c.heads + h) * ((int64_t)dim << c.page_log2);
+  const int64_t ph = (int64_t)pid * c.heads + h;
+  const int64_t at = ph * ((int64_t)dim << c.page_log2);
   if (!is_v) {
-    // 16 codes of one token per step; old rows only if the scale grew
-    const int chunks = dim >> 4;
-    const int lo = grew ? 0 : o0, hi = fresh ? c.page : o1;
-    for (int i = threadIdx.x; i < (hi - lo) * chunks; i += kThreads) {
-      const int r = i / chunks, ch = i - r * chunks, slot = lo + r;
-      u32x4v* dst = (u32x4v*)(cache + (int64_t)slot * dim + 16 * ch);
-      u32x4v w = {0, 0, 0, 0};
-      if (slot >= o0 && slot < o1) {
-        const float* x = &rows[(slot - o0) * pitch + 16 * ch];
+    const int units = dim >> 3, half = p.rot >> 1, n = (o1 - o0) * units;
+    const T* src = (const T*)p.k + h * p.k_hs;
+    float x[U][8];
+    int slot[U], unit[U];
+    uint32_t amax = 0;
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          w[e >> 2] |= ((uint32_t)(zero ? 0 : code_of(x[e], s_new)) & 0xffu) << (8 * (e & 3));
-      } else if (slot < o0) {
-        const u32x4v old = *dst;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) w[e] = recode(old[e], ratio);
+    for (int i = 0; i < U; ++i) {
+      const int w = i * kThreads + tid;
+      if (w < n) {
+        const int t = w / units;
+        unit[i] = w - t * units;
+        slot[i] = o0 + t;
+        load_unit(src + (t0 + t) * p.k_ts, unit[i], half, p.interleaved, p.k_vec, x[i]);
       }
-      *dst = w;
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (i * kThreads + tid < n) {
+        const int u = unit[i];
+        float cs[4], sn[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (4 * u + e < half) turn((int32_t)(base + slot[i]), p.inv_freq[4 * u + e], &cs[e], &sn[e]);
+        turn_unit(x[i], cs, sn, half - 4 * u);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) amax = umax(amax, abs_bits(x[i][e]));
+      }
+    }
+    const Scale s = grow_scale(c.ks + ph, amax, fresh);
+    int8_t* cache = c.k + at;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      if (i * kThreads + tid < n) {
+        int8_t* row = cache + (int64_t)slot[i] * dim;
+        const int u = unit[i];
+        uint32_t q[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) q[e] = s.zero ? 0u : code_of(x[i][e], s.now);
+        if (p.rot % 8 == 0 && 4 * u < half && !p.interleaved) {
+          *(uint32_t*)(row + 4 * u) = q[0] | q[2] << 8 | q[4] << 16 | q[6] << 24;
+          *(uint32_t*)(row + 4 * u + half) = q[1] | q[3] << 8 | q[5] << 16 | q[7] << 24;
+        } else if (p.rot % 8 == 0) {
+          *(u32x2*)(row + 8 * u) = u32x2{q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24,
+                                         q[4] | q[5] << 8 | q[6] << 16 | q[7] << 24};
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            int ea, eb;
+            pair_elems(4 * u + e, half, p.interleaved, &ea, &eb);
+            row[ea] = (int8_t)q[2 * e];
+            row[eb] = (int8_t)q[2 * e + 1];
+          }
+        }
+      }
+    }
+    // the rest of the page, 16 codes a step: 0 if it starts anew, coded anew
+    // if the scale grew
+    const int chunks = dim >> 4;
+    if (fresh) {
+      for (int i = o1 * chunks + tid; i < chunks << c.page_log2; i += kThreads)
+        ((u32x4v*)cache)[i] = u32x4v{0, 0, 0, 0};
+    } else if (s.grew) {
+      for (int i = tid; i < o0 * chunks; i += kThreads) {
+        u32x4v w = ((u32x4v*)cache)[i];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) w[e] = recode(w[e], s.ratio);
+        ((u32x4v*)cache)[i] = w;
+      }
     }
   } else {
-    // 16 tokens of one column per step; a step that mixes old and new slots
-    // keeps the old ones' bytes
-    const int c_lo = grew ? 0 : o0 >> 4, c_hi = fresh ? c.page >> 4 : (o1 + 15) >> 4;
-    const int n = c_hi - c_lo;
-    for (int i = threadIdx.x; i < n * dim; i += kThreads) {
-      const int d = i / n, ch = c_lo + (i - d * n);
-      u32x4v* dst = (u32x4v*)(cache + ((int64_t)d << c.page_log2) + 16 * ch);
-      u32x4v w = {0, 0, 0, 0};
-      if (16 * ch < o0 || (16 * ch + 16 > o1 && !fresh)) {
-        w = *dst;
-        if (grew) {
+    // 16 slots of a column: those from o0's on; loads of a wave run along
+    // the columns, a row each
+    constexpr int J = (U + 1) / 2;
+    const int c_lo = o0 >> 4, c_hi = (o1 + 15) >> 4, n = (c_hi - c_lo) * dim;
+    const T* src = (const T*)p.v + h * p.v_hs;
+    T x[J][16];
+    uint32_t amax = 0;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = recode(w[e], ratio);
-        }
-      }
+    for (int i = 0; i < J; ++i) {
+      const int w = i * kThreads + tid, ch = w / dim, d = w - ch * dim, s0 = 16 * (c_lo + ch);
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const int slot = 16 * ch + e;
-        if (slot >= o0 && slot < o1) {
-          const int code = zero ? 0 : code_of(rows[(slot - o0) * pitch + d], s_new);
-          const uint32_t m = 0xffu << (8 * (e & 3));
-          w[e >> 2] = (w[e >> 2] & ~m) | (((uint32_t)code << (8 * (e & 3))) & m);
+        x[i][e] = (T)0.0f;
+        if (w < n && s0 + e >= o0 && s0 + e < o1) x[i][e] = src[(t0 + (s0 + e - o0)) * p.v_ts + d];
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < J; ++i)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) amax = umax(amax, abs_bits(to_f32(x[i][e])));
+    const Scale s = grow_scale(c.vs + ph, amax, fresh);
+    int8_t* cache = c.v + at;
+#pragma unroll
+    for (int i = 0; i < J; ++i) {
+      const int w = i * kThreads + tid;
+      if (w >= n) continue;
+      const int ch = w / dim, d = w - ch * dim, s0 = 16 * (c_lo + ch);
+      u32x4v* dst = (u32x4v*)(cache + ((int64_t)d << c.page_log2) + s0);
+      u32x4v q = {0, 0, 0, 0};
+      // the old slots of a column that also has new ones keep their codes
+      if (s0 < o0 || (s0 + 16 > o1 && !fresh)) {
+        q = *dst;
+        if (s.grew) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) q[e] = recode(q[e], s.ratio);
         }
       }
-      *dst = w;
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
+        if (s0 + e >= o0 && s0 + e < o1) {
+          const uint32_t code = s.zero ? 0u : code_of(to_f32(x[i][e]), s.now);
+          q[e >> 2] = (q[e >> 2] & ~(0xffu << (8 * (e & 3)))) | code << (8 * (e & 3));
+        }
+      *dst = q;
+    }
+    if (fresh) {
+      const int rest = (c.page >> 4) - c_hi;
+      for (int i = tid; i < rest * dim; i += kThreads) {
+        const int ch = i / dim, d = i - ch * dim;
+        *(u32x4v*)(cache + ((int64_t)d << c.page_log2) + 16 * (c_hi + ch)) = u32x4v{0, 0, 0, 0};
+      }
+    } else if (s.grew) {
+      for (int i = tid; i < c_lo * dim; i += kThreads) {
+        const int ch = i / dim, d = i - ch * dim;
+        u32x4v* dst = (u32x4v*)(cache + ((int64_t)d << c.page_log2) + 16 * ch);
+        u32x4v q = *dst;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) q[e] = recode(q[e], s.ratio);
+        *dst = q;
+      }
     }
   }
 }
@@ -265,29 +438,41 @@ __global__ __launch_bounds__(kThreads) void kv_dequant_kernel(KvCache c, T* __re
 
 }  // namespace
 
+template <typename T>
+static hipError_t launch_append(const AppendParams& p, int64_t rows, dim3 grid, hipStream_t s) {
+  // K units of a page's new rows over the threads; V's 16-token columns may
+  // begin and end inside the rows, so that they can be one more than the rows
+  // fill: rows + 15 bounds their tokens
+  const int64_t page = p.c.page;
+  const int64_t k_units = rows * (p.c.dim / 8);
+  const int64_t v_cols = ((rows + 15 + 15) / 16 < page / 16 ? (rows + 15 + 15) / 16 : page / 16) * p.c.dim;
+  const int64_t need_k = (k_units + kThreads - 1) / kThreads;
+  const int64_t need_v = 2 * ((v_cols + kThreads - 1) / kThreads);
+  const int64_t u = need_k > need_v ? need_k : need_v;
+  if (u <= 2)
+    hipLaunchKernelGGL((kv_append_kernel<T, 2>), grid, dim3(kThreads), 0, s, p);
+  else if (u <= 4)
+    hipLaunchKernelGGL((kv_append_kernel<T, 4>), grid, dim3(kThreads), 0, s, p);
+  else if (u <= 8)
+    hipLaunchKernelGGL((kv_append_kernel<T, 8>), grid, dim3(kThreads), 0, s, p);
+  else
+    hipLaunchKernelGGL((kv_append_kernel<T, 16>), grid, dim3(kThreads), 0, s, p);
+  return hipGetLastError();
+}
+
 hipError_t launch_kv_append(const AppendParams& in, int32_t dtype, int64_t max_new,
                             hipStream_t s) {
   AppendParams p = in;
   p.max_new = max_new;
   p.touched = (int32_t)pages_touched(max_new, p.c.page);
   p.cache_blocks = (int32_t)((int64_t)p.batch * p.touched * p.c.heads * 2);
+  // a workgroup per token while that leaves CUs without work
+  p.turn = p.T >= 2048 ? kTurn : 1;
   const int64_t rows = max_new < p.c.page ? max_new : p.c.page;
-  const size_t lds = (size_t)rows * (p.c.dim + 4) * sizeof(float);
-  const dim3 grid((unsigned)(p.cache_blocks + (p.q ? p.T : 0)));
-#define Q4_APPEND(T)                                                                            \
-  do {                                                                                          \
-    if (lds > 65536) {                                                                          \
-      const hipError_t e = hipFuncSetAttribute(                                                 \
-          (const void*)kv_append_kernel<T>, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds); \
-      if (e != hipSuccess) return e;                                                            \
-    }                                                                                           \
-    hipLaunchKernelGGL((kv_append_kernel<T>), grid, dim3(kThreads), lds, s, p);                 \
-  } while (0)
-  if (dtype == Q4_DTYPE_F32) Q4_APPEND(float);
-  else if (dtype == Q4_DTYPE_F16) Q4_APPEND(_Float16);
-  else Q4_APPEND(bf16);
-#undef Q4_APPEND
-  return hipGetLastError();
+  const dim3 grid((unsigned)(p.cache_blocks + (p.q ? (p.T + p.turn - 1) / p.turn : 0)));
+  if (dtype == Q4_DTYPE_F32) return launch_append<float>(p, rows, grid, s);
+  if (dtype == Q4_DTYPE_F16) return launch_append<_Float16>(p, rows, grid, s);
+  return launch_append<bf16>(p, rows, grid, s);
 }
 
 hipError_t launch_kv_dequant(const KvCache& c, int32_t dtype, void* k, void* v, hipStream_t s) {

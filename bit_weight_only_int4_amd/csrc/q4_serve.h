@@ -36,7 +36,9 @@ struct AppendParams {
   const float* inv_freq;
   int32_t rot, interleaved;
   int32_t touched;       // pages of one sequence that the launch covers
-  int32_t cache_blocks;  // workgroups that store; the rest turn queries
+  int32_t cache_blocks;  // workgroups that store; the rest turn queries,
+  int32_t turn;          // so many tokens each
+  int32_t k_vec, q_vec;  // rows of k, and of q and q_out, allow vector accesses
 };
 
 hipError_t launch_kv_append(const AppendParams& p, int32_t dtype, int64_t max_new, hipStream_t s);

@@ -167,6 +167,11 @@ q4_status q4_kv_append(const void* k, int64_t k_ts, int64_t k_hs, const void* v,
   p.inv_freq = inv_freq;
   p.rot = (int32_t)rot;
   p.interleaved = interleaved;
+  auto vec = [&](const void* x, int64_t ts, int64_t hs) {
+    return aligned(x, 16) && ts * e % 16 == 0 && hs * e % 16 == 0 && rot % 8 == 0;
+  };
+  p.k_vec = vec(k, k_ts, k_hs);
+  p.q_vec = q && vec(q, q_ts, q_hs) && vec(q_out, qo_ts, qo_hs);
   return status_of(q4::launch_kv_append(p, dtype, max_new, (hipStream_t)stream));
 }
 
