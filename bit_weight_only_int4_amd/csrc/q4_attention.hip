@@ -1,5 +1,5 @@
 // q4_attention.hip -- plan and launch of attention over the paged cache.
-#include "q4_attention_kernels.h"
+#include "q4_attention_wide.h"
 
 namespace q4 {
 
@@ -66,7 +66,7 @@ __device__ __forceinline__ void join_row(const AttnParams& p, int n, int64_t at,
 __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnParams p) {
   const int64_t rr = blockIdx.x % p.max_rows;
   const uint32_t bh = blockIdx.x / p.max_rows;
-  const Block k = block_of(p, bh / p.c.heads, bh % p.c.heads, (int)(rr / kRows));
+  const Block k = block_of(p, bh / p.c.heads, bh % p.c.heads, (int)(rr / p.block_rows));
   if (rr >= k.rows) return;
   const int n = (k.tiles + p.split_tiles - 1) / p.split_tiles;
   if (n <= 1) return;
@@ -107,6 +107,9 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Which kernel, and how much of it.
 //
+// Sequences that may bring kWideMin rows to a kv head run the wide kernel,
+// whose workgroups share keys and values between 128 of them.
+//
 // Rows of many keys run the stream kernel, whose waves share all keys evenly:
 // where a unit has at least kStreamTiles tiles by max_len, units are few enough
 // for their running sum in LDS, and the line's length fits 32 bits.  Below,
@@ -120,21 +123,23 @@ AttnPlan plan_attention(int32_t dtype, int64_t T, int64_t batch, int64_t heads, 
                         int64_t window) {
   (void)dtype;
   (void)page;
-  constexpr int64_t kTargetBlocks = 1024, kMinTiles = 16, kStreamTiles = 32;
-  constexpr int64_t kStreamUnits = 8192, kStreamWaves = 2048;
+  constexpr int64_t kTargetBlocks = 1024, kWideTarget = 512, kMinTiles = 16, kStreamTiles = 32;
+  constexpr int64_t kStreamUnits = 8192, kStreamWaves = 2048, kWideMin = 64;
   AttnPlan pl{};
   const int64_t group = heads / kv_heads;
+  const bool wide = max_new * group >= kWideMin;
   pl.max_rows = (int32_t)(max_new * group);
-  pl.row_blocks = (int32_t)ceil_div(max_new * group, attn::kRows);
-  // a block's queries span at most kRows positions
+  pl.block_rows = wide ? attn::kWideRows : attn::kRows;
+  pl.row_blocks = (int32_t)ceil_div(max_new * group, pl.block_rows);
+  // a block's queries span at most block_rows positions
   int64_t span = max_len;
-  if (window > 0 && window + attn::kRows < span) span = window + attn::kRows;
+  if (window > 0 && window + pl.block_rows < span) span = window + pl.block_rows;
   int64_t tiles = ceil_div(span, attn::kTile) + (window > 0 ? 1 : 0);
   if (tiles < 1) tiles = 1;
   const int64_t units = batch * pl.row_blocks, blocks = units * kv_heads;
   pl.splits = 1;
   pl.split_tiles = (int32_t)tiles;
-  if (tiles >= kStreamTiles && pl.row_blocks <= 2 && units <= kStreamUnits &&
+  if (!wide && tiles >= kStreamTiles && pl.row_blocks <= 2 && units <= kStreamUnits &&
       (double)tiles * (double)blocks < 1073741824.0) {
     int64_t waves = ceil_div(tiles * blocks, attn::kMinPiece);
     if (waves > kStreamWaves) waves = kStreamWaves;
@@ -143,7 +148,7 @@ AttnPlan plan_attention(int32_t dtype, int64_t T, int64_t batch, int64_t heads, 
     pl.workspace = pl.parts * (size_t)(dim + 2) * sizeof(float) + (size_t)(1 + blocks) * sizeof(int32_t);
     return pl;
   }
-  int64_t splits = ceil_div(kTargetBlocks, blocks > 0 ? blocks : 1);
+  int64_t splits = ceil_div(wide ? kWideTarget : kTargetBlocks, blocks > 0 ? blocks : 1);
   if (splits > tiles / kMinTiles) splits = tiles / kMinTiles;
   if (splits < 1) splits = 1;
   pl.split_tiles = (int32_t)ceil_div(tiles, splits);

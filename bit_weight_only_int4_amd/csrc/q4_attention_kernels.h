@@ -116,8 +116,8 @@ __device__ __forceinline__ Block block_of(const AttnParams& p, int b, int h, int
   k.b = b;
   k.sp = seq_span(p.c.cu_new, p.c.lengths, k.b, p.T);
   k.rows = (int64_t)k.sp.n * p.group;
-  k.row0 = (int64_t)rb * kRows;
-  const int64_t last = k.row0 + kRows < k.rows ? k.row0 + kRows : k.rows;
+  k.row0 = (int64_t)rb * p.block_rows;
+  const int64_t last = k.row0 + p.block_rows < k.rows ? k.row0 + p.block_rows : k.rows;
   k.keys = key_range(k.sp.pos0 + k.row0 / p.group, k.sp.pos0 + (last - 1) / p.group, p.window,
                      p.max_len);
   k.tile0 = (int)(k.keys.lo / kTile);

@@ -2,7 +2,7 @@
 // included by q4_attention_d2.hip and q4_attention_d3.hip.
 #pragma once
 
-#include "q4_attention_kernels.h"
+#include "q4_attention_wide.h"
 
 namespace q4 {
 
@@ -13,6 +13,12 @@ static hipError_t launch_attention_pages(const AttnParams& p, hipStream_t s) {
     const size_t bytes = (size_t)p.batch * p.row_blocks * sizeof(int32_t);
     hipLaunchKernelGGL((attention_stream_kernel<DT, ND, UNIFORM>),
                        dim3((unsigned)(p.stream_waves / kWaves)), dim3(kThreads), bytes, s, p);
+    return hipGetLastError();
+  }
+  if (p.block_rows == kWideRows) {
+    const size_t bytes = (size_t)2 * (4 * ((DT + 3) / 4) + DT) * 1024;
+    const dim3 grid((unsigned)((int64_t)p.batch * p.c.heads * p.row_blocks * p.splits));
+    hipLaunchKernelGGL((attention_wide_kernel<DT, ND, UNIFORM>), grid, dim3(kThreads), bytes, s, p);
     return hipGetLastError();
   }
   const size_t lds = (size_t)(kWaves * kRows * (16 * DT + 4) + 2 * kWaves * kRows) * sizeof(float);

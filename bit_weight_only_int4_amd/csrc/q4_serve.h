@@ -55,6 +55,7 @@ struct AttnParams {
   float scale_log2;             // scale * log2(e)
   int32_t q_vec;                // 16-byte aligned query rows
   int32_t max_rows;             // per sequence and kv head
+  int32_t block_rows;           // query rows of a workgroup: 16, or 128 (attention_wide_kernel)
   int32_t row_blocks;           // per sequence and kv head
   int32_t splits;               // workgroups along the keys (grid)
   int32_t split_tiles;          // tiles of 64 keys each of them takes
@@ -67,7 +68,7 @@ struct AttnParams {
 };
 
 struct AttnPlan {
-  int32_t max_rows, row_blocks, splits, split_tiles, stream_waves;
+  int32_t max_rows, block_rows, row_blocks, splits, split_tiles, stream_waves;
   size_t parts;  // rows of partial outputs in the workspace
   size_t workspace;
 };

@@ -293,6 +293,7 @@ q4_status q4_attention(const void* q, int64_t q_ts, int64_t q_hs, void* out, int
   p.scale_log2 = scale * 1.4426950408889634f;
   p.q_vec = aligned(q, 16) && q_ts * e % 16 == 0 && q_hs * e % 16 == 0;
   p.max_rows = pl.max_rows;
+  p.block_rows = pl.block_rows;
   p.row_blocks = pl.row_blocks;
   p.splits = pl.splits;
   p.split_tiles = pl.split_tiles;

@@ -109,6 +109,38 @@ def test_many_new_tokens(page, dtype):
     check([97, 200], [600, 201], 4, 1, 128, page, dtype, seed=12, window=150)
 
 
+@pytest.mark.parametrize("dim", [16, 48, 64, 80, 96, 128, 144, 192, 256])
+@pytest.mark.parametrize("page,dtype", [(16, "f32"), (64, "f16"), (128, "f32"), (32, "bf16")])
+def test_chunks_of_all_head_sizes(dim, page, dtype):
+    check([33, 70, 1], [33, 400, 90], 4, 2, dim, page, dtype, seed=dim, layout="fused")
+
+
+@pytest.mark.parametrize("window", [1, 40, 64, 129, 1000])
+@pytest.mark.parametrize("page", [16, 64])
+def test_chunks_under_windows(window, page):
+    check([150, 64, 3, 0], [700, 64, 200, 10], 3, 1, 64, page, "f32", window=window, seed=window)
+
+
+@pytest.mark.parametrize("heads,kv_heads", [(1, 1), (5, 1), (32, 8), (130, 1)])
+def test_chunks_of_head_groups(heads, kv_heads):
+    check([65, 129, 2], [80, 300, 2], heads, kv_heads, 32, 64, "f16", seed=heads)
+
+
+def test_chunks_over_long_contexts_are_split():
+    check([40, 7], [5000, 2100], 8, 2, 128, 64, "bf16", seed=1)
+    check([40, 7], [5000, 2100], 8, 2, 64, 16, "f32", seed=2, window=3000)
+    check([20, 5], [40, 2100], 8, 2, 64, 16, "f32", seed=3, max_len=100000)
+
+
+def test_chunks_with_scores_and_scales_far_apart():
+    check([100, 30], [400, 70], 4, 2, 64, 64, "f32", q_gain=40.0, seed=8)
+    check([100, 30], [400, 70], 4, 2, 64, 64, "bf16", q_gain=40.0, seed=8)
+    check([100, 30], [400, 70], 4, 2, 64, 64, "f32", scale=0.0, seed=9)
+    check([100, 30], [400, 70], 4, 2, 64, 64, "f32", scale=-0.3, seed=10)
+    check([100, 30], [400, 70], 4, 2, 64, 16, "f32", spread=3.0, seed=11)
+    check([100, 30], [400, 70], 4, 2, 64, 128, "f32", spread=3.0, seed=12)
+
+
 def test_empty_sequences_and_queries_before_the_start():
     # length 0 (queries see nothing), no new tokens, more new tokens than the length
     got, ref, tol = run([1, 0, 3, 2, 0], [0, 50, 2, 40, 0], 4, 2, 64, 16, "f32")
