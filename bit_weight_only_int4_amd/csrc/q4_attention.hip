@@ -62,17 +62,39 @@ __device__ __forceinline__ void join_row(const AttnParams& p, int n, int64_t at,
   store_elem(p.out, out + tid, total == 0.0f ? 0.0f : o / total, p.dtype);
 }
 
-// One query row of the blocks that have more than one split.
+// The blocks that have more than one split: dim / 4 threads a query row, so
+// that many rows with few parts share a workgroup.
 __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnParams p) {
-  const int64_t rr = blockIdx.x % p.max_rows;
-  const uint32_t bh = blockIdx.x / p.max_rows;
+  const int quads = p.c.dim >> 2, at_once = kThreads / quads;
+  const int mine = threadIdx.x / quads, d = 4 * (threadIdx.x - mine * quads);
+  const int per_bh = (p.max_rows + at_once - 1) / at_once;
+  const int64_t rr = (int64_t)(blockIdx.x % per_bh) * at_once + mine;
+  const uint32_t bh = blockIdx.x / per_bh;
+  if (mine >= at_once || rr >= p.max_rows) return;
   const Block k = block_of(p, bh / p.c.heads, bh % p.c.heads, (int)(rr / p.block_rows));
   if (rr >= k.rows) return;
   const int n = (k.tiles + p.split_tiles - 1) / p.split_tiles;
   if (n <= 1) return;
   const int64_t tk = rr / p.group;
   const int64_t tq = k.sp.t0 + tk, hq = k.h * p.group + (rr - tk * p.group);
-  join_row(p, n, tq * p.heads + hq, p.T * p.heads, tq * p.o_ts + hq * p.o_hs, p.splits);
+  const int64_t at = tq * p.heads + hq, stride = p.T * p.heads;
+  float m = -__builtin_inff();
+#pragma unroll 4
+  for (int s = 0; s < n; ++s) m = fmaxf(m, p.part_ml[2 * (at + s * stride)]);
+  const float ref = m > -__builtin_inff() ? m : 0.0f;
+  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+  float den = 0.0f;
+#pragma unroll 4
+  for (int s = 0; s < n; ++s) {
+    const int64_t a = at + s * stride;
+    const float f = exp2_fast(p.part_ml[2 * a] - ref), ds = p.part_ml[2 * a + 1];
+    den += ds != ds ? ds : f * ds;  // a part without a maximum: 0, or NaN
+    acc += f * *(const f32x4*)&p.part_o[a * p.c.dim + d];
+  }
+  const float inv = den == 0.0f ? 0.0f : 1.0f / den;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    store_elem(p.out, tq * p.o_ts + hq * p.o_hs + d + e, acc[e] * inv, p.dtype);
 }
 
 // One query row of the units whose tiles several waves had; zeros for those
@@ -107,8 +129,14 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Which kernel, and how much of it.
 //
-// Sequences that may bring kWideMin rows to a kv head run the wide kernel,
-// whose workgroups share keys and values between 128 of them.
+// Where sequences may bring kWideMin rows to a kv head, and there are kWideAll
+// in all, the wide kernel, whose workgroups share keys and values between 128
+// rows, or 64 where those would leave CUs without a workgroup.  Below, its
+// barriers and part-filled blocks cost more than the sharing gives (8
+// sequences over 2000 to 4000 tokens, 32 query and 8 kv heads of 128: with 64
+// rows of each kv head 43.9 us against 38.7 of 16-row workgroups in bf16 and
+// 47.9 against 40.2 in fp32, with 128 52.6 against 57.6 and 63.8 against 61.2,
+// with 192 54.7 against 80.6 and 64.5 against 85.2).
 //
 // Rows of many keys run the stream kernel, whose waves share all keys evenly:
 // where a unit has at least kStreamTiles tiles by max_len, units are few enough
@@ -124,12 +152,14 @@ AttnPlan plan_attention(int32_t dtype, int64_t T, int64_t batch, int64_t heads, 
   (void)dtype;
   (void)page;
   constexpr int64_t kTargetBlocks = 1024, kWideTarget = 512, kMinTiles = 16, kStreamTiles = 32;
-  constexpr int64_t kStreamUnits = 8192, kStreamWaves = 2048, kWideMin = 64;
+  constexpr int64_t kStreamUnits = 8192, kStreamWaves = 2048, kWideMin = 96, kWideAll = 8192;
   AttnPlan pl{};
   const int64_t group = heads / kv_heads;
-  const bool wide = max_new * group >= kWideMin;
+  const bool wide = max_new * group >= kWideMin && batch * kv_heads * max_new * group >= kWideAll;
   pl.max_rows = (int32_t)(max_new * group);
-  pl.block_rows = wide ? attn::kWideRows : attn::kRows;
+  constexpr int kBlock = attn::kWaves * attn::kRows;
+  const bool large = batch * kv_heads * ceil_div(max_new * group, 2 * kBlock) >= 512;
+  pl.block_rows = !wide ? attn::kRows : large ? 2 * kBlock : kBlock;
   pl.row_blocks = (int32_t)ceil_div(max_new * group, pl.block_rows);
   // a block's queries span at most block_rows positions
   int64_t span = max_len;
@@ -162,13 +192,16 @@ hipError_t launch_attention(const AttnParams& p, hipStream_t s) {
   const hipError_t e = p.dtype == Q4_DTYPE_F32 ? launch_attention_digits<3>(p, s)
                                                : launch_attention_digits<2>(p, s);
   if (e != hipSuccess || (p.splits <= 1 && !p.stream_waves)) return e;
-  const dim3 grid((unsigned)((int64_t)p.batch * p.c.heads * p.max_rows));
-  const int32_t most = p.stream_waves ? p.stream_waves : p.splits;
-  const size_t lds = (most + (size_t)(attn::kThreads / (p.c.dim / 4)) * p.c.dim) * sizeof(float);
-  if (p.stream_waves)
-    hipLaunchKernelGGL(attn::attention_stream_join_kernel, grid, dim3(attn::kThreads), lds, s, p);
-  else
-    hipLaunchKernelGGL(attn::attention_join_kernel, grid, dim3(attn::kThreads), lds, s, p);
+  const int64_t bh = (int64_t)p.batch * p.c.heads, at_once = attn::kThreads / (p.c.dim / 4);
+  if (p.stream_waves) {
+    const size_t lds = (p.stream_waves + (size_t)at_once * p.c.dim) * sizeof(float);
+    hipLaunchKernelGGL(attn::attention_stream_join_kernel, dim3((unsigned)(bh * p.max_rows)),
+                       dim3(attn::kThreads), lds, s, p);
+  } else {
+    hipLaunchKernelGGL(attn::attention_join_kernel,
+                       dim3((unsigned)(bh * ((p.max_rows + at_once - 1) / at_once))),
+                       dim3(attn::kThreads), 0, s, p);
+  }
   return hipGetLastError();
 }
 

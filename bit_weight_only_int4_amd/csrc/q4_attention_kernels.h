@@ -76,18 +76,27 @@ __device__ __forceinline__ float join_digits(const int32_t (&a)[ND]) {
   return low;
 }
 
-// Over the four lanes that hold a column.
+// Over the four lanes that hold a column, l % 16 apart: the rows of 16 lanes
+// change places in pairs, then the halves.
+template <typename F>
+__device__ __forceinline__ uint32_t column_fold(uint32_t x, F f) {
+  auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+  x = f(r[0], r[1]);
+  r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  return f(r[0], r[1]);
+}
 __device__ __forceinline__ float column_max(float x) {
-  x = fmaxf(x, __shfl_xor(x, 16, 64));
-  return fmaxf(x, __shfl_xor(x, 32, 64));
+  return bits_f32(column_fold(f32_bits(x), [](uint32_t a, uint32_t b) {
+    return f32_bits(fmaxf(bits_f32(a), bits_f32(b)));
+  }));
 }
 __device__ __forceinline__ float column_sum(float x) {
-  x += __shfl_xor(x, 16, 64);
-  return x + __shfl_xor(x, 32, 64);
+  return bits_f32(column_fold(f32_bits(x), [](uint32_t a, uint32_t b) {
+    return f32_bits(bits_f32(a) + bits_f32(b));
+  }));
 }
 __device__ __forceinline__ uint32_t column_umax(uint32_t x) {
-  x = umax(x, (uint32_t)__shfl_xor((int)x, 16, 64));
-  return umax(x, (uint32_t)__shfl_xor((int)x, 32, 64));
+  return column_fold(x, [](uint32_t a, uint32_t b) { return umax(a, b); });
 }
 
 __device__ __forceinline__ float load_elem(const void* p, int64_t i, int32_t dtype) {

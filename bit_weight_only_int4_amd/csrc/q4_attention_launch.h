@@ -15,10 +15,17 @@ static hipError_t launch_attention_pages(const AttnParams& p, hipStream_t s) {
                        dim3((unsigned)(p.stream_waves / kWaves)), dim3(kThreads), bytes, s, p);
     return hipGetLastError();
   }
-  if (p.block_rows == kWideRows) {
-    const size_t bytes = (size_t)2 * (4 * ((DT + 3) / 4) + DT) * 1024;
+  if (p.block_rows > kRows) {
+    const size_t bytes = (size_t)4 * (4 * ((DT + 3) / 4) + DT) * 1024;
     const dim3 grid((unsigned)((int64_t)p.batch * p.c.heads * p.row_blocks * p.splits));
-    hipLaunchKernelGGL((attention_wide_kernel<DT, ND, UNIFORM>), grid, dim3(kThreads), bytes, s, p);
+    const auto run = p.block_rows == 2 * kWaves * kRows ? attention_wide_kernel<DT, ND, 2, UNIFORM>
+                                                        : attention_wide_kernel<DT, ND, 1, UNIFORM>;
+    if (bytes > 65536) {
+      const hipError_t e = hipFuncSetAttribute(
+          (const void*)run, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+      if (e != hipSuccess) return e;
+    }
+    hipLaunchKernelGGL(run, grid, dim3(kThreads), bytes, s, p);
     return hipGetLastError();
   }
   const size_t lds = (size_t)(kWaves * kRows * (16 * DT + 4) + 2 * kWaves * kRows) * sizeof(float);

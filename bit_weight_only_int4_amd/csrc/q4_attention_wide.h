@@ -2,18 +2,20 @@
 // of a prompt) over the paged 8-bit cache.
 //
 // The mathematics and the operand layouts are those of
-// q4_attention_kernels.h.  Here a workgroup holds 128 rows of a kv head, 32 in
-// each of its four waves, and all of them read a tile's keys and values from
-// LDS, where global loads have put them directly, 1 KB to an operand of 16
-// rows and 64 columns in the order of the lanes that read it (so that neither
-// side has a bank conflict).  Two buffers: the next tile loads while one is
-// worked on, with one barrier a tile.
+// q4_attention_kernels.h.  Here a workgroup holds 128 (or 64) rows of a kv
+// head, 32 (16) in each of its four waves, and all of them read the keys and
+// values of two tiles at a time from LDS, where global loads have put them
+// directly, 1 KB to an operand of 16 rows and 64 columns in the order of the
+// lanes that read it (so that neither side has a bank conflict).  Two buffers:
+// the next pair of tiles loads while one is worked on, with one barrier a pair.
 //
-// Bound by the vector unit: a score takes 11 issue slots (4 of them the
-// exponential) and an output element 3 a tile, together 1200 cycles for 16
-// rows and 64 tokens of a head of 128, where the matrix unit needs 512 (two
-// digits).  What keeps them few:
+// Bound by the vector unit: with two digits a score takes 11 issue slots (4 of
+// them the exponential) and an output element 3 a pair of tiles, where the
+// matrix unit needs half their time.  What keeps them few:
 //   * with two digits scores stay integers until the maximum is known;
+//   * two tiles share a maximum and their outputs' way from integers to fp32
+//     (one tile at a time took 1398 us where this takes 1277: 4 x 2048 tokens
+//     over 8192 each, 32 query and 8 kv heads of 128, bf16);
 //   * the running maximum is only a reference that keeps the exponentials in
 //     range: outputs are rescaled when a row's maximum passes it by 2^8, not
 //     at every new maximum;
@@ -25,8 +27,6 @@
 namespace q4 {
 namespace attn {
 
-constexpr int kColumns = 2;                              // 16-row blocks of a wave
-constexpr int kWideRows = kWaves * kColumns * kRows;     // 128
 constexpr float kSlack = 8.0f;                           // log2 that a maximum may pass the reference by
 
 typedef __attribute__((address_space(3))) void* lds_ptr;
@@ -49,40 +49,57 @@ __device__ __forceinline__ typename Raw<ND>::type raw_join(const int32_t (&a)[ND
   else return join_digits<ND>(a);
 }
 
-__device__ __forceinline__ int32_t column_max(int32_t x) {
-  auto r = __builtin_amdgcn_permlane16_swap((uint32_t)x, (uint32_t)x, false, false);
-  x = (int32_t)r[0] > (int32_t)r[1] ? (int32_t)r[0] : (int32_t)r[1];
-  r = __builtin_amdgcn_permlane32_swap((uint32_t)x, (uint32_t)x, false, false);
-  return (int32_t)r[0] > (int32_t)r[1] ? (int32_t)r[0] : (int32_t)r[1];
-}
-
-// Probabilities of a tile that the row sees whole and one page covers, as
-// tile_softmax.  mx is a reference, at most kSlack below the maximum.
+// The digits' range of pair_softmax: its exponentials may pass 1 by the
+// rounding of a product below kFarScore, 2^-8.
 template <int ND>
-__device__ __forceinline__ void whole_tile_softmax(const typename Raw<ND>::type (&raw)[4][4],
-                                                   float unit, float vs, float& mx, float& sum,
-                                                   i32x4 (&pd)[ND], float& alpha, float& w) {
-  typename Raw<ND>::type best = raw[0][0];
+__device__ __forceinline__ constexpr float pair_digit_max() {
+  return ND == 3 ? 8257536.0f : 32256.0f;  // 126 * 256^(ND - 1)
+}
+constexpr float kFarScore = 65536.0f;
+
+// Probabilities of two tiles that the row sees whole.  unit, vs: of the lane's
+// tokens of each tile.  mx is a reference, at most kSlack below the
+// maximum.  False, with nothing changed, where scores or scales are far out or
+// not finite (tile_softmax takes those).
+template <int ND>
+__device__ __forceinline__ bool pair_softmax(const typename Raw<ND>::type (&raw)[2][4][4],
+                                             const float (&unit)[2], const float (&vs)[2],
+                                             float& mx, float& sum, i32x4 (&pd)[2][ND],
+                                             float& alpha, float& w) {
+  float tops[2];
 #pragma unroll
-  for (int a = 0; a < 4; ++a)
+  for (int t = 0; t < 2; ++t) {
+    typename Raw<ND>::type best = raw[t][0][0];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) best = raw[a][i] > best ? raw[a][i] : best;
-  const float top = (float)column_max(best) * unit;
+    for (int a = 0; a < 4; ++a)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) best = raw[t][a][i] > best ? raw[t][a][i] : best;
+    tops[t] = (float)best * unit[t];
+  }
+  const float top = column_max(fmaxf(tops[0], tops[1]));
+  const bool fine = __builtin_fabsf(tops[0]) < kFarScore && __builtin_fabsf(tops[1]) < kFarScore &&
+                    vs[0] < 1e30f && vs[1] < 1e30f;
+  if (__any(!fine)) return false;
+  // the largest p * scale is the digits' unit
+  const float big = fmaxf(column_max(fmaxf(exp2_fast(tops[0] - top) * vs[0],
+                                           exp2_fast(tops[1] - top) * vs[1])), 1e-30f);
   float part = 0.0f;
 #pragma unroll
-  for (int a = 0; a < 4; ++a) {
-    uint32_t bits[4], out[ND];
+  for (int t = 0; t < 2; ++t) {
+    const float to_digits = pair_digit_max<ND>() * (vs[t] / big);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      // at most 1 but for the product's rounding, and NaN only where unit is
-      const float e = __builtin_amdgcn_fmed3f(
-          exp2_fast(__builtin_fmaf((float)raw[a][i], unit, -top)), 0.0f, 1.0f);
-      part += e;
-      bits[i] = f32_bits(__builtin_fmaf(e, digit_max<ND>(), 8388608.0f + (float)digit_bias<ND>()));
+    for (int a = 0; a < 4; ++a) {
+      uint32_t bits[4], out[ND];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float e = exp2_fast(__builtin_fmaf((float)raw[t][a][i], unit[t], -top));
+        part += e;
+        bits[i] = f32_bits(__builtin_fmaf(e, to_digits, 8388608.0f + (float)digit_bias<ND>()));
+      }
+      pack_digits<ND>(bits[0], bits[1], bits[2], bits[3], out);
+#pragma unroll
+      for (int i = 0; i < ND; ++i) pd[t][i][a] = (int32_t)out[i];
     }
-    pack_digits<ND>(bits[0], bits[1], bits[2], bits[3], out);
-#pragma unroll
-    for (int i = 0; i < ND; ++i) pd[i][a] = (int32_t)out[i];
   }
   alpha = 1.0f;
   if (__any(top > mx + kSlack)) {
@@ -91,15 +108,17 @@ __device__ __forceinline__ void whole_tile_softmax(const typename Raw<ND>::type 
     mx = to;
   }
   const float beta = exp2_fast(top - mx);
-  sum = sum * alpha + (beta * part + (unit - unit));  // NaN shows
-  w = beta * vs * (1.0f / digit_max<ND>());
+  sum = sum * alpha + beta * part;
+  w = beta * big * (1.0f / pair_digit_max<ND>());
+  return true;
 }
 
-template <int DT, int ND, bool UNIFORM>
+// NC: 16-row blocks of a wave.
+template <int DT, int ND, int NC, bool UNIFORM>
 __global__ __launch_bounds__(kThreads, DT <= 8 ? 2 : 1) void attention_wide_kernel(AttnParams p) {
   constexpr int NS = (DT + 3) / 4;
   constexpr int KF = 4 * NS, FR = KF + DT;  // operands (1 KB each) of a tile: keys, all
-  extern __shared__ char tiles[];           // [2][FR][1024]
+  extern __shared__ char tiles[];           // [2 buffers][2 tiles][FR][1024]
   // Heads vary fastest, so that an XCD keeps to few of them, then row blocks,
   // the last first as they have the most keys: those that run together share
   // their keys in L2.
@@ -133,9 +152,9 @@ __global__ __launch_bounds__(kThreads, DT <= 8 ? 2 : 1) void attention_wide_kern
       key = segment_page(p, table, k.keys, token0 + 16 * (col >> 2));
     }
   };
-  float ks_next = 0.0f, vs_next = 0.0f;
-  // every fourth operand of the tile, straight to LDS, and the lane's scales
-  auto fetch = [&](int tile, int buf, int32_t key, int32_t own) {
+  float ks_next[2] = {0.0f, 0.0f}, vs_next[2] = {0.0f, 0.0f};
+  // every fourth operand of a tile, straight to LDS, and the lane's scales
+  auto fetch = [&](int tile, int buf, int at, int32_t key, int32_t own) {
     const int64_t token0 = (int64_t)(k.tile0 + tile) * kTile;
     const int k_slot = (int)((token0 + (UNIFORM ? 0 : 16 * (col >> 2))) & page_mask);
     const int v_slot = (int)((token0 + (UNIFORM ? 0 : 16 * g)) & page_mask);
@@ -145,7 +164,7 @@ __global__ __launch_bounds__(kThreads, DT <= 8 ? 2 : 1) void attention_wide_kern
     const int8_t* vb = c.v + ph * ((int64_t)dim << c.page_log2) + v_slot;
     const uint32_t k_off = (uint32_t)(((UNIFORM ? 16 * (col >> 2) : 0) + (col & 3)) * dim);
     const uint32_t v_off = (uint32_t)((col << c.page_log2) + (UNIFORM ? 16 * g : 0));
-    char* to = tiles + buf * FR * 1024;
+    char* to = tiles + (2 * buf + at) * FR * 1024;
 #pragma unroll
     for (int i = 0; i < (FR + kWaves - 1) / kWaves; ++i) {
       const int f = kWaves * i + wave;
@@ -160,25 +179,33 @@ __global__ __launch_bounds__(kThreads, DT <= 8 ? 2 : 1) void attention_wide_kern
       }
       __builtin_amdgcn_global_load_lds((global_ptr)src, (lds_ptr)(to + f * 1024), 16, 0, 0);
     }
-    ks_next = own >= 0 ? c.ks[ph] : nan;
-    vs_next = own >= 0 ? c.vs[ph] : nan;
+    ks_next[at] = own >= 0 ? c.ks[ph] : nan;
+    vs_next[at] = own >= 0 ? c.vs[ph] : nan;
   };
-  int32_t key = 0, own = 0, buf = 0;
+  int32_t key[2] = {0, 0}, own[2] = {0, 0}, buf = 0;
+  auto pages_of_pair = [&](int tile) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (tile + i < t_end) pages_of(tile + i, key[i], own[i]);
+  };
+  auto fetch_pair = [&](int tile, int to) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if (tile + i < t_end) fetch(tile + i, to, i, key[i], own[i]);
+  };
   int t = split * p.split_tiles;
-  if (t < t_end) {
-    pages_of(t, key, own);
-    fetch(t, 0, key, own);
-    if (t + 1 < t_end) pages_of(t + 1, key, own);
-  }
+  pages_of_pair(t);
+  fetch_pair(t, 0);
+  pages_of_pair(t + 2);
 
   // the lane's query rows and what they see
-  Column<DT> st[kColumns];
-  i32x4 qd[kColumns][NS][ND];
-  float q_unit[kColumns];
-  int64_t see_lo[kColumns], see_hi[kColumns];
-  const int64_t wave_row = k.row0 + wave * kColumns * kRows;
+  Column<DT> st[NC];
+  i32x4 qd[NC][NS][ND];
+  float q_unit[NC];
+  int64_t see_lo[NC], see_hi[NC];
+  const int64_t wave_row = k.row0 + wave * NC * kRows;
 #pragma unroll
-  for (int n = 0; n < kColumns; ++n) {
+  for (int n = 0; n < NC; ++n) {
     const int64_t r = wave_row + n * kRows + col;
     const bool valid = r < k.rows;
     const int64_t tok = valid ? r / p.group : 0;
@@ -191,7 +218,7 @@ __global__ __launch_bounds__(kThreads, DT <= 8 ? 2 : 1) void attention_wide_kern
                                    qd[n]);
   }
   // positions that some and all of the wave's rows see
-  const int64_t rows_end = wave_row + kColumns * kRows < k.rows ? wave_row + kColumns * kRows : k.rows;
+  const int64_t rows_end = wave_row + NC * kRows < k.rows ? wave_row + NC * kRows : k.rows;
   const int64_t pos_first = k.sp.pos0 + wave_row / p.group;
   const int64_t pos_last = k.sp.pos0 + (rows_end - 1) / p.group;
   const bool idle = wave_row >= k.rows;
@@ -199,87 +226,115 @@ __global__ __launch_bounds__(kThreads, DT <= 8 ? 2 : 1) void attention_wide_kern
   const int64_t all_hi = pos_first < k.keys.hi ? pos_first : k.keys.hi - 1;
   const int64_t all_lo = p.window > 0 ? pos_last - p.window + 1 : 0;
 
-  for (; t < t_end; ++t, buf ^= 1) {
-    // this wave's part of the tile has landed; past the barrier all of it has,
-    // and every wave is done with the other buffer
+  for (; t < t_end; t += 2, buf ^= 1) {
+    // this wave's part of the tiles has landed; past the barrier all of them
+    // have, and every wave is done with the other buffer
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    const float ks = ks_next, vs = vs_next;
-    if (t + 1 < t_end) {
-      fetch(t + 1, buf ^ 1, key, own);
-      if (t + 2 < t_end) pages_of(t + 2, key, own);
-    }
+    const float ks[2] = {ks_next[0], ks_next[1]}, vs[2] = {vs_next[0], vs_next[1]};
+    fetch_pair(t + 2, buf ^ 1);
+    pages_of_pair(t + 4);
+    // A wave in its matrix instructions goes before one in its exponentials, so
+    // that the two units are busy at once (4% here)
+    __builtin_amdgcn_s_setprio(0);
     const int64_t token0 = (int64_t)(k.tile0 + t) * kTile;
-    if (idle || token0 >= some.hi || token0 + kTile <= some.lo) continue;
-    const bool whole = token0 >= all_lo && token0 + kTile - 1 <= all_hi;
-    const char* from = tiles + buf * FR * 1024 + 16 * lane;
-    typename Raw<ND>::type raw[kColumns][4][4];
+    if (idle || token0 >= some.hi || token0 + 2 * kTile <= some.lo) continue;
+    const bool whole =
+        t + 1 < t_end && token0 >= all_lo && token0 + 2 * kTile - 1 <= all_hi;
+    const char* from = tiles + 2 * buf * FR * 1024 + 16 * lane;
+    i32x4 pd[NC][2][ND];
+    float w[NC];
+    bool pairs = false;
 #pragma unroll
-    for (int a = 0; a < 4; ++a) {
-      i32x4 kd[NS];
+    for (int n = 0; n < NC; ++n) {
+      bool done = false;
+      if (whole) {
+        typename Raw<ND>::type raw[2][4][4];
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-      for (int s = 0; s < NS; ++s) kd[s] = *(const i32x4*)(from + (a * NS + s) * 1024);
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int n = 0; n < kColumns; ++n) {
-        i32x4 acc[ND];
+          for (int a = 0; a < 4; ++a) {
+            i32x4 acc[ND];
 #pragma unroll
-        for (int i = 0; i < ND; ++i) {
-          acc[i] = i32x4{0, 0, 0, 0};
+            for (int s = 0; s < NS; ++s) {
+              const i32x4 kd = *(const i32x4*)(from + (i * FR + a * NS + s) * 1024);
 #pragma unroll
-          for (int s = 0; s < NS; ++s)
-            acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(kd[s], qd[n][s][i], acc[i], 0, 0, 0);
+              for (int m = 0; m < ND; ++m)
+                acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(
+                    kd, qd[n][s][m], s == 0 ? i32x4{0, 0, 0, 0} : acc[m], 0, 0, 0);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              int32_t part[ND];
+#pragma unroll
+              for (int m = 0; m < ND; ++m) part[m] = acc[m][e];
+              raw[i][a][e] = raw_join<ND>(part);
+            }
+          }
+        __builtin_amdgcn_s_setprio(0);
+        const float unit[2] = {q_unit[n] * ks[0], q_unit[n] * ks[1]};
+        float alpha = 1.0f;
+        done = pair_softmax<ND>(raw, unit, vs, st[n].mx, st[n].sum, pd[n], alpha, w[n]);
+        if (done && __any(alpha != 1.0f)) {
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) st[n].o[dt][e] *= alpha;
         }
+      }
+      if (!done) {
+        // a tile at a time, with masks; the pair adds nothing below
+        w[n] = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          int32_t part[ND];
+        for (int i = 0; i < 2; ++i)
 #pragma unroll
-          for (int i = 0; i < ND; ++i) part[i] = acc[i][e];
-          raw[n][a][e] = raw_join<ND>(part);
+          for (int m = 0; m < ND; ++m) pd[n][i][m] = i32x4{0, 0, 0, 0};
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+          const int64_t first = token0 + i * kTile;
+          if (t + i >= t_end || first >= some.hi || first + kTile <= some.lo) continue;
+          i32x4 kd[4][NS], vd[DT], digits[ND];
+#pragma unroll
+          for (int a = 0; a < 4; ++a)
+#pragma unroll
+            for (int s = 0; s < NS; ++s)
+              kd[a][s] = *(const i32x4*)(from + (i * FR + a * NS + s) * 1024);
+          float sc[4][4], alpha, worth;
+          tile_scores<NS, ND>(kd, qd[n], sc);
+          const int64_t lo = see_lo[n] - (first + 16 * g), hi = see_hi[n] - (first + 16 * g);
+          tile_softmax<ND, true, UNIFORM>(
+              sc, q_unit[n] * (i ? ks[1] : ks[0]), i ? vs[1] : vs[0],
+              (int)(lo > 16 ? 16 : lo < 0 ? 0 : lo), (int)(hi < -1 ? -1 : hi > 15 ? 15 : hi),
+              st[n].mx, st[n].sum, digits, alpha, worth);
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt)
+            vd[dt] = *(const i32x4*)(from + (i * FR + KF + dt) * 1024);
+          tile_values<DT, ND>(vd, digits, alpha, worth, st[n].o);
         }
       }
+      pairs |= done;
     }
-    i32x4 pd[kColumns][ND];
-    float w[kColumns];
-#pragma unroll
-    for (int n = 0; n < kColumns; ++n) {
-      float alpha;
-      const float unit = q_unit[n] * ks;
-      if (UNIFORM && whole) {
-        whole_tile_softmax<ND>(raw[n], unit, vs, st[n].mx, st[n].sum, pd[n], alpha, w[n]);
-      } else {
-        float sc[4][4];
-#pragma unroll
-        for (int a = 0; a < 4; ++a)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[a][e] = (float)raw[n][a][e];
-        const int64_t base = token0 + 16 * g;
-        const int64_t lo = see_lo[n] - base, hi = see_hi[n] - base;
-        tile_softmax<ND, true, UNIFORM>(sc, unit, vs, (int)(lo > 16 ? 16 : lo < 0 ? 0 : lo),
-                                        (int)(hi < -1 ? -1 : hi > 15 ? 15 : hi), st[n].mx,
-                                        st[n].sum, pd[n], alpha, w[n]);
-      }
-      if (__any(alpha != 1.0f)) {
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) st[n].o[dt][e] *= alpha;
-      }
-    }
+    if (!pairs) continue;
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt) {
-      const i32x4 vd = *(const i32x4*)(from + (KF + dt) * 1024);
+      const i32x4 v0 = *(const i32x4*)(from + (KF + dt) * 1024);
+      const i32x4 v1 = *(const i32x4*)(from + (FR + KF + dt) * 1024);
 #pragma unroll
-      for (int n = 0; n < kColumns; ++n) {
+      for (int n = 0; n < NC; ++n) {
         i32x4 acc[ND];
 #pragma unroll
-        for (int i = 0; i < ND; ++i)
-          acc[i] = __builtin_amdgcn_mfma_i32_16x16x64_i8(vd, pd[n][i], i32x4{0, 0, 0, 0}, 0, 0, 0);
+        for (int m = 0; m < ND; ++m) {
+          acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(v0, pd[n][0][m], i32x4{0, 0, 0, 0}, 0, 0, 0);
+          acc[m] = __builtin_amdgcn_mfma_i32_16x16x64_i8(v1, pd[n][1][m], acc[m], 0, 0, 0);
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           int32_t part[ND];
 #pragma unroll
-          for (int i = 0; i < ND; ++i) part[i] = acc[i][e];
+          for (int m = 0; m < ND; ++m) part[m] = acc[m][e];
           st[n].o[dt][e] = __builtin_fmaf((float)raw_join<ND>(part), w[n], st[n].o[dt][e]);
         }
       }
@@ -287,7 +342,7 @@ __global__ __launch_bounds__(kThreads, DT <= 8 ? 2 : 1) void attention_wide_kern
   }
 
 #pragma unroll
-  for (int n = 0; n < kColumns; ++n) {
+  for (int n = 0; n < NC; ++n) {
     const int64_t r = wave_row + n * kRows + col;
     const float sum = column_sum(st[n].sum);
     if (r >= k.rows) continue;

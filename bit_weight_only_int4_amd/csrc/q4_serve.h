@@ -55,7 +55,7 @@ struct AttnParams {
   float scale_log2;             // scale * log2(e)
   int32_t q_vec;                // 16-byte aligned query rows
   int32_t max_rows;             // per sequence and kv head
-  int32_t block_rows;           // query rows of a workgroup: 16, or 128 (attention_wide_kernel)
+  int32_t block_rows;           // query rows of a workgroup: 16, or 64 or 128 (attention_wide_kernel)
   int32_t row_blocks;           // per sequence and kv head
   int32_t splits;               // workgroups along the keys (grid)
   int32_t split_tiles;          // tiles of 64 keys each of them takes

@@ -109,36 +109,45 @@ def test_many_new_tokens(page, dtype):
     check([97, 200], [600, 201], 4, 1, 128, page, dtype, seed=12, window=150)
 
 
+# sequences that make the rows many enough for the kernel that shares keys between them
+FILL = [1] * 75
+
+
 @pytest.mark.parametrize("dim", [16, 48, 64, 80, 96, 128, 144, 192, 256])
 @pytest.mark.parametrize("page,dtype", [(16, "f32"), (64, "f16"), (128, "f32"), (32, "bf16")])
 def test_chunks_of_all_head_sizes(dim, page, dtype):
-    check([33, 70, 1], [33, 400, 90], 4, 2, dim, page, dtype, seed=dim, layout="fused")
+    check([33, 70, 1] + FILL, [33, 400, 90] + FILL, 4, 2, dim, page, dtype, seed=dim, layout="fused")
 
 
 @pytest.mark.parametrize("window", [1, 40, 64, 129, 1000])
 @pytest.mark.parametrize("page", [16, 64])
 def test_chunks_under_windows(window, page):
-    check([150, 64, 3, 0], [700, 64, 200, 10], 3, 1, 64, page, "f32", window=window, seed=window)
+    check([150, 64, 3, 0] + FILL, [700, 64, 200, 10] + FILL, 3, 1, 64, page, "f32", window=window, seed=window)
 
 
 @pytest.mark.parametrize("heads,kv_heads", [(1, 1), (5, 1), (32, 8), (130, 1)])
 def test_chunks_of_head_groups(heads, kv_heads):
-    check([65, 129, 2], [80, 300, 2], heads, kv_heads, 32, 64, "f16", seed=heads)
+    check([65, 129, 2] + FILL, [80, 300, 2] + FILL, heads, kv_heads, 32, 64, "f16", seed=heads)
 
 
 def test_chunks_over_long_contexts_are_split():
-    check([40, 7], [5000, 2100], 8, 2, 128, 64, "bf16", seed=1)
-    check([40, 7], [5000, 2100], 8, 2, 64, 16, "f32", seed=2, window=3000)
-    check([20, 5], [40, 2100], 8, 2, 64, 16, "f32", seed=3, max_len=100000)
+    check([40, 7] + FILL, [5000, 2100] + FILL, 8, 2, 128, 64, "bf16", seed=1)
+    check([40, 7] + FILL, [5000, 2100] + FILL, 8, 2, 64, 16, "f32", seed=2, window=3000)
+    check([40, 5] + FILL, [60, 2100] + FILL, 8, 2, 64, 16, "f32", seed=3, max_len=100000)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_many_blocks_of_chunks(dtype):
+    """More than 512 workgroups of 128 rows by the bounds."""
+    check([130] + [3] * 120, [600] + [9] * 120, 16, 4, 64, 64, dtype, seed=5)
 
 
 def test_chunks_with_scores_and_scales_far_apart():
-    check([100, 30], [400, 70], 4, 2, 64, 64, "f32", q_gain=40.0, seed=8)
-    check([100, 30], [400, 70], 4, 2, 64, 64, "bf16", q_gain=40.0, seed=8)
-    check([100, 30], [400, 70], 4, 2, 64, 64, "f32", scale=0.0, seed=9)
-    check([100, 30], [400, 70], 4, 2, 64, 64, "f32", scale=-0.3, seed=10)
-    check([100, 30], [400, 70], 4, 2, 64, 16, "f32", spread=3.0, seed=11)
-    check([100, 30], [400, 70], 4, 2, 64, 128, "f32", spread=3.0, seed=12)
+    for kw in (dict(q_gain=40.0, seed=8), dict(scale=0.0, seed=9), dict(scale=-0.3, seed=10), dict(spread=3.0, seed=12),
+               dict(q_gain=3e5, seed=13)):
+        for page in (16, 64, 128):
+            check([100, 30] + FILL, [400, 170] + FILL, 4, 2, 64, page, "f32", **kw)
+    check([100, 30] + FILL, [400, 170] + FILL, 4, 2, 64, 64, "bf16", q_gain=40.0, seed=8)
 
 
 def test_empty_sequences_and_queries_before_the_start():
@@ -222,17 +231,32 @@ def test_zero_scales(page):
 # (an infinite key scale is left out: a score of -inf is no weight at all)
 @pytest.mark.parametrize("which,value", [("k", np.nan), ("v", np.nan), ("v", np.inf)])
 @pytest.mark.parametrize("page", [16, 64, 128])
-def test_a_page_that_is_not_finite_shows_only_where_it_is_seen(which, value, page):
-    """Sequence 0's last page; earlier queries of the same call do not see it."""
-    new, lengths = [40, 1], [page + 20, 300]
+@pytest.mark.parametrize("new,fill", [(40, []), (60, FILL)])
+def test_a_page_that_is_not_finite_shows_only_where_it_is_seen(which, value, page, new, fill):
+    """Sequence 0's second page; earlier queries of the same call do not see it."""
+    lengths = [page + 20, 300] + fill
 
     def edit(b, k, v, ks, vs):
         (ks if which == "k" else vs)[b.table[0, 1]] = value
-    got, ref, tol = run(new, lengths, 4, 2, 64, page, "f32", edit=edit, seed=14)
-    sees = np.array([lengths[0] - 40 + i >= page for i in range(40)] + [False])
+    with np.errstate(invalid="ignore"):
+        got, ref, tol = run([new, 1] + fill, lengths, 4, 2, 64, page, "f32", edit=edit, seed=14)
+    sees = np.array([lengths[0] - new + i >= page for i in range(new)] + [False] * (1 + len(fill)))
     assert (~np.isfinite(got[sees])).all(axis=2).all()
     assert np.isfinite(got[~sees]).all()
-    assert (np.abs(got - ref)[~sees] <= tol[~sees]).all()
+    assert (np.abs(got[~sees] - ref[~sees]) <= tol[~sees]).all()
+
+
+def test_bad_pages_in_chunks():
+    need_gpu()
+    b = Batch([90] + FILL, [200] + FILL, 16, 0)
+    caches = [torch.from_numpy(x).cuda() for x in random_cache(b, 2, 64, 1)]
+    q = torch.randn((b.T, 4, 64), device="cuda")
+    table, cu, ln = b.device()
+    clean = q4.attention(q, *caches, table, cu, ln, max_new=90)
+    table[0, 9] = b.pages  # positions 144 .. 159; the new tokens are at 110 .. 199
+    got = q4.attention(q, *caches, table, cu, ln, max_new=90)
+    assert clean.isfinite().all() and got[34:90].isnan().all()
+    assert torch.allclose(got[:34], clean[:34], rtol=1e-5, atol=1e-6) and torch.equal(got[90:], clean[90:])
 
 
 @pytest.mark.parametrize("value", [np.nan, np.inf, -np.inf])
