@@ -5,14 +5,23 @@ namespace q4 {
 
 namespace attn {
 
-// Adds the parts of one query row, n of them, part s at rows at + s * stride of
-// part_o and part_ml, and writes the output.  The parts' weights come first,
-// a thread each, so that their outputs then load without waiting for one
-// another: 4 elements a thread, dim / 4 threads a part, four parts a step.
-__device__ __forceinline__ void join_row(const AttnParams& p, int n, int64_t at, int64_t stride,
-                                         int64_t out, int32_t max_parts) {
-  extern __shared__ float lds[];  // weights [max_parts], then [parts at once][dim]
+// Joins the splits of a query row, a workgroup each, where there may be many.
+// The parts' weights come first, a thread each, so that their outputs then
+// load without waiting for one another: 4 elements a thread, dim / 4 threads a
+// part, four parts a step.
+__global__ __launch_bounds__(kThreads) void attention_join_many_kernel(AttnParams p) {
+  extern __shared__ float lds[];  // weights [splits], then [parts at once][dim]
   __shared__ float red[2 * kWaves];
+  const int64_t rr = blockIdx.x % p.max_rows;
+  const uint32_t bh = blockIdx.x / p.max_rows;
+  const Block k = block_of(p, bh / p.c.heads, bh % p.c.heads, (int)(rr / p.block_rows));
+  if (rr >= k.rows) return;
+  const int n = (k.tiles + p.split_tiles - 1) / p.split_tiles;
+  if (n <= 1) return;
+  const int64_t tk = rr / p.group;
+  const int64_t tq = k.sp.t0 + tk, hq = k.h * p.group + (rr - tk * p.group);
+  const int64_t at = tq * p.heads + hq, stride = p.T * p.heads;
+  const int64_t out = tq * p.o_ts + hq * p.o_hs;
   const int tid = threadIdx.x, wave = tid >> 6, lane = tid & 63, dim = p.c.dim;
   float* weight = lds;
   float m = -__builtin_inff();
@@ -49,21 +58,21 @@ __device__ __forceinline__ void join_row(const AttnParams& p, int n, int64_t at,
       for (int i = 0; i < 4; ++i) acc += weight[s + i * at_once] * v[i];
     }
     for (; s < n; s += at_once) acc += weight[s] * *(const f32x4*)(src + s * stride * dim);
-    float* o = lds + max_parts + part * dim + d;
+    float* o = lds + p.splits + part * dim + d;
 #pragma unroll
     for (int e = 0; e < 4; ++e) o[e] = acc[e];
   }
   __syncthreads();
   if (tid >= dim) return;
   float o = 0.0f, total = 0.0f;
-  for (int i = 0; i < at_once; ++i) o += lds[max_parts + i * dim + tid];
+  for (int i = 0; i < at_once; ++i) o += lds[p.splits + i * dim + tid];
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) total += red[kWaves + w];
   store_elem(p.out, out + tid, total == 0.0f ? 0.0f : o / total, p.dtype);
 }
 
-// The blocks that have more than one split: dim / 4 threads a query row, so
-// that many rows with few parts share a workgroup.
+// Joins few splits: dim / 4 threads a query row, so that many rows share a
+// workgroup.
 __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnParams p) {
   const int quads = p.c.dim >> 2, at_once = kThreads / quads;
   const int mine = threadIdx.x / quads, d = 4 * (threadIdx.x - mine * quads);
@@ -97,28 +106,6 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnParams p) 
     store_elem(p.out, tq * p.o_ts + hq * p.o_hs + d + e, acc[e] * inv, p.dtype);
 }
 
-// One query row of the units whose tiles several waves had; zeros for those
-// without a tile.
-__global__ __launch_bounds__(kThreads) void attention_stream_join_kernel(AttnParams p) {
-  const int64_t rr = blockIdx.x % p.max_rows;
-  const uint32_t bh = blockIdx.x / p.max_rows;
-  const int b = bh / p.c.heads, h = bh % p.c.heads, rb = (int)(rr / kRows);
-  const Block k = block_of(p, b, h, rb);
-  if (rr >= k.rows) return;
-  const int64_t tk = rr / p.group;
-  const int64_t tq = k.sp.t0 + tk, hq = k.h * p.group + (rr - tk * p.group);
-  const int64_t out = tq * p.o_ts + hq * p.o_hs;
-  if (k.tiles == 0) {
-    if ((int)threadIdx.x < p.c.dim) store_elem(p.out, out + threadIdx.x, 0.0f, p.dtype);
-    return;
-  }
-  const int unit = (h * p.batch + b) * p.row_blocks + rb;
-  const int32_t piece = p.stream_info[0], start = p.stream_info[1 + unit];
-  const int32_t first = start / piece, n = (start + k.tiles - 1) / piece - first + 1;
-  if (n <= 1) return;
-  join_row(p, n, ((int64_t)first + unit) * kRows + (rr - k.row0), kRows, out, p.stream_waves);
-}
-
 }  // namespace attn
 
 namespace {
@@ -138,21 +125,24 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // 47.9 against 40.2 in fp32, with 128 52.6 against 57.6 and 63.8 against 61.2,
 // with 192 54.7 against 80.6 and 64.5 against 85.2).
 //
-// Rows of many keys run the stream kernel, whose waves share all keys evenly:
-// where a unit has at least kStreamTiles tiles by max_len, units are few enough
-// for their running sum in LDS, and the line's length fits 32 bits.  Below,
-// one workgroup per unit needs no second launch.
-//
-// Otherwise the keys of a row block go to several workgroups while row blocks
-// alone leave CUs without work.  max_len and the window bound the tiles:
-// neither the grid nor the workspace depends on device-side lengths.
+// Else 16 rows a workgroup.  The keys of a row block go to several workgroups,
+// each at least kMinTiles tiles, where row blocks alone do not give every CU
+// one (kTargetBlocks); and, where they do, to at most kRagged, each at least
+// kRaggedTiles tiles, as sequences differ in length and the longest would run
+// alone at the end (64 sequences of 500 to 8000 tokens, 8 kv heads of 128: 104
+// us with one, 81 with four; of 9000 tokens each, where nothing is gained, 204
+// and 212).  Equal pieces for all workgroups, cut from the tiles of all
+// sequences in a row, were measured and not kept: the longer way to the first
+// key and the second launch cost what the balance gave (84 and 231 us).
+// max_len and the window bound the tiles: neither the grid nor the workspace
+// depends on device-side lengths.
 AttnPlan plan_attention(int32_t dtype, int64_t T, int64_t batch, int64_t heads, int64_t kv_heads,
                         int64_t dim, int64_t page, int64_t max_new, int64_t max_len,
                         int64_t window) {
   (void)dtype;
   (void)page;
-  constexpr int64_t kTargetBlocks = 1024, kWideTarget = 512, kMinTiles = 16, kStreamTiles = 32;
-  constexpr int64_t kStreamUnits = 8192, kStreamWaves = 2048, kWideMin = 96, kWideAll = 8192;
+  constexpr int64_t kTargetBlocks = 256, kWideTarget = 512, kMinTiles = 4, kWideTiles = 16;
+  constexpr int64_t kRagged = 4, kRaggedTiles = 24, kWideMin = 96, kWideAll = 8192;
   AttnPlan pl{};
   const int64_t group = heads / kv_heads;
   const bool wide = max_new * group >= kWideMin && batch * kv_heads * max_new * group >= kWideAll;
@@ -166,23 +156,15 @@ AttnPlan plan_attention(int32_t dtype, int64_t T, int64_t batch, int64_t heads, 
   if (window > 0 && window + pl.block_rows < span) span = window + pl.block_rows;
   int64_t tiles = ceil_div(span, attn::kTile) + (window > 0 ? 1 : 0);
   if (tiles < 1) tiles = 1;
-  const int64_t units = batch * pl.row_blocks, blocks = units * kv_heads;
-  pl.splits = 1;
-  pl.split_tiles = (int32_t)tiles;
-  if (!wide && tiles >= kStreamTiles && pl.row_blocks <= 2 && units <= kStreamUnits &&
-      (double)tiles * (double)blocks < 1073741824.0) {
-    int64_t waves = ceil_div(tiles * blocks, attn::kMinPiece);
-    if (waves > kStreamWaves) waves = kStreamWaves;
-    pl.stream_waves = (int32_t)(ceil_div(waves, attn::kWaves) * attn::kWaves);
-    pl.parts = (size_t)(pl.stream_waves + blocks) * attn::kRows;
-    pl.workspace = pl.parts * (size_t)(dim + 2) * sizeof(float) + (size_t)(1 + blocks) * sizeof(int32_t);
-    return pl;
-  }
-  int64_t splits = ceil_div(wide ? kWideTarget : kTargetBlocks, blocks > 0 ? blocks : 1);
-  if (splits > tiles / kMinTiles) splits = tiles / kMinTiles;
+  const int64_t blocks = batch * kv_heads * pl.row_blocks;
+  const int64_t target = wide ? kWideTarget : kTargetBlocks, least = wide ? kWideTiles : kMinTiles;
+  int64_t splits = ceil_div(target, blocks > 0 ? blocks : 1);
+  if (splits > tiles / least) splits = tiles / least;
+  if (!wide && blocks >= kTargetBlocks) splits = tiles / kRaggedTiles < kRagged ? tiles / kRaggedTiles : kRagged;
   if (splits < 1) splits = 1;
   pl.split_tiles = (int32_t)ceil_div(tiles, splits);
   pl.splits = (int32_t)ceil_div(tiles, pl.split_tiles);
+  pl.few = !wide && blocks * pl.splits <= 256;
   pl.parts = pl.splits > 1 ? (size_t)pl.splits * (size_t)(T * heads) : 0;
   pl.workspace = pl.parts * (size_t)(dim + 2) * sizeof(float);
   return pl;
@@ -191,11 +173,11 @@ AttnPlan plan_attention(int32_t dtype, int64_t T, int64_t batch, int64_t heads, 
 hipError_t launch_attention(const AttnParams& p, hipStream_t s) {
   const hipError_t e = p.dtype == Q4_DTYPE_F32 ? launch_attention_digits<3>(p, s)
                                                : launch_attention_digits<2>(p, s);
-  if (e != hipSuccess || (p.splits <= 1 && !p.stream_waves)) return e;
+  if (e != hipSuccess || p.splits <= 1) return e;
   const int64_t bh = (int64_t)p.batch * p.c.heads, at_once = attn::kThreads / (p.c.dim / 4);
-  if (p.stream_waves) {
-    const size_t lds = (p.stream_waves + (size_t)at_once * p.c.dim) * sizeof(float);
-    hipLaunchKernelGGL(attn::attention_stream_join_kernel, dim3((unsigned)(bh * p.max_rows)),
+  if (p.splits > 16) {
+    const size_t lds = (p.splits + (size_t)at_once * p.c.dim) * sizeof(float);
+    hipLaunchKernelGGL(attn::attention_join_many_kernel, dim3((unsigned)(bh * p.max_rows)),
                        dim3(attn::kThreads), lds, s, p);
   } else {
     hipLaunchKernelGGL(attn::attention_join_kernel,

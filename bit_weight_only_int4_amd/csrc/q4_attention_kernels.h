@@ -37,7 +37,6 @@ constexpr int kTile = 64;   // tokens per step of a wave
 constexpr int kWaves = 4;   // waves of a workgroup, each over its own tiles
 constexpr int kRows = 16;   // query rows of a workgroup
 constexpr int kThreads = 64 * kWaves;
-constexpr int kMinPiece = 2;  // tiles of a wave in attention_stream_kernel
 
 // largest integer that ND digits hold with the offsets of pack_digits
 template <int ND>
@@ -132,12 +131,6 @@ __device__ __forceinline__ Block block_of(const AttnParams& p, int b, int h, int
   k.tile0 = (int)(k.keys.lo / kTile);
   k.tiles = k.keys.hi > k.keys.lo ? (int)((k.keys.hi + kTile - 1) / kTile) - k.tile0 : 0;
   return k;
-}
-
-// Tiles of one wave's piece of a line of `total`, dealt to `waves` of them.
-__device__ __forceinline__ int32_t stream_piece(int32_t total, int32_t waves) {
-  const int32_t piece = (total + waves - 1) / waves;
-  return piece > kMinPiece ? piece : kMinPiece;
 }
 
 // Where the 16 tokens at token0 (a multiple of 16) of the sequence lie: their
@@ -480,10 +473,72 @@ __device__ __forceinline__ void attend(const AttnParams& p, const Block& k, int 
   }
 }
 
+// Joins the parts of a workgroup's waves through LDS and writes them: finished
+// (`whole`), or as partial outputs from row `first` of the workspace on, a row
+// for each of token * heads + head.  lds: W * 16 (16 DT + 6) floats.
+template <int DT, int W>
+__device__ __forceinline__ void join_waves(const AttnParams& p, const Block& k, const Column<DT>& st,
+                                           float* lds, bool whole, int64_t first) {
+  const int wave = threadIdx.x >> 6, col = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
+  const int dim = p.c.dim;
+  // [wave][row][dim] outputs, then maxima and sums
+  const float sum = column_sum(st.sum);
+  constexpr int pitch = 16 * DT + 4;
+  float* lo = lds;
+  float* lm = lds + W * kRows * pitch;
+  float* ls = lm + W * kRows;
+#pragma unroll
+  for (int dt = 0; dt < DT; ++dt)
+    *(f32x4*)&lo[(wave * kRows + col) * pitch + 16 * dt + 4 * g] =
+        f32x4{st.o[dt][0], st.o[dt][1], st.o[dt][2], st.o[dt][3]};
+  if (g == 0) {
+    lm[wave * kRows + col] = st.mx;
+    ls[wave * kRows + col] = sum;
+  }
+  __syncthreads();
+  // 4 W threads a row, 4 elements a step
+  const int row = threadIdx.x / (4 * W), sub = threadIdx.x % (4 * W);
+  const int64_t rr = k.row0 + row;
+  if (rr >= k.rows) return;
+  float m = lm[row];
+#pragma unroll
+  for (int i = 1; i < W; ++i) m = fmaxf(m, lm[i * kRows + row]);
+  const float ref = m > -__builtin_inff() ? m : 0.0f;
+  float f[W], den = 0.0f;
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    f[i] = exp2_fast(lm[i * kRows + row] - ref);
+    // a wave without a maximum has a sum of 0, or NaN, which has to show
+    const float si = ls[i * kRows + row];
+    den += si != si ? si : f[i] * si;
+  }
+  const int64_t tk = rr / p.group;
+  const int64_t tq = k.sp.t0 + tk, hq = k.h * p.group + (rr - tk * p.group);
+  const int64_t at = first + tq * p.heads + hq;
+  const float inv = den == 0.0f ? 0.0f : 1.0f / den;  // no key seen: 0
+  for (int d = 4 * sub; d < dim; d += 16 * W) {
+    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < W; ++i)
+      acc += f[i] * *(const f32x4*)&lo[(i * kRows + row) * pitch + d];
+    if (whole) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        store_elem(p.out, tq * p.o_ts + hq * p.o_hs + d + e, acc[e] * inv, p.dtype);
+    } else {
+      *(f32x4*)&p.part_o[at * dim + d] = acc;
+    }
+  }
+  if (!whole && sub == 0) {
+    p.part_ml[2 * at] = m;
+    p.part_ml[2 * at + 1] = den;
+  }
+}
+
 // One workgroup: 16 query rows of one kv head, one split of their keys, the
-// tiles dealt to its four waves in turn and joined through LDS.
-template <int DT, int ND, bool UNIFORM>
-__global__ __launch_bounds__(kThreads, DT <= 4 ? 3 : DT <= 8 ? 2 : 1) void attention_kernel(AttnParams p) {
+// tiles dealt to its W waves in turn and joined through LDS.
+template <int DT, int ND, int W, bool UNIFORM>
+__global__ __launch_bounds__(64 * W, DT <= 4 && W == 4 ? 3 : DT <= 8 ? 2 : 1) void attention_kernel(AttnParams p) {
   extern __shared__ float lds[];
   // Heads vary fastest, then sequences, row blocks and splits: consecutive
   // workgroups go to the 8 XCDs in turn, so that neither the sequences' lengths
@@ -500,172 +555,11 @@ __global__ __launch_bounds__(kThreads, DT <= 4 ? 3 : DT <= 8 ? 2 : 1) void atten
   // a block whose tiles fit one split writes its output itself
   const int n_splits = (k.tiles + p.split_tiles - 1) / p.split_tiles;
   if (split > 0 && split >= n_splits) return;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int col = lane & 15, g = lane >> 4;
-  const int dim = p.c.dim;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int t_end = (split + 1) * p.split_tiles < k.tiles ? (split + 1) * p.split_tiles : k.tiles;
   Column<DT> st;
-  attend<DT, ND, UNIFORM>(p, k, split * p.split_tiles + wave, t_end, kWaves, st);
-
-  // join the waves' parts: [wave][row][dim] outputs, then maxima and sums
-  const float sum = column_sum(st.sum);
-  constexpr int pitch = 16 * DT + 4;
-  float* lo = lds;
-  float* lm = lds + kWaves * kRows * pitch;
-  float* ls = lm + kWaves * kRows;
-#pragma unroll
-  for (int dt = 0; dt < DT; ++dt)
-    *(f32x4*)&lo[(wave * kRows + col) * pitch + 16 * dt + 4 * g] =
-        f32x4{st.o[dt][0], st.o[dt][1], st.o[dt][2], st.o[dt][3]};
-  if (g == 0) {
-    lm[wave * kRows + col] = st.mx;
-    ls[wave * kRows + col] = sum;
-  }
-  __syncthreads();
-  // 16 threads a row, 4 elements a step
-  const int row = threadIdx.x >> 4, sub = threadIdx.x & 15;
-  const int64_t rr = k.row0 + row;
-  if (rr >= k.rows) return;
-  float m = lm[row];
-#pragma unroll
-  for (int i = 1; i < kWaves; ++i) m = fmaxf(m, lm[i * kRows + row]);
-  const float ref = m > -__builtin_inff() ? m : 0.0f;
-  float f[kWaves], den = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kWaves; ++i) {
-    f[i] = exp2_fast(lm[i * kRows + row] - ref);
-    // a wave without a maximum has a sum of 0, or NaN, which has to show
-    const float si = ls[i * kRows + row];
-    den += si != si ? si : f[i] * si;
-  }
-  const int64_t tk = rr / p.group;
-  const int64_t tq = k.sp.t0 + tk, hq = k.h * p.group + (rr - tk * p.group);
-  const int64_t at = (int64_t)split * p.T * p.heads + tq * p.heads + hq;
-  const float inv = den == 0.0f ? 0.0f : 1.0f / den;  // no key seen: 0
-  for (int d = 4 * sub; d < dim; d += 64) {
-    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int i = 0; i < kWaves; ++i)
-      acc += f[i] * *(const f32x4*)&lo[(i * kRows + row) * pitch + d];
-    if (n_splits <= 1) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        store_elem(p.out, tq * p.o_ts + hq * p.o_hs + d + e, acc[e] * inv, p.dtype);
-    } else {
-      *(f32x4*)&p.part_o[at * dim + d] = acc;
-    }
-  }
-  if (n_splits > 1 && sub == 0) {
-    p.part_ml[2 * at] = m;
-    p.part_ml[2 * at + 1] = den;
-  }
-}
-
-// Many keys for few rows: the tiles of all units, a unit being the 16 rows of
-// one sequence, row block and kv head, lie on one line, head after head, and
-// every wave takes an equal piece of it, whatever the sequences' lengths.
-// Waves work alone: a unit that lies in one wave's piece is finished there,
-// the parts of the others go to the workspace and attention_stream_join_kernel
-// adds them.  Walking along the line, either the wave or the unit number grows
-// by one from part to part, so their sum numbers the parts.
-//
-// Measured against the workgroup kernel's splits at 64 sequences of 500 to
-// 8000 tokens (8 kv heads of 128): its workgroups last four tiles per wave,
-// most of it the start-up chain table -> page -> keys, and the sequences'
-// lengths leave a tail.
-template <int DT, int ND, bool UNIFORM>
-__global__ __launch_bounds__(kThreads, DT <= 4 ? 3 : DT <= 8 ? 2 : 1) void attention_stream_kernel(
-    AttnParams p) {
-  extern __shared__ int32_t ends[];  // [units of a head]: tiles up to and with each
-  __shared__ int32_t wave_total[kWaves];
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-  const int col = lane & 15, g = lane >> 4;
-  const int units = p.batch * p.row_blocks;
-  // running sum of the units' tiles: a thread's share, then over threads
-  const int per = (units + kThreads - 1) / kThreads;
-  int32_t mine = 0;
-  for (int i = 0; i < per; ++i) {
-    const int u = threadIdx.x * per + i;
-    if (u >= units) break;
-    const Block k = block_of(p, u / p.row_blocks, 0, u % p.row_blocks);
-    mine += k.row0 < k.rows ? k.tiles : 0;
-    ends[u] = mine;
-  }
-  int32_t before = mine;
-#pragma unroll
-  for (int m = 1; m < 64; m <<= 1) {
-    const int32_t o = __shfl_up(before, m, 64);
-    before += lane >= m ? o : 0;
-  }
-  if (lane == 63) wave_total[wave] = before;
-  __syncthreads();
-  int32_t line = 0;
-  before -= mine;
-#pragma unroll
-  for (int w = 0; w < kWaves; ++w) {
-    before += w < wave ? wave_total[w] : 0;
-    line += wave_total[w];
-  }
-  for (int i = 0; i < per; ++i) {
-    const int u = threadIdx.x * per + i;
-    if (u >= units) break;
-    ends[u] += before;
-  }
-  __syncthreads();
-  line = __builtin_amdgcn_readfirstlane(line);
-  const int32_t total = line * p.c.heads;
-  const int32_t piece = stream_piece(total, p.stream_waves);
-  if (blockIdx.x == 0 && threadIdx.x == 0) p.stream_info[0] = piece;
-  const int32_t me = (int32_t)blockIdx.x * kWaves + wave;
-  int32_t at = me * piece;
-  const int32_t end = at + piece < total ? at + piece : total;
-  while (at < end) {
-    const int h = at / line;
-    const int32_t rem = at - h * line;
-    // the unit that holds `rem`: the first whose end is past it
-    int lo = 0, hi = units - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (ends[mid] > rem) hi = mid; else lo = mid + 1;
-    }
-    const int u = __builtin_amdgcn_readfirstlane(lo);
-    const Block k = block_of(p, u / p.row_blocks, h, u % p.row_blocks);
-    const int32_t start = h * line + __builtin_amdgcn_readfirstlane(ends[u]) - k.tiles;
-    const int t = at - start;
-    const int t_end = end - start < k.tiles ? end - start : k.tiles;
-    Column<DT> st;
-    attend<DT, ND, UNIFORM>(p, k, t, t_end, 1, st);
-    const float sum = column_sum(st.sum);
-    const int unit = h * units + u;
-    if (t == 0 && lane == 0) p.stream_info[1 + unit] = start;
-    const int64_t r = k.row0 + col;
-    if (r < k.rows) {
-      const int dim = p.c.dim;
-      if (t == 0 && t_end == k.tiles) {
-        const int64_t tok = r / p.group;
-        const int64_t o = (k.sp.t0 + tok) * p.o_ts + (h * p.group + (r - tok * p.group)) * p.o_hs;
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt)
-          if (16 * dt < dim)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              store_elem(p.out, o + 16 * dt + 4 * g + i, st.o[dt][i] * inv, p.dtype);
-      } else {
-        const int64_t slot = ((int64_t)me + unit) * kRows + col;
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt)
-          if (16 * dt < dim)
-            *(f32x4*)&p.part_o[slot * dim + 16 * dt + 4 * g] =
-                f32x4{st.o[dt][0], st.o[dt][1], st.o[dt][2], st.o[dt][3]};
-        if (g == 0) {
-          p.part_ml[2 * slot] = st.mx;
-          p.part_ml[2 * slot + 1] = sum;
-        }
-      }
-    }
-    at = start + t_end;
-  }
+  attend<DT, ND, UNIFORM>(p, k, split * p.split_tiles + wave, t_end, W, st);
+  join_waves<DT, W>(p, k, st, lds, n_splits <= 1, split * p.T * p.heads);
 }
 
 }  // namespace attn

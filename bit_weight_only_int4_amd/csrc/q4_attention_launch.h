@@ -6,15 +6,23 @@
 
 namespace q4 {
 
+template <int DT, int ND, int W, bool UNIFORM>
+static hipError_t launch_attention_waves(const AttnParams& p, hipStream_t s) {
+  using namespace attn;
+  const size_t lds = (size_t)W * kRows * (16 * DT + 6) * sizeof(float);
+  if (lds > 65536) {
+    const hipError_t e = hipFuncSetAttribute((const void*)attention_kernel<DT, ND, W, UNIFORM>,
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
+    if (e != hipSuccess) return e;
+  }
+  const dim3 grid((unsigned)((int64_t)p.batch * p.c.heads * p.row_blocks * p.splits));
+  hipLaunchKernelGGL((attention_kernel<DT, ND, W, UNIFORM>), grid, dim3(64 * W), lds, s, p);
+  return hipGetLastError();
+}
+
 template <int DT, int ND, bool UNIFORM>
 static hipError_t launch_attention_pages(const AttnParams& p, hipStream_t s) {
   using namespace attn;
-  if (p.stream_waves) {
-    const size_t bytes = (size_t)p.batch * p.row_blocks * sizeof(int32_t);
-    hipLaunchKernelGGL((attention_stream_kernel<DT, ND, UNIFORM>),
-                       dim3((unsigned)(p.stream_waves / kWaves)), dim3(kThreads), bytes, s, p);
-    return hipGetLastError();
-  }
   if (p.block_rows > kRows) {
     const size_t bytes = (size_t)4 * (4 * ((DT + 3) / 4) + DT) * 1024;
     const dim3 grid((unsigned)((int64_t)p.batch * p.c.heads * p.row_blocks * p.splits));
@@ -28,16 +36,10 @@ static hipError_t launch_attention_pages(const AttnParams& p, hipStream_t s) {
     hipLaunchKernelGGL(run, grid, dim3(kThreads), bytes, s, p);
     return hipGetLastError();
   }
-  const size_t lds = (size_t)(kWaves * kRows * (16 * DT + 4) + 2 * kWaves * kRows) * sizeof(float);
-  if (lds > 65536) {
-    const hipError_t e =
-        hipFuncSetAttribute((const void*)attention_kernel<DT, ND, UNIFORM>,
-                            hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    if (e != hipSuccess) return e;
-  }
-  const dim3 grid((unsigned)((int64_t)p.batch * p.c.heads * p.row_blocks * p.splits));
-  hipLaunchKernelGGL((attention_kernel<DT, ND, UNIFORM>), grid, dim3(kThreads), lds, s, p);
-  return hipGetLastError();
+  // where CUs have a workgroup or two at most, eight waves shorten each
+  if constexpr (DT <= 8)
+    if (p.few) return launch_attention_waves<DT, ND, 8, UNIFORM>(p, s);
+  return launch_attention_waves<DT, ND, 4, UNIFORM>(p, s);
 }
 
 template <int DT, int ND>

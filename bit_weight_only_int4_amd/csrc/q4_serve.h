@@ -58,17 +58,14 @@ struct AttnParams {
   int32_t block_rows;           // query rows of a workgroup: 16, or 64 or 128 (attention_wide_kernel)
   int32_t row_blocks;           // per sequence and kv head
   int32_t splits;               // workgroups along the keys (grid)
+  int32_t few;                  // few workgroups: eight waves in each
   int32_t split_tiles;          // tiles of 64 keys each of them takes
-  // parts of outputs, and their rows' maximum (log2) and sum: [splits][T *
-  // heads][dim] and [2], or [waves + units][16 rows][dim] and [2]
-  float* part_o;
-  float* part_ml;
-  int32_t stream_waves;         // > 0: attention_stream_kernel
-  int32_t* stream_info;         // piece, then the first tile of each unit on the line
+  float* part_o;                // [splits][T * heads][dim]
+  float* part_ml;               // [splits][T * heads][2]: maximum (log2), sum
 };
 
 struct AttnPlan {
-  int32_t max_rows, block_rows, row_blocks, splits, split_tiles, stream_waves;
+  int32_t max_rows, block_rows, row_blocks, splits, split_tiles, few;
   size_t parts;  // rows of partial outputs in the workspace
   size_t workspace;
 };

@@ -295,12 +295,11 @@ q4_status q4_attention(const void* q, int64_t q_ts, int64_t q_hs, void* out, int
   p.max_rows = pl.max_rows;
   p.block_rows = pl.block_rows;
   p.row_blocks = pl.row_blocks;
+  p.few = pl.few;
   p.splits = pl.splits;
   p.split_tiles = pl.split_tiles;
   p.part_o = (float*)workspace;
   p.part_ml = p.part_o + pl.parts * head_dim;
-  p.stream_waves = pl.stream_waves;
-  p.stream_info = (int32_t*)(p.part_ml + 2 * pl.parts);
   return status_of(q4::launch_attention(p, (hipStream_t)stream));
 }
 
