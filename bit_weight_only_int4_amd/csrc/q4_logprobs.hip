@@ -239,8 +239,8 @@ __device__ __forceinline__ float logprob_of(float x, const Stats& a) {
   return (x - a.m) - log2_fast(a.s) * kLn2;
 }
 
-// The target's logit, loaded before the sums are known: 0 and no target, NaN
-// where it is past the row.
+// The target's logit, loaded before the sums are known (NaN where the target
+// is past the row), and whether there is a target.
 struct Target {
   float x;
   bool is;
