@@ -274,10 +274,10 @@ def launch_times(suite, torch, reps=64):
 
 
 def source_digest():
-    """The digest the build stamps beside the library: HIP sources and the C
-    header, comments and blank space removed."""
+    """The digest of the layer's HIP sources and C header, comments and blank
+    space removed."""
     from bit_weight_only_int4_amd import build as hip_build
-    return hip_build.source_digest()
+    return hip_build.layer_digest()
 
 
 def stored_traffic():

@@ -38,11 +38,12 @@ CFLAGS = [
 ]
 
 
-def source_digest() -> str:
-    """sha256 over the HIP sources and the C headers with comments and blank
-    space removed: edits to comments alone keep it."""
+# sources of the operators around the layer (include/q4serve.h)
+SERVE = ("q4serve.h", "q4_serve", "q4_kv", "q4_attention", "q4_logprobs")
+
+
+def _digest(files) -> str:
     h = hashlib.sha256()
-    files = sorted(glob.glob(os.path.join(CSRC, "*"))) + sorted(glob.glob(os.path.join(INCLUDE, "*.h")))
     for f in files:
         with open(f) as fh:
             text = fh.read()
@@ -51,6 +52,22 @@ def source_digest() -> str:
         h.update(os.path.basename(f).encode())
         h.update(" ".join(text.split()).encode())
     return h.hexdigest()
+
+
+def _sources():
+    return sorted(glob.glob(os.path.join(CSRC, "*"))) + sorted(glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
+def source_digest() -> str:
+    """sha256 over the HIP sources and the C headers with comments and blank
+    space removed: edits to comments alone keep it."""
+    return _digest(_sources())
+
+
+def layer_digest() -> str:
+    """The same over the 4-bit layer's sources alone: measurements of the
+    layer hold as long as these do."""
+    return _digest(f for f in _sources() if not os.path.basename(f).startswith(SERVE))
 
 
 def stamp_path(lib: str) -> str:
