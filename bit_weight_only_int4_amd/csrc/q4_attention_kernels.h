@@ -26,6 +26,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "q4_kv.h"
 #include "q4_serve.h"
 #include "q4_serve_device.h"
@@ -133,12 +135,47 @@ __device__ __forceinline__ Block block_of(const AttnParams& p, int b, int h, int
   return k;
 }
 
-// Where the 16 tokens at token0 (a multiple of 16) of the sequence lie: their
-// page, -1 if it is not in the cache, -2 if no query sees them.
-__device__ __forceinline__ int32_t segment_page(const AttnParams& p, const int32_t* row,
+// The page that holds the 16 tokens at token0 (a multiple of 16) of the
+// sequence, given its table entry: -1 if it is not in the cache, -2 if no query
+// sees them.
+__device__ __forceinline__ int32_t segment_page(const AttnParams& p, int32_t raw,
                                                 const KeyRange& keys, int64_t token0) {
-  if (token0 + 16 <= keys.lo || token0 >= keys.hi) return -2;
-  return page_at(row, p.c.max_pages, p.c.pages, token0 >> p.c.page_log2);
+  const int32_t page = page_checked(raw, p.c.max_pages, p.c.pages, token0 >> p.c.page_log2);
+  return token0 + 16 <= keys.lo || token0 >= keys.hi ? -2 : page;
+}
+
+// A lane's pages of a tile: of the keys that it loads, and of its 16 tokens
+// (the same where one page covers the tile; then it has a token that is seen).
+struct Pages {
+  int32_t key, own;
+};
+
+template <bool UNIFORM>
+__device__ __forceinline__ Pages load_pages(const AttnParams& p, const int32_t* table,
+                                            int64_t token0) {
+  const int lane = threadIdx.x & 63;
+  Pages r;
+  r.own = page_raw(table, p.c.max_pages,
+                   (token0 + (UNIFORM ? 0 : 16 * (lane >> 4))) >> p.c.page_log2);
+  r.key = UNIFORM ? r.own
+                  : page_raw(table, p.c.max_pages,
+                             (token0 + 16 * ((lane & 15) >> 2)) >> p.c.page_log2);
+  return r;
+}
+
+template <bool UNIFORM>
+__device__ __forceinline__ Pages check_pages(const AttnParams& p, const Pages& raw,
+                                             const KeyRange& keys, int64_t token0) {
+  const int lane = threadIdx.x & 63;
+  Pages r;
+  if (UNIFORM) {
+    r.own = r.key = page_checked(__builtin_amdgcn_readfirstlane(raw.own), p.c.max_pages, p.c.pages,
+                                 token0 >> p.c.page_log2);
+  } else {
+    r.own = segment_page(p, raw.own, keys, token0 + 16 * (lane >> 4));
+    r.key = segment_page(p, raw.key, keys, token0 + 16 * ((lane & 15) >> 2));
+  }
+  return r;
 }
 
 // Elements d0 .. d0 + 15 of a query row as fp32, 16 bytes at a time where the
@@ -350,11 +387,13 @@ __device__ __forceinline__ void tile_values(const i32x4 (&vd)[DT], const i32x4 (
   }
 }
 
-// A tile's operands: keys, values, the lane's scales and page.
+// A tile's operands: keys, values, the lane's scales, and whether its page is
+// in the cache (else the scales stand for NaN).
 template <int NS, int DT>
 struct Tile {
   i32x4 kd[4][NS], vd[DT];
   float ks, vs;
+  bool k_in, v_in;
 };
 
 // A wave's tiles t, t + step, ... below t_end of a block's keys, into the
@@ -373,22 +412,7 @@ __device__ __forceinline__ void attend(const AttnParams& p, const Block& k, int 
   const int32_t* table = c.table + (int64_t)k.b * c.table_ld;
   const int page_mask = c.page - 1;
   const float nan = bits_f32(0x7fc00000u);
-  // page of the tile's keys that this lane loads, and of its 16 tokens
-  struct Pages {
-    int32_t key, own;
-  };
-  auto pages_of = [&](int tile) {
-    const int64_t token0 = (int64_t)(k.tile0 + tile) * kTile;
-    Pages r;
-    if (UNIFORM) {  // the tile has a token that is seen, and so its page has
-      r.own = r.key = __builtin_amdgcn_readfirstlane(
-          page_at(table, c.max_pages, c.pages, token0 >> c.page_log2));
-    } else {
-      r.own = segment_page(p, table, k.keys, token0 + 16 * g);
-      r.key = segment_page(p, table, k.keys, token0 + 16 * (col >> 2));
-    }
-    return r;
-  };
+  auto first_token = [&](int tile) { return (int64_t)(k.tile0 + tile) * kTile; };
   // Addresses are a 64-bit base of the page, of the wave where one page covers
   // the tile, and 32-bit offsets of the lane in it that do not change.
   uint32_t k_off[NS];
@@ -398,36 +422,37 @@ __device__ __forceinline__ void attend(const AttnParams& p, const Block& k, int 
     k_off[s] = (uint32_t)(((UNIFORM ? 16 * (col >> 2) : 0) + (col & 3)) * dim + (d < dim ? d : 0));
   }
   const uint32_t v_off = (uint32_t)((col << c.page_log2) + (UNIFORM ? 16 * g : 0));
-  // what is not seen, or not in the cache, is read from page 0: its scores
-  // are masked, or NaN by their scale
+  // What is not seen, or not in the cache, is read from page 0: its scores are
+  // masked, or NaN by their scale.  Scales load first: they are needed first.
   auto load_keys = [&](int tile, const Pages& pg, Tile<NS, DT>& o) {
-    const int64_t token0 = (int64_t)(k.tile0 + tile) * kTile;
-    const int slot = (int)((token0 + (UNIFORM ? 0 : 16 * (col >> 2))) & page_mask);
+    const int slot = (int)((first_token(tile) + (UNIFORM ? 0 : 16 * (col >> 2))) & page_mask);
+    o.k_in = pg.own >= 0;
+    o.ks = c.ks[(int64_t)(pg.own > 0 ? pg.own : 0) * c.heads + k.h];
     const int8_t* base =
         c.k + ((((int64_t)(pg.key > 0 ? pg.key : 0) * c.heads + k.h) << c.page_log2) + slot) * dim;
 #pragma unroll
     for (int a = 0; a < 4; ++a)
 #pragma unroll
       for (int s = 0; s < NS; ++s) o.kd[a][s] = *(const i32x4*)(base + 4 * a * dim + k_off[s]);
-    o.ks = pg.own >= 0 ? c.ks[(int64_t)pg.own * c.heads + k.h] : nan;
   };
   auto load_values = [&](int tile, const Pages& pg, Tile<NS, DT>& o) {
-    const int64_t token0 = (int64_t)(k.tile0 + tile) * kTile;
     const int64_t ph = (int64_t)(pg.own > 0 ? pg.own : 0) * c.heads + k.h;
+    o.v_in = pg.own >= 0;
+    o.vs = c.vs[ph];
     const int8_t* v = c.v + ph * ((int64_t)dim << c.page_log2) +
-                      ((token0 + (UNIFORM ? 0 : 16 * g)) & page_mask);
+                      ((first_token(tile) + (UNIFORM ? 0 : 16 * g)) & page_mask);
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt)
       o.vd[dt] = *(const i32x4*)(v + ((dt < d16 ? 16 * dt : 0) << c.page_log2) + v_off);
-    o.vs = pg.own >= 0 ? c.vs[ph] : nan;
   };
   Tile<NS, DT> cur;
-  Pages pg{0, 0}, pg_next{0, 0};  // of the tile at hand and the next
   column_init(st);
   if (t >= t_end) return;
-  pg = pages_of(t);
+  // pages of the tile at hand, and the table entries of the next
+  Pages pg = check_pages<UNIFORM>(p, load_pages<UNIFORM>(p, table, first_token(t)), k.keys,
+                                  first_token(t));
   load_keys(t, pg, cur);
-  if (t + step < t_end) pg_next = pages_of(t + step);
+  Pages raw = load_pages<UNIFORM>(p, table, first_token(t + step));
 
   // the lane's query row and the positions it sees
   const int64_t r = k.row0 + col;
@@ -448,29 +473,33 @@ __device__ __forceinline__ void attend(const AttnParams& p, const Block& k, int 
   const float q_unit = row_digits<NS, ND>(
       p, (k.sp.t0 + tok) * p.q_ts + (int64_t)head * p.q_hs, valid, g, qd);
 
-  for (; t < t_end; t += step) {
-    const int64_t token0 = (int64_t)(k.tile0 + t) * kTile;
+  // The last tile apart: with the loads of a next tile under a condition every
+  // wait for this one's values would wait for them as well.
+  auto one_tile = [&](auto more) {
+    const int64_t token0 = first_token(t);
     load_values(t, pg, cur);
     float sc[4][4];
     tile_scores<NS, ND>(cur.kd, qd, sc);
-    const float unit = q_unit * cur.ks;
-    if (t + step < t_end) {
-      load_keys(t + step, pg_next, cur);
-      pg = pg_next;
-      if (t + 2 * step < t_end) pg_next = pages_of(t + 2 * step);
+    const float unit = q_unit * (cur.k_in ? cur.ks : nan), vs = cur.v_in ? cur.vs : nan;
+    if constexpr (decltype(more)::value) {
+      pg = check_pages<UNIFORM>(p, raw, k.keys, first_token(t + step));
+      load_keys(t + step, pg, cur);
+      raw = load_pages<UNIFORM>(p, table, first_token(t + 2 * step));
     }
     i32x4 pd[ND];
     float alpha, w;
     if (token0 >= all_lo && token0 + kTile - 1 <= all_hi) {
-      tile_softmax<ND, false, UNIFORM>(sc, unit, cur.vs, 0, 0, st.mx, st.sum, pd, alpha, w);
+      tile_softmax<ND, false, UNIFORM>(sc, unit, vs, 0, 0, st.mx, st.sum, pd, alpha, w);
     } else {
       const int64_t base = token0 + 16 * g;
       const int lo = (int)(see_lo - base > 16 ? 16 : see_lo - base < 0 ? 0 : see_lo - base);
       const int hi = (int)(see_hi - base < -1 ? -1 : see_hi - base > 15 ? 15 : see_hi - base);
-      tile_softmax<ND, true, UNIFORM>(sc, unit, cur.vs, lo, hi, st.mx, st.sum, pd, alpha, w);
+      tile_softmax<ND, true, UNIFORM>(sc, unit, vs, lo, hi, st.mx, st.sum, pd, alpha, w);
     }
     tile_values<DT, ND>(cur.vd, pd, alpha, w, st.o);
-  }
+  };
+  for (; t + step < t_end; t += step) one_tile(std::true_type{});
+  one_tile(std::false_type{});
 }
 
 // Joins the parts of a workgroup's waves through LDS and writes them: finished

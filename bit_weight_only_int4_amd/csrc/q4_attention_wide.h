@@ -14,12 +14,14 @@
 // matrix unit needs half their time.  What keeps them few:
 //   * with two digits scores stay integers until the maximum is known;
 //   * two tiles share a maximum and their outputs' way from integers to fp32
-//     (one tile at a time took 1398 us where this takes 1277: 4 x 2048 tokens
-//     over 8192 each, 32 query and 8 kv heads of 128, bf16);
+//     (one tile at a time took 1398 us where this took 1277, and now takes 1208:
+//     4 x 2048 tokens over 8192 each, 32 query and 8 kv heads of 128, bf16);
 //   * the running maximum is only a reference that keeps the exponentials in
 //     range: outputs are rescaled when a row's maximum passes it by 2^8, not
 //     at every new maximum;
-//   * tiles that all rows of a wave see whole skip the masks.
+//   * tiles that all rows of a wave see whole skip the masks;
+//   * nothing after a pair's loads waits for them before the next barrier: a
+//     page number is checked a pair after its load (1277 to 1208 us).
 #pragma once
 
 #include "q4_attention_kernels.h"
@@ -141,21 +143,13 @@ __global__ __launch_bounds__(kThreads, DT <= 8 ? 2 : 1) void attention_wide_kern
   const float nan = bits_f32(0x7fc00000u);
   const int t_end = (split + 1) * p.split_tiles < k.tiles ? (split + 1) * p.split_tiles : k.tiles;
 
-  // pages of the tile's keys that this lane loads, and of its 16 tokens
-  auto pages_of = [&](int tile, int32_t& key, int32_t& own) {
-    const int64_t token0 = (int64_t)(k.tile0 + tile) * kTile;
-    if (UNIFORM) {
-      own = key = __builtin_amdgcn_readfirstlane(
-          page_at(table, c.max_pages, c.pages, token0 >> c.page_log2));
-    } else {
-      own = segment_page(p, table, k.keys, token0 + 16 * g);
-      key = segment_page(p, table, k.keys, token0 + 16 * (col >> 2));
-    }
-  };
+  auto first_token = [&](int tile) { return (int64_t)(k.tile0 + tile) * kTile; };
   float ks_next[2] = {0.0f, 0.0f}, vs_next[2] = {0.0f, 0.0f};
+  bool in_next[2] = {false, false};
   // every fourth operand of a tile, straight to LDS, and the lane's scales
-  auto fetch = [&](int tile, int buf, int at, int32_t key, int32_t own) {
-    const int64_t token0 = (int64_t)(k.tile0 + tile) * kTile;
+  auto fetch = [&](int tile, int buf, int at, const Pages& pg) {
+    const int32_t key = pg.key, own = pg.own;
+    const int64_t token0 = first_token(tile);
     const int k_slot = (int)((token0 + (UNIFORM ? 0 : 16 * (col >> 2))) & page_mask);
     const int v_slot = (int)((token0 + (UNIFORM ? 0 : 16 * g)) & page_mask);
     const int64_t ph = (int64_t)(own > 0 ? own : 0) * c.heads + k.h;
@@ -179,24 +173,27 @@ __global__ __launch_bounds__(kThreads, DT <= 8 ? 2 : 1) void attention_wide_kern
       }
       __builtin_amdgcn_global_load_lds((global_ptr)src, (lds_ptr)(to + f * 1024), 16, 0, 0);
     }
-    ks_next[at] = own >= 0 ? c.ks[ph] : nan;
-    vs_next[at] = own >= 0 ? c.vs[ph] : nan;
+    ks_next[at] = c.ks[ph];
+    vs_next[at] = c.vs[ph];
+    in_next[at] = own >= 0;
   };
-  int32_t key[2] = {0, 0}, own[2] = {0, 0}, buf = 0;
-  auto pages_of_pair = [&](int tile) {
+  int32_t buf = 0;
+  // table entries of the next pair of tiles, checked when it is fetched
+  Pages raw[2];
+  auto load_pair = [&](int tile) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if (tile + i < t_end) pages_of(tile + i, key[i], own[i]);
+    for (int i = 0; i < 2; ++i) raw[i] = load_pages<UNIFORM>(p, table, first_token(tile + i));
   };
   auto fetch_pair = [&](int tile, int to) {
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      if (tile + i < t_end) fetch(tile + i, to, i, key[i], own[i]);
+      if (tile + i < t_end)
+        fetch(tile + i, to, i, check_pages<UNIFORM>(p, raw[i], k.keys, first_token(tile + i)));
   };
   int t = split * p.split_tiles;
-  pages_of_pair(t);
+  load_pair(t);
   fetch_pair(t, 0);
-  pages_of_pair(t + 2);
+  load_pair(t + 2);
 
   // the lane's query rows and what they see
   Column<DT> st[NC];
@@ -232,9 +229,10 @@ __global__ __launch_bounds__(kThreads, DT <= 8 ? 2 : 1) void attention_wide_kern
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    const float ks[2] = {ks_next[0], ks_next[1]}, vs[2] = {vs_next[0], vs_next[1]};
+    const float ks[2] = {in_next[0] ? ks_next[0] : nan, in_next[1] ? ks_next[1] : nan};
+    const float vs[2] = {in_next[0] ? vs_next[0] : nan, in_next[1] ? vs_next[1] : nan};
     fetch_pair(t + 2, buf ^ 1);
-    pages_of_pair(t + 4);
+    load_pair(t + 4);
     // A wave in its matrix instructions goes before one in its exponentials, so
     // that the two units are busy at once (4% here)
     __builtin_amdgcn_s_setprio(0);

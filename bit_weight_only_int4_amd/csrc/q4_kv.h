@@ -34,11 +34,18 @@ Q4_HD SeqSpan seq_span(const int32_t* cu_new, const int32_t* lengths, int64_t b,
 }
 
 // The page number at entry `index` of a sequence's table row, or -1 if the
-// entry lies past the table or its page outside the cache.
+// entry lies past the table or its page outside the cache, in two steps: the
+// load, which any index may make (max_pages >= 1), and the check, which the
+// kernels put off until they need the page, as a use right after a load would
+// wait for it and for every load before it.
+Q4_HD int32_t page_raw(const int32_t* row, int64_t max_pages, int64_t index) {
+  return row[index < 0 ? 0 : index < max_pages ? index : max_pages - 1];
+}
+Q4_HD int32_t page_checked(int32_t raw, int64_t max_pages, int64_t pages, int64_t index) {
+  return (index >= 0 && index < max_pages && raw >= 0 && raw < pages) ? raw : -1;
+}
 Q4_HD int32_t page_at(const int32_t* row, int64_t max_pages, int64_t pages, int64_t index) {
-  if (index < 0 || index >= max_pages) return -1;
-  const int32_t p = row[index];
-  return (p >= 0 && p < pages) ? p : -1;
+  return page_checked(page_raw(row, max_pages, index), max_pages, pages, index);
 }
 
 // Pages that `n` consecutive positions can touch.
