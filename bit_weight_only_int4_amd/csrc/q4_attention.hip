@@ -12,13 +12,13 @@ namespace attn {
 __global__ __launch_bounds__(kThreads) void attention_join_many_kernel(AttnParams p) {
   extern __shared__ float lds[];  // weights [splits], then [parts at once][dim]
   __shared__ float red[2 * kWaves];
-  const int64_t rr = blockIdx.x % p.max_rows;
-  const uint32_t bh = blockIdx.x / p.max_rows;
-  const Block k = block_of(p, bh / p.c.heads, bh % p.c.heads, (int)(rr / p.block_rows));
+  const uint32_t rr = blockIdx.x % (uint32_t)p.max_rows;
+  const uint32_t bh = blockIdx.x / (uint32_t)p.max_rows;
+  const Block k = block_of(p, bh / p.c.heads, bh % p.c.heads, (int)((uint32_t)rr / (uint32_t)p.block_rows));
   if (rr >= k.rows) return;
   const int n = (k.tiles + p.split_tiles - 1) / p.split_tiles;
   if (n <= 1) return;
-  const int64_t tk = rr / p.group;
+  const int64_t tk = row_token(p, rr);
   const int64_t tq = k.sp.t0 + tk, hq = k.h * p.group + (rr - tk * p.group);
   const int64_t at = tq * p.heads + hq, stride = p.T * p.heads;
   const int64_t out = tq * p.o_ts + hq * p.o_hs;
@@ -72,7 +72,8 @@ __global__ __launch_bounds__(kThreads) void attention_join_many_kernel(AttnParam
 }
 
 // Joins few splits: dim / 4 threads a query row, so that many rows share a
-// workgroup.
+// workgroup; maxima, sums and outputs of kJoinAtOnce parts load together.
+constexpr int kJoinAtOnce = 8;
 __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnParams p) {
   const int quads = p.c.dim >> 2, at_once = kThreads / quads;
   const int mine = threadIdx.x / quads, d = 4 * (threadIdx.x - mine * quads);
@@ -80,25 +81,38 @@ __global__ __launch_bounds__(kThreads) void attention_join_kernel(AttnParams p) 
   const int64_t rr = (int64_t)(blockIdx.x % per_bh) * at_once + mine;
   const uint32_t bh = blockIdx.x / per_bh;
   if (mine >= at_once || rr >= p.max_rows) return;
-  const Block k = block_of(p, bh / p.c.heads, bh % p.c.heads, (int)(rr / p.block_rows));
+  const Block k = block_of(p, bh / p.c.heads, bh % p.c.heads, (int)((uint32_t)rr / (uint32_t)p.block_rows));
   if (rr >= k.rows) return;
   const int n = (k.tiles + p.split_tiles - 1) / p.split_tiles;
   if (n <= 1) return;
-  const int64_t tk = rr / p.group;
+  const int64_t tk = row_token(p, rr);
   const int64_t tq = k.sp.t0 + tk, hq = k.h * p.group + (rr - tk * p.group);
   const int64_t at = tq * p.heads + hq, stride = p.T * p.heads;
-  float m = -__builtin_inff();
-#pragma unroll 4
-  for (int s = 0; s < n; ++s) m = fmaxf(m, p.part_ml[2 * (at + s * stride)]);
-  const float ref = m > -__builtin_inff() ? m : 0.0f;
+  float m = -__builtin_inff(), den = 0.0f;
   f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-  float den = 0.0f;
-#pragma unroll 4
-  for (int s = 0; s < n; ++s) {
-    const int64_t a = at + s * stride;
-    const float f = exp2_fast(p.part_ml[2 * a] - ref), ds = p.part_ml[2 * a + 1];
-    den += ds != ds ? ds : f * ds;  // a part without a maximum: 0, or NaN
-    acc += f * *(const f32x4*)&p.part_o[a * p.c.dim + d];
+  for (int s = 0; s < n; s += kJoinAtOnce) {
+    float top[kJoinAtOnce], sum[kJoinAtOnce];
+    f32x4 o[kJoinAtOnce];
+#pragma unroll
+    for (int i = 0; i < kJoinAtOnce; ++i) {
+      const int64_t a = at + (s + i < n ? s + i : n - 1) * stride;
+      top[i] = p.part_ml[2 * a];
+      sum[i] = p.part_ml[2 * a + 1];
+      o[i] = *(const f32x4*)&p.part_o[a * p.c.dim + d];
+    }
+    const float before = m;
+#pragma unroll
+    for (int i = 0; i < kJoinAtOnce; ++i) m = fmaxf(m, top[i]);
+    const float ref = m > -__builtin_inff() ? m : 0.0f, keep = exp2_fast(before - ref);
+    den *= keep;
+    acc *= keep;
+#pragma unroll
+    for (int i = 0; i < kJoinAtOnce; ++i) {
+      if (s + i >= n) break;
+      const float f = exp2_fast(top[i] - ref);
+      den += sum[i] != sum[i] ? sum[i] : f * sum[i];  // a part without a maximum: 0, or NaN
+      acc += f * o[i];
+    }
   }
   const float inv = den == 0.0f ? 0.0f : 1.0f / den;
 #pragma unroll
@@ -116,14 +130,25 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Which kernel, and how much of it.
 //
-// Where sequences may bring kWideMin rows to a kv head, and there are kWideAll
-// in all, the wide kernel, whose workgroups share keys and values between 128
-// rows, or 64 where those would leave CUs without a workgroup.  Below, its
-// barriers and part-filled blocks cost more than the sharing gives (8
-// sequences over 2000 to 4000 tokens, 32 query and 8 kv heads of 128: with 64
-// rows of each kv head 43.9 us against 38.7 of 16-row workgroups in bf16 and
-// 47.9 against 40.2 in fp32, with 128 52.6 against 57.6 and 63.8 against 61.2,
-// with 192 54.7 against 80.6 and 64.5 against 85.2).
+// Where sequences may bring more rows to a kv head than two blocks of 16, and
+// there is work enough, the wide kernel, whose workgroups share keys and values
+// between 128 rows, or 64 where those would leave CUs without a workgroup.
+// Enough is kWideAll rows in all, or kWideWork rows times tiles, with the keys
+// split into pieces of at least kWideTiles tiles.  Below, its barriers and its
+// longer way to the first key cost more than the sharing gives.  Bf16, 32 query
+// and 8 kv heads of 128, 16-row workgroups against wide ones, us:
+//   new tokens x sequences over positions   rows   rows x tiles   16-row   wide
+//   128 x 1 over 1000                       4096          2^16      11.9   21.8
+//   64 x 1 over 4000                        2048          2^17      22.2   26.0
+//   64 x 4 over 1000                        8192          2^17      18.2   25.2
+//   128 x 1 over 4000                       4096          2^18      33.5   33.4
+//   64 x 1 over 16000                       2048          2^19      54.1   40.8
+//   32 x 4 over 16000                       4096          2^20       100   67.9
+//   256 x 4 over 256                       32768          2^17      31.2   20.4
+//   64 x 64 over 64                       131072          2^17       105   50.4
+//   16 x 64 over 2000                      32768          2^20       165    105
+//   12 x 16 over 4000                       6144          2^19      53.9   43.3
+//   8 x 256 over 100 (32 rows a head)      65536          2^17      61.6   78.1
 //
 // Else 16 rows a workgroup.  The keys of a row block go to several workgroups,
 // each at least kMinTiles tiles, where row blocks alone do not give every CU
@@ -141,20 +166,23 @@ AttnPlan plan_attention(int32_t dtype, int64_t T, int64_t batch, int64_t heads, 
                         int64_t window) {
   (void)dtype;
   (void)page;
-  constexpr int64_t kTargetBlocks = 256, kWideTarget = 512, kMinTiles = 4, kWideTiles = 16;
-  constexpr int64_t kRagged = 4, kRaggedTiles = 24, kWideMin = 96, kWideAll = 8192;
+  constexpr int64_t kTargetBlocks = 256, kWideTarget = 512, kMinTiles = 4, kWideTiles = 12;
+  constexpr int64_t kRagged = 4, kRaggedTiles = 24, kWideMin = 33, kWideAll = 16384, kWideWork = 1 << 18;
   AttnPlan pl{};
   const int64_t group = heads / kv_heads;
-  const bool wide = max_new * group >= kWideMin && batch * kv_heads * max_new * group >= kWideAll;
-  pl.max_rows = (int32_t)(max_new * group);
   constexpr int kBlock = attn::kWaves * attn::kRows;
+  // positions that a block's queries span
+  auto span_of = [&](int64_t rows) {
+    return window > 0 && window + rows < max_len ? window + rows : max_len;
+  };
+  const int64_t rows = batch * kv_heads * max_new * group;
+  const bool wide = max_new * group >= kWideMin &&
+                    (rows >= kWideAll || rows * ceil_div(span_of(kBlock), attn::kTile) >= kWideWork);
+  pl.max_rows = (int32_t)(max_new * group);
   const bool large = batch * kv_heads * ceil_div(max_new * group, 2 * kBlock) >= 512;
   pl.block_rows = !wide ? attn::kRows : large ? 2 * kBlock : kBlock;
   pl.row_blocks = (int32_t)ceil_div(max_new * group, pl.block_rows);
-  // a block's queries span at most block_rows positions
-  int64_t span = max_len;
-  if (window > 0 && window + pl.block_rows < span) span = window + pl.block_rows;
-  int64_t tiles = ceil_div(span, attn::kTile) + (window > 0 ? 1 : 0);
+  int64_t tiles = ceil_div(span_of(pl.block_rows), attn::kTile) + (window > 0 ? 1 : 0);
   if (tiles < 1) tiles = 1;
   const int64_t blocks = batch * kv_heads * pl.row_blocks;
   const int64_t target = wide ? kWideTarget : kTargetBlocks, least = wide ? kWideTiles : kMinTiles;
@@ -175,7 +203,7 @@ hipError_t launch_attention(const AttnParams& p, hipStream_t s) {
                                                : launch_attention_digits<2>(p, s);
   if (e != hipSuccess || p.splits <= 1) return e;
   const int64_t bh = (int64_t)p.batch * p.c.heads, at_once = attn::kThreads / (p.c.dim / 4);
-  if (p.splits > 16) {
+  if (p.splits > attn::kJoinAtOnce) {
     const size_t lds = (p.splits + (size_t)at_once * p.c.dim) * sizeof(float);
     hipLaunchKernelGGL(attn::attention_join_many_kernel, dim3((unsigned)(bh * p.max_rows)),
                        dim3(attn::kThreads), lds, s, p);

@@ -120,6 +120,12 @@ struct Block {
   KeyRange keys;
 };
 
+// The token of a query row: rows are below 2^31 + 128, and a division of 64
+// bits takes a hundred instructions on the way to the first key.
+__device__ __forceinline__ int64_t row_token(const AttnParams& p, int64_t row) {
+  return (uint32_t)row / (uint32_t)p.group;
+}
+
 __device__ __forceinline__ Block block_of(const AttnParams& p, int b, int h, int rb) {
   Block k;
   k.h = h;
@@ -128,8 +134,8 @@ __device__ __forceinline__ Block block_of(const AttnParams& p, int b, int h, int
   k.rows = (int64_t)k.sp.n * p.group;
   k.row0 = (int64_t)rb * p.block_rows;
   const int64_t last = k.row0 + p.block_rows < k.rows ? k.row0 + p.block_rows : k.rows;
-  k.keys = key_range(k.sp.pos0 + k.row0 / p.group, k.sp.pos0 + (last - 1) / p.group, p.window,
-                     p.max_len);
+  k.keys = key_range(k.sp.pos0 + row_token(p, k.row0),
+                     k.sp.pos0 + row_token(p, last > 0 ? last - 1 : 0), p.window, p.max_len);
   k.tile0 = (int)(k.keys.lo / kTile);
   k.tiles = k.keys.hi > k.keys.lo ? (int)((k.keys.hi + kTile - 1) / kTile) - k.tile0 : 0;
   return k;
@@ -457,7 +463,7 @@ __device__ __forceinline__ void attend(const AttnParams& p, const Block& k, int 
   // the lane's query row and the positions it sees
   const int64_t r = k.row0 + col;
   const bool valid = r < k.rows;
-  const int64_t tok = valid ? r / p.group : 0;
+  const int64_t tok = valid ? row_token(p, r) : 0;
   const int head = k.h * p.group + (int)(valid ? r - tok * p.group : 0);
   const int64_t pos = valid ? k.sp.pos0 + tok : -1;
   const int64_t see_lo64 = p.window > 0 ? pos - p.window + 1 : 0;
@@ -465,7 +471,8 @@ __device__ __forceinline__ void attend(const AttnParams& p, const Block& k, int 
   const int64_t see_lo = see_lo64 > 0 ? see_lo64 : 0;
   // positions that every row of the block sees
   const int64_t last_row = (k.row0 + kRows < k.rows ? k.row0 + kRows : k.rows) - 1;
-  const int64_t pos_first = k.sp.pos0 + k.row0 / p.group, pos_last = k.sp.pos0 + last_row / p.group;
+  const int64_t pos_first = k.sp.pos0 + row_token(p, k.row0);
+  const int64_t pos_last = k.sp.pos0 + row_token(p, last_row);
   const int64_t all_hi = pos_first < k.keys.hi ? pos_first : k.keys.hi - 1;
   const int64_t all_lo = p.window > 0 ? pos_last - p.window + 1 : 0;
 
@@ -541,7 +548,7 @@ __device__ __forceinline__ void join_waves(const AttnParams& p, const Block& k, 
     const float si = ls[i * kRows + row];
     den += si != si ? si : f[i] * si;
   }
-  const int64_t tk = rr / p.group;
+  const int64_t tk = row_token(p, rr);
   const int64_t tq = k.sp.t0 + tk, hq = k.h * p.group + (rr - tk * p.group);
   const int64_t at = first + tq * p.heads + hq;
   const float inv = den == 0.0f ? 0.0f : 1.0f / den;  // no key seen: 0

@@ -205,7 +205,7 @@ __global__ __launch_bounds__(kThreads, DT <= 8 ? 2 : 1) void attention_wide_kern
   for (int n = 0; n < NC; ++n) {
     const int64_t r = wave_row + n * kRows + col;
     const bool valid = r < k.rows;
-    const int64_t tok = valid ? r / p.group : 0;
+    const int64_t tok = valid ? row_token(p, r) : 0;
     const int head = k.h * p.group + (int)(valid ? r - tok * p.group : 0);
     const int64_t pos = valid ? k.sp.pos0 + tok : -1;
     see_lo[n] = p.window > 0 && pos >= p.window ? pos - p.window + 1 : 0;
@@ -216,8 +216,8 @@ __global__ __launch_bounds__(kThreads, DT <= 8 ? 2 : 1) void attention_wide_kern
   }
   // positions that some and all of the wave's rows see
   const int64_t rows_end = wave_row + NC * kRows < k.rows ? wave_row + NC * kRows : k.rows;
-  const int64_t pos_first = k.sp.pos0 + wave_row / p.group;
-  const int64_t pos_last = k.sp.pos0 + (rows_end - 1) / p.group;
+  const int64_t pos_first = k.sp.pos0 + row_token(p, wave_row);
+  const int64_t pos_last = k.sp.pos0 + row_token(p, rows_end - 1);
   const bool idle = wave_row >= k.rows;
   const KeyRange some = key_range(pos_first, pos_last, p.window, k.keys.hi);
   const int64_t all_hi = pos_first < k.keys.hi ? pos_first : k.keys.hi - 1;
@@ -344,7 +344,7 @@ __global__ __launch_bounds__(kThreads, DT <= 8 ? 2 : 1) void attention_wide_kern
     const int64_t r = wave_row + n * kRows + col;
     const float sum = column_sum(st[n].sum);
     if (r >= k.rows) continue;
-    const int64_t tok = r / p.group;
+    const int64_t tok = row_token(p, r);
     const int64_t tq = k.sp.t0 + tok, hq = k.h * p.group + (r - tok * p.group);
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // no key seen: 0
     const int64_t at = (int64_t)split * p.T * p.heads + tq * p.heads + hq;

@@ -136,6 +136,18 @@ def test_chunks_over_long_contexts_are_split():
     check([40, 5] + FILL, [60, 2100] + FILL, 8, 2, 64, 16, "f32", seed=3, max_len=100000)
 
 
+@pytest.mark.parametrize("new,lengths,heads,kv_heads,dim,page,dtype,window", [
+    ([70, 5], [17000, 900], 8, 2, 64, 64, "bf16", 0),
+    ([70, 5], [17000, 900], 8, 2, 128, 16, "f32", 0),
+    ([40, 33, 0], [14000, 33, 50], 16, 16, 32, 64, "f16", 0),
+    ([9, 9, 1] + [9] * 9, [20000, 19, 1] + [700] * 9, 8, 2, 80, 128, "f32", 0),
+    ([70, 66, 3], [30000, 29000, 3], 8, 2, 64, 32, "bf16", 20000),
+])
+def test_chunks_of_few_sequences_over_long_contexts(new, lengths, heads, kv_heads, dim, page, dtype, window):
+    """Few rows, so that rows times keys make the choice of the shared keys."""
+    check(new, lengths, heads, kv_heads, dim, page, dtype, window=window, seed=dim)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_many_blocks_of_chunks(dtype):
     """More than 512 workgroups of 128 rows by the bounds."""
