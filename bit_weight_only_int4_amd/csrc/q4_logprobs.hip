@@ -15,7 +15,7 @@
 // values in random order.  What reaches the last bar is ranked by counting.  A
 // full buffer is cut to its top_k best.  (A sorted list in the lanes, an entry
 // inserted at a time through ballots, took 75 us for 512 rows of 128257 and
-// top_k 5, where this takes 61 us and none at all 54 us.)
+// top_k 5, where this took 61; now 55, and none at all 49.)
 //
 // Bound by HBM reads for many rows; for a few rows, whose parts go to several
 // workgroups and are joined by a second launch, by latency.
@@ -592,12 +592,17 @@ LogprobPlan plan_logprobs(int64_t M, int64_t V, int64_t top_k, int32_t dtype) {
 
 hipError_t launch_logprobs(const LogprobParams& p, int32_t dtype, hipStream_t s) {
   const dim3 grid((unsigned)(p.M * p.splits));
-  // a long row of its own workgroup is shared by 16 waves
-  const bool wide = p.splits == 1 && p.V >= 16 * 64 * kChunk;
+  // A long row of its own workgroup is shared by eight waves while there are
+  // few rows.  Registers leave a CU 24 waves: with 16 a row the next row could
+  // not start beside it.  Waves a row, us (fp32, top_k 5): 512 x 128257 60.3
+  // with 16, 55.2 with 8, 54.7 with 4 (bf16 53.4, 43.4, 52.5); 300 x 128257
+  // 51.5, 42.1, 42.0; 512 x 16400 18.2 with 8, 14.1 with 4; 1024 x 128257 111,
+  // 96.5, 96.2; 2000 x 20000 106, 52.4, 40.2; 4096 x 32003 217, 113, 99.9.
+  const bool wide = p.splits == 1 && p.V >= 32 * 64 * kChunk && p.M < 1024;
 #define Q4_LOGPROBS(T)                                                                         \
   do {                                                                                         \
     if (wide)                                                                                  \
-      hipLaunchKernelGGL((logprobs_kernel<T, 16>), grid, dim3(1024), 0, s, p);                 \
+      hipLaunchKernelGGL((logprobs_kernel<T, 8>), grid, dim3(512), 0, s, p);                   \
     else                                                                                       \
       hipLaunchKernelGGL((logprobs_kernel<T, 4>), grid, dim3(256), 0, s, p);                   \
     if (p.splits > 1)                                                                          \

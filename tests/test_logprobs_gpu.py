@@ -70,6 +70,14 @@ def test_rows_and_parts(M, V, dtype):
     check(x, xd, t, 20)
 
 
+@pytest.mark.parametrize("M,V", [(300, 32767), (300, 32768), (280, 40003), (1030, 33000)])
+@pytest.mark.parametrize("dtype,k", [("f32", 0), ("f32", 32), ("bf16", 7)])
+def test_long_rows_without_parts(M, V, dtype, k):
+    need_gpu()
+    xd, x, t = logits_of(M, V, dtype, M)
+    check(x, xd, t, k)
+
+
 @pytest.mark.parametrize("k", [1, 2, 3, 19, 31, 32])
 def test_ties_go_to_the_lowest_index(k):
     need_gpu()
