@@ -580,12 +580,14 @@ __global__ __launch_bounds__(64 * W, DT <= 4 && W == 4 ? 3 : DT <= 8 ? 2 : 1) vo
   // workgroups go to the 8 XCDs in turn, so that neither the sequences' lengths
   // nor the splits that the short ones do not need load one XCD more than
   // another, and the row blocks of a head share an L2 where there are 8 heads.
+  // The last splits, which only long sequences have, come first, so that these
+  // do not end alone (32 sequences of 450 to 9000 tokens: 58 to 53 us).
   uint32_t id = blockIdx.x;
   const int h = id % p.c.heads;
   id /= p.c.heads;
   const int b = id % p.batch;
   id /= p.batch;
-  const int rb = id % p.row_blocks, split = id / p.row_blocks;
+  const int rb = id % p.row_blocks, split = p.splits - 1 - (int)(id / p.row_blocks);
   const Block k = block_of(p, b, h, rb);
   if (k.row0 >= k.rows) return;
   // a block whose tiles fit one split writes its output itself
