@@ -34,30 +34,43 @@ namespace {
 constexpr int kMaxTop = 32;
 constexpr int kChunk = 16;             // elements of a thread's step
 constexpr int32_t kNone = 0x7fffffff;  // index of an empty list entry
-constexpr int kPartStats = 4;          // m, S, W of a part (padded)
+constexpr int kPartStats = 4;          // m, s, W, c of a part
 constexpr int kMaxParts = 64;          // of a row: a lane each in the join
 
+// S is s + c, c what the additions to s have rounded off: a row whose largest
+// logit holds nearly all has S = 1 + r with a small r that its entropy and log
+// probabilities hang on.
 struct Stats {
-  float m, s, w;
+  float m, s, w, c;
 };
+
+// Adds to S.
+__device__ __forceinline__ void add_sum(float& s, float& c, float x) {
+  const float t = s + x, part = t - s;
+  c += (s - (t - part)) + (x - part);
+  s = t;
+}
 
 // Joins two; an empty side (m = -inf) leaves the other as it is.
 __device__ __forceinline__ Stats stats_join(const Stats& a, const Stats& b) {
   const float m = fmaxf(a.m, b.m);
-  if (m == -__builtin_inff()) return Stats{m, a.s + b.s, a.w + b.w};
+  if (m == -__builtin_inff()) return Stats{m, a.s + b.s, a.w + b.w, 0.0f};
   const float da = (a.m - m) * kLog2e, db = (b.m - m) * kLog2e;  // <= 0
   const float fa = exp2_fast(da), fb = exp2_fast(db);
   // a side too far below to count may overflow in d S (a NaN shows in its S)
   const float wa = fa > 0.0f ? fa * (a.w + da * a.s) : 0.0f;
   const float wb = fb > 0.0f ? fb * (b.w + db * b.s) : 0.0f;
   const float sa = a.s == 0.0f ? 0.0f : fa * a.s, sb = b.s == 0.0f ? 0.0f : fb * b.s;
-  return Stats{m, sa + sb, wa + wb};
+  Stats r{m, sa, wa + wb, fa * a.c + fb * b.c};
+  add_sum(r.s, r.c, sb);
+  return r;
 }
 
 __device__ __forceinline__ Stats stats_wave(Stats a) {
 #pragma unroll
   for (int m = 1; m < 64; m <<= 1)
-    a = stats_join(a, Stats{__shfl_xor(a.m, m, 64), __shfl_xor(a.s, m, 64), __shfl_xor(a.w, m, 64)});
+    a = stats_join(a, Stats{__shfl_xor(a.m, m, 64), __shfl_xor(a.s, m, 64), __shfl_xor(a.w, m, 64),
+                            __shfl_xor(a.c, m, 64)});
   return a;
 }
 
@@ -107,7 +120,7 @@ __device__ __forceinline__ float kth_of_groups(const uint32_t* keys, int k, int 
   return kth < 0x00800000u ? -__builtin_inff() : key_value(kth);  // -inf's key and below
 }
 
-// The largest of each W neighbouring lanes (W = 4 or 16), in every one of them.
+// The largest of each W neighbouring lanes (W = 4 or 8), in every one of them.
 template <int W>
 __device__ __forceinline__ float group_max(float v) {
   auto dpp = [&](auto ctrl) {
@@ -116,10 +129,7 @@ __device__ __forceinline__ float group_max(float v) {
   };
   v = fmaxf(v, dpp(std::integral_constant<int, 0xb1>{}));   // quad_perm 1 0 3 2
   v = fmaxf(v, dpp(std::integral_constant<int, 0x4e>{}));   // quad_perm 2 3 0 1
-  if (W == 16) {
-    v = fmaxf(v, dpp(std::integral_constant<int, 0x124>{}));  // row_ror 4
-    v = fmaxf(v, dpp(std::integral_constant<int, 0x128>{}));  // row_ror 8
-  }
+  if (W == 8) v = fmaxf(v, dpp(std::integral_constant<int, 0x141>{}));  // row_half_mirror
   return v;
 }
 
@@ -227,16 +237,21 @@ struct Result {
   float lse, entropy;
 };
 
+// ln (s + c), to a few roundings of itself also where S is close to 1.
+__device__ __forceinline__ float log_sum(const Stats& a) {
+  return __builtin_fmaf(a.c, __builtin_amdgcn_rcpf(a.s), log2_fast(a.s) * kLn2);
+}
+
 __device__ __forceinline__ Result finish(const Stats& a) {
   if (a.s == 0.0f) return Result{-__builtin_inff(), 0.0f};  // nothing but -inf
-  const float log_s = log2_fast(a.s) * kLn2;
+  const float log_s = log_sum(a);
   return Result{a.m + log_s, log_s - kLn2 * (a.w / a.s)};
 }
 
 // Log probability of x given the statistics: x - m first, as both may be large.
 __device__ __forceinline__ float logprob_of(float x, const Stats& a) {
   if (a.s == 0.0f) return -__builtin_inff();
-  return (x - a.m) - log2_fast(a.s) * kLn2;
+  return (x - a.m) - log_sum(a);
 }
 
 // The target's logit, loaded before the sums are known (NaN where the target
@@ -322,7 +337,7 @@ __global__ __launch_bounds__(64 * W) void logprobs_kernel(LogprobParams p) {
 
   Target target{0.0f, false};
   if (p.splits == 1 && tid == 0) target = target_of<T>(p, row);
-  Stats st{-inf, 0.0f, 0.0f};
+  Stats st{-inf, 0.0f, 0.0f, 0.0f};
   Best best{best_val[wave], best_id[wave], 0, -inf, kNone};
   int step = 0;
   if (tid == 0) top_count = 0;
@@ -339,16 +354,17 @@ __global__ __launch_bounds__(64 * W) void logprobs_kernel(LogprobParams p) {
     // an empty sum stays 0 (d is -inf), one too far below may overflow in d S
     st.w = f > 0.0f ? f * (st.w + d * st.s) : 0.0f;
     st.s = f * st.s;
+    st.c = f * st.c;
     st.m = m;
-    float s = 0.0f, w = 0.0f;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f}, w = 0.0f;  // four, for fewer roundings
 #pragma unroll
     for (int e = 0; e < kChunk; ++e) {
       const float y = (v[e] - ref) * kLog2e;
       const float ex = exp2_fast(y);
-      s += ex;
+      s[e % 4] += ex;
       w = __builtin_fmaf(ex, fmaxf(y, -1e5f), w);  // y may be -inf; a NaN shows in s
     }
-    st.s += s;
+    add_sum(st.s, st.c, (s[0] + s[1]) + (s[2] + s[3]));
     st.w += w;
     if (k > 0) {
       if ((step & (step - 1)) == 0) {  // steps 0, 1, 2, 4, ...
@@ -474,6 +490,7 @@ __global__ __launch_bounds__(64 * W) void logprobs_kernel(LogprobParams p) {
       p.part[part * kPartStats] = st.m;
       p.part[part * kPartStats + 1] = st.s;
       p.part[part * kPartStats + 2] = st.w;
+      p.part[part * kPartStats + 3] = st.c;
     }
     rank_entries(entries, found, k, [&](int rank, float v, int32_t i) {
       p.part_val[part * k + rank] = v;
@@ -494,10 +511,10 @@ __global__ __launch_bounds__(256) void logprobs_join_kernel(LogprobParams p) {
   if (tid == 0) count = 0;
   Target target{0.0f, false};
   if (tid == 0) target = target_of<T>(p, row);
-  Stats st{-__builtin_inff(), 0.0f, 0.0f};
+  Stats st{-__builtin_inff(), 0.0f, 0.0f, 0.0f};
   if (lane < p.splits) {
     const float* q = p.part + (row * p.splits + lane) * kPartStats;
-    st = Stats{q[0], q[1], q[2]};
+    st = Stats{q[0], q[1], q[2], q[3]};
   }
   // a group is a part's best depth + 1, and its value the least of them: k of
   // the row are no less than that of the need-th group

@@ -243,3 +243,33 @@ def test_logprobs_replay_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(r, e)) and torch.equal(d, ed)
+
+
+@pytest.mark.parametrize("V", [5000, 40003, 128257])
+@pytest.mark.parametrize("M", [1, 300])
+def test_rows_that_one_logit_fills(M, V):
+    """Log probability and entropy next to 0, to a part of themselves.
+
+    The other terms sum to r = S - 1, about 10^-5 here.  ln S = log1p(r): the
+    largest logit's thread adds 1 to its step's sum in at most 5 additions that
+    round by 2^-24 each (the later ones keep what they round off), and each term
+    2^y errs by |y| 2^-23 + 2^-22 of itself with y to 2^5."""
+    need_gpu()
+    if M * V > 20_000_000:
+        V = 66_000
+    g = np.random.default_rng(V)
+    t = torch.from_numpy(g.normal(0, 0.5, (M, V))).float()
+    where = torch.from_numpy(g.integers(0, V, M))
+    t[torch.arange(M), where] = float(np.log(V) + 11.5)
+    x = t.double()
+    big = x.max(1, keepdim=True).values
+    e = torch.exp(x - big)
+    e[torch.arange(M), where] = 0.0
+    rest = e.sum(1)
+    lp = -torch.log1p(rest)
+    ent = -lp - (e * (x - big)).sum(1) / (1 + rest)
+    r = q4.token_logprobs(t.cuda(), where.cuda(), top_k=1)
+    tol = 5 * 2.0 ** -24 + 2.0 ** -17 * rest
+    assert ((r.logprob.double().cpu() - lp).abs() <= tol).all()
+    assert ((r.top_logprobs[:, 0].double().cpu() - lp).abs() <= tol).all()
+    assert ((r.entropy.double().cpu() - ent).abs() <= 5 * 2.0 ** -24 + 2.0 ** -17 * 40 * rest).all()
