@@ -150,6 +150,12 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 //   12 x 16 over 4000                       6144          2^19      53.9   43.3
 //   8 x 256 over 100 (32 rows a head)      65536          2^17      61.6   78.1
 //
+// 128 rows a workgroup of the wide kernel, except for fp32 queries up to heads
+// of 192: two row blocks of four digits a wave leave no registers there.  64
+// against 128 rows, us, 3 x 300 to 2048 tokens over up to 8192, heads of 32
+// 227 and 249, 64 229 and 251, 80 313 and 325, 96 371 and 354, 128 338 and 394,
+// 192 736 and 789, 256 (a wave a SIMD either way) 1120 and 984.
+//
 // Else 16 rows a workgroup.  The keys of a row block go to several workgroups,
 // each at least kMinTiles tiles, where row blocks alone do not give every CU
 // one (kTargetBlocks); and, where they do, to at most kRagged, each at least
@@ -164,7 +170,6 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 AttnPlan plan_attention(int32_t dtype, int64_t T, int64_t batch, int64_t heads, int64_t kv_heads,
                         int64_t dim, int64_t page, int64_t max_new, int64_t max_len,
                         int64_t window) {
-  (void)dtype;
   (void)page;
   constexpr int64_t kTargetBlocks = 256, kWideTarget = 512, kMinTiles = 4, kWideTiles = 12;
   constexpr int64_t kRagged = 4, kRaggedTiles = 24, kWideMin = 33, kWideAll = 16384, kWideWork = 1 << 18;
@@ -179,7 +184,8 @@ AttnPlan plan_attention(int32_t dtype, int64_t T, int64_t batch, int64_t heads, 
   const bool wide = max_new * group >= kWideMin &&
                     (rows >= kWideAll || rows * ceil_div(span_of(kBlock), attn::kTile) >= kWideWork);
   pl.max_rows = (int32_t)(max_new * group);
-  const bool large = batch * kv_heads * ceil_div(max_new * group, 2 * kBlock) >= 512;
+  const bool large = (dtype != Q4_DTYPE_F32 || dim > 192) &&
+                     batch * kv_heads * ceil_div(max_new * group, 2 * kBlock) >= 512;
   pl.block_rows = !wide ? attn::kRows : large ? 2 * kBlock : kBlock;
   pl.row_blocks = (int32_t)ceil_div(max_new * group, pl.block_rows);
   int64_t tiles = ceil_div(span_of(pl.block_rows), attn::kTile) + (window > 0 ? 1 : 0);
@@ -199,8 +205,8 @@ AttnPlan plan_attention(int32_t dtype, int64_t T, int64_t batch, int64_t heads, 
 }
 
 hipError_t launch_attention(const AttnParams& p, hipStream_t s) {
-  const hipError_t e = p.dtype == Q4_DTYPE_F32 ? launch_attention_digits<3>(p, s)
-                                               : launch_attention_digits<2>(p, s);
+  const hipError_t e = p.dtype == Q4_DTYPE_F32 ? launch_attention_digits<4>(p, s)
+                                               : launch_attention_digits<3>(p, s);
   if (e != hipSuccess || p.splits <= 1) return e;
   const int64_t bh = (int64_t)p.batch * p.c.heads, at_once = attn::kThreads / (p.c.dim / 4);
   if (p.splits > attn::kJoinAtOnce) {

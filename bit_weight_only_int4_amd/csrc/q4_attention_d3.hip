@@ -1,4 +1,4 @@
-// q4_attention_d3.hip -- attention for fp32 queries (three digits).
+// q4_attention_d3.hip -- attention for 16-bit queries (three digits).
 #include "q4_attention_launch.h"
 
 namespace q4 {

@@ -10,8 +10,18 @@
 // fp32.  The probabilities of a tile of 64 tokens are held the same way
 // against the tile's own largest (which is 1 for the largest score): the
 // tile's contribution is an exact integer sum, and running maximum, sum and
-// output are fp32.  Three digits keep 23 bits (fp32 queries), two keep 15
-// (16-bit queries, whose own rounding is 2^-8 or 2^-11).
+// output are fp32.
+//
+// Digits.  An element's own rounding is relative to itself, a digit's step to
+// the row's largest element (the tile's largest probability), so digits have
+// to reach past the type's bits by what elements lie apart: 16-bit queries
+// take three (23 bits), fp32 ones four (31).  With one fewer, which was
+// measured first, a query channel 200 times the others cost 16-bit outputs
+// 4e-3 of themselves and fp32 ones 1e-5, a first token with nine tenths of the
+// weight and no value 7e-3 and 3e-5; now 1e-5 and 5e-8, 3e-5 and 1e-7.  Its
+// price is in the prompt chunks, which the vector unit bounds (2890 tokens
+// over up to 5441: bf16 217 to 267 us, fp32 283 to 338); decode steps wait for
+// memory (64 sequences of 500 to 8000: 78 to 79).
 //
 // Layout.  A wave holds 16 query rows as the columns of both products:
 // S^T = K Q^T gives lane l the scores of column l % 16 for 4 rows of each of
@@ -43,11 +53,11 @@ constexpr int kThreads = 64 * kWaves;
 // largest integer that ND digits hold with the offsets of pack_digits
 template <int ND>
 __device__ __forceinline__ constexpr float digit_max() {
-  return ND == 3 ? 8323072.0f : 32512.0f;  // 127 * 256^(ND - 1)
+  return ND == 4 ? 2130706432.0f : 8323072.0f;  // 127 * 256^(ND - 1)
 }
 template <int ND>
 __device__ __forceinline__ constexpr uint32_t digit_bias() {
-  return ND == 3 ? 0x8080u : 0x80u;
+  return ND == 4 ? 0x808080u : 0x8080u;
 }
 
 // Digits of four integers, each given as X + digit_bias: word i holds digit i
@@ -59,22 +69,33 @@ __device__ __forceinline__ void pack_digits(uint32_t b0, uint32_t b1, uint32_t b
   const uint32_t lo = __builtin_amdgcn_perm(b1, b0, 0x05010400u);
   const uint32_t hi = __builtin_amdgcn_perm(b3, b2, 0x05010400u);
   w[0] = __builtin_amdgcn_perm(hi, lo, 0x05040100u) ^ 0x80808080u;
-  w[1] = __builtin_amdgcn_perm(hi, lo, 0x07060302u);
-  if constexpr (ND == 3) {
-    w[1] ^= 0x80808080u;
-    const uint32_t l2 = __builtin_amdgcn_perm(b1, b0, 0x0c0c0602u);
-    const uint32_t h2 = __builtin_amdgcn_perm(b3, b2, 0x0c0c0602u);
-    w[2] = __builtin_amdgcn_perm(h2, l2, 0x05040100u);
+  w[1] = __builtin_amdgcn_perm(hi, lo, 0x07060302u) ^ 0x80808080u;
+  const uint32_t l2 = __builtin_amdgcn_perm(b1, b0, 0x07030602u);
+  const uint32_t h2 = __builtin_amdgcn_perm(b3, b2, 0x07030602u);
+  w[2] = __builtin_amdgcn_perm(h2, l2, 0x05040100u);
+  if constexpr (ND == 4) {
+    w[2] ^= 0x80808080u;
+    w[3] = __builtin_amdgcn_perm(h2, l2, 0x07060302u);
   }
 }
 
+// x (0 <= x <= digit_max + 1/2) to the nearest integer, with digit_bias added.
+// Below 2^24 the sum with 2^23 and the bias holds it in the low bits.
+template <int ND>
+__device__ __forceinline__ uint32_t digit_bits(float p, float to_digits) {
+  if constexpr (ND == 4)
+    return (uint32_t)(int)__builtin_rintf(p * to_digits) + digit_bias<ND>();
+  else
+    return f32_bits(__builtin_fmaf(p, to_digits, 8388608.0f + (float)digit_bias<ND>()));
+}
+
 // sum_i acc_i 256^i in fp32.  The digit sums are below 2^22 in magnitude (64
-// or 256 products of at most 2^14), so the two low ones join exactly.
+// or 256 products of at most 2^14), so that two neighbours join exactly.
 template <int ND>
 __device__ __forceinline__ float join_digits(const int32_t (&a)[ND]) {
   const float low = (float)(a[1] * 256 + a[0]);
-  if constexpr (ND == 3) return __builtin_fmaf((float)a[2], 65536.0f, low);
-  return low;
+  if constexpr (ND == 4) return __builtin_fmaf((float)(a[3] * 256 + a[2]), 65536.0f, low);
+  return __builtin_fmaf((float)a[2], 65536.0f, low);
 }
 
 // Over the four lanes that hold a column, l % 16 apart: the rows of 16 lanes
@@ -241,7 +262,7 @@ __device__ __forceinline__ float row_digits(const AttnParams& p, int64_t at, boo
   const float a = bits_f32(amax);
   const int ex = __builtin_amdgcn_frexp_expf(a);  // a = m 2^ex, m in [1/2, 1)
   const float m = __builtin_amdgcn_frexp_mantf(a);
-  const int up = amax == 0 ? 0 : (ND == 3 ? 23 : 15) - ex - (m > 127.0f / 128.0f ? 1 : 0);
+  const int up = amax == 0 ? 0 : 8 * ND - 1 - ex - (m > 127.0f / 128.0f ? 1 : 0);
   const float sign = p.scale_log2 < 0.0f ? -1.0f : 1.0f;
 #pragma unroll
   for (int s = 0; s < NS; ++s)
@@ -356,7 +377,7 @@ __device__ __forceinline__ void tile_softmax(float (&sc)[4][4], float unit, floa
     uint32_t bits[4], out[ND];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      bits[i] = f32_bits(__builtin_fmaf(sc[a][i], to_digits, 8388608.0f + (float)digit_bias<ND>()));
+      bits[i] = digit_bits<ND>(sc[a][i], to_digits);
     pack_digits<ND>(bits[0], bits[1], bits[2], bits[3], out);
 #pragma unroll
     for (int i = 0; i < ND; ++i) pd[i][a] = (int32_t)out[i];

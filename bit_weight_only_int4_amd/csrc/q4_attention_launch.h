@@ -1,5 +1,5 @@
 // q4_attention_launch.h -- the attention kernel for one number of digits;
-// included by q4_attention_d2.hip and q4_attention_d3.hip.
+// included by q4_attention_d3.hip and q4_attention_d4.hip.
 #pragma once
 
 #include "q4_attention_wide.h"
@@ -26,8 +26,9 @@ static hipError_t launch_attention_pages(const AttnParams& p, hipStream_t s) {
   if (p.block_rows > kRows) {
     const size_t bytes = (size_t)4 * (4 * ((DT + 3) / 4) + DT) * 1024;
     const dim3 grid((unsigned)((int64_t)p.batch * p.c.heads * p.row_blocks * p.splits));
-    const auto run = p.block_rows == 2 * kWaves * kRows ? attention_wide_kernel<DT, ND, 2, UNIFORM>
-                                                        : attention_wide_kernel<DT, ND, 1, UNIFORM>;
+    auto run = attention_wide_kernel<DT, ND, 1, UNIFORM>;
+    if constexpr (ND == 3 || DT > 12)
+      if (p.block_rows == 2 * kWaves * kRows) run = attention_wide_kernel<DT, ND, 2, UNIFORM>;
     if (bytes > 65536) {
       const hipError_t e = hipFuncSetAttribute(
           (const void*)run, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);

@@ -9,19 +9,20 @@
 // lanes that read it (so that neither side has a bank conflict).  Two buffers:
 // the next pair of tiles loads while one is worked on, with one barrier a pair.
 //
-// Bound by the vector unit: with two digits a score takes 11 issue slots (4 of
-// them the exponential) and an output element 3 a pair of tiles, where the
-// matrix unit needs half their time.  What keeps them few:
-//   * with two digits scores stay integers until the maximum is known;
+// Bound by the vector unit: with three digits a score takes 14 issue slots (4
+// of them the exponential) and an output element 5 a pair of tiles.  What keeps
+// them few:
 //   * two tiles share a maximum and their outputs' way from integers to fp32
-//     (one tile at a time took 1398 us where this took 1277, and now takes 1208:
-//     4 x 2048 tokens over 8192 each, 32 query and 8 kv heads of 128, bf16);
+//     (one tile at a time took 1398 us where this took 1277, both with two
+//     digits: 4 x 2048 tokens over 8192 each, 32 query and 8 kv heads of 128,
+//     bf16; now 1532);
 //   * the running maximum is only a reference that keeps the exponentials in
 //     range: outputs are rescaled when a row's maximum passes it by 2^8, not
 //     at every new maximum;
 //   * tiles that all rows of a wave see whole skip the masks;
 //   * nothing after a pair's loads waits for them before the next barrier: a
-//     page number is checked a pair after its load (1277 to 1208 us).
+//     page number is checked a pair after its load (1277 to 1208 us with two
+//     digits).
 #pragma once
 
 #include "q4_attention_kernels.h"
@@ -34,28 +35,11 @@ constexpr float kSlack = 8.0f;                           // log2 that a maximum 
 typedef __attribute__((address_space(3))) void* lds_ptr;
 typedef const __attribute__((address_space(1))) void* global_ptr;
 
-// Scores of a tile before the maximum is taken: integers where two digits
-// make them (below 2^31: 256 products of 2^14 times 257), else fp32.
-template <int ND>
-struct Raw {
-  typedef float type;
-};
-template <>
-struct Raw<2> {
-  typedef int32_t type;
-};
-
-template <int ND>
-__device__ __forceinline__ typename Raw<ND>::type raw_join(const int32_t (&a)[ND]) {
-  if constexpr (ND == 2) return a[1] * 256 + a[0];
-  else return join_digits<ND>(a);
-}
-
 // The digits' range of pair_softmax: its exponentials may pass 1 by the
 // rounding of a product below kFarScore, 2^-8.
 template <int ND>
 __device__ __forceinline__ constexpr float pair_digit_max() {
-  return ND == 3 ? 8257536.0f : 32256.0f;  // 126 * 256^(ND - 1)
+  return ND == 4 ? 2113929216.0f : 8257536.0f;  // 126 * 256^(ND - 1)
 }
 constexpr float kFarScore = 65536.0f;
 
@@ -64,19 +48,19 @@ constexpr float kFarScore = 65536.0f;
 // maximum.  False, with nothing changed, where scores or scales are far out or
 // not finite (tile_softmax takes those).
 template <int ND>
-__device__ __forceinline__ bool pair_softmax(const typename Raw<ND>::type (&raw)[2][4][4],
+__device__ __forceinline__ bool pair_softmax(const float (&raw)[2][4][4],
                                              const float (&unit)[2], const float (&vs)[2],
                                              float& mx, float& sum, i32x4 (&pd)[2][ND],
                                              float& alpha, float& w) {
   float tops[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    typename Raw<ND>::type best = raw[t][0][0];
+    float best = raw[t][0][0];
 #pragma unroll
     for (int a = 0; a < 4; ++a)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) best = raw[t][a][i] > best ? raw[t][a][i] : best;
-    tops[t] = (float)best * unit[t];
+      for (int i = 0; i < 4; ++i) best = fmaxf(best, raw[t][a][i]);
+    tops[t] = best * unit[t];
   }
   const float top = column_max(fmaxf(tops[0], tops[1]));
   const bool fine = __builtin_fabsf(tops[0]) < kFarScore && __builtin_fabsf(tops[1]) < kFarScore &&
@@ -94,9 +78,9 @@ __device__ __forceinline__ bool pair_softmax(const typename Raw<ND>::type (&raw)
       uint32_t bits[4], out[ND];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float e = exp2_fast(__builtin_fmaf((float)raw[t][a][i], unit[t], -top));
+        const float e = exp2_fast(__builtin_fmaf(raw[t][a][i], unit[t], -top));
         part += e;
-        bits[i] = f32_bits(__builtin_fmaf(e, to_digits, 8388608.0f + (float)digit_bias<ND>()));
+        bits[i] = digit_bits<ND>(e, to_digits);
       }
       pack_digits<ND>(bits[0], bits[1], bits[2], bits[3], out);
 #pragma unroll
@@ -248,7 +232,7 @@ __global__ __launch_bounds__(kThreads, DT <= 8 ? 2 : 1) void attention_wide_kern
     for (int n = 0; n < NC; ++n) {
       bool done = false;
       if (whole) {
-        typename Raw<ND>::type raw[2][4][4];
+        float raw[2][4][4];
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int i = 0; i < 2; ++i)
@@ -268,7 +252,7 @@ __global__ __launch_bounds__(kThreads, DT <= 8 ? 2 : 1) void attention_wide_kern
               int32_t part[ND];
 #pragma unroll
               for (int m = 0; m < ND; ++m) part[m] = acc[m][e];
-              raw[i][a][e] = raw_join<ND>(part);
+              raw[i][a][e] = join_digits<ND>(part);
             }
           }
         __builtin_amdgcn_s_setprio(0);
@@ -333,7 +317,7 @@ __global__ __launch_bounds__(kThreads, DT <= 8 ? 2 : 1) void attention_wide_kern
           int32_t part[ND];
 #pragma unroll
           for (int m = 0; m < ND; ++m) part[m] = acc[m][e];
-          st[n].o[dt][e] = __builtin_fmaf((float)raw_join<ND>(part), w[n], st[n].o[dt][e]);
+          st[n].o[dt][e] = __builtin_fmaf(join_digits<ND>(part), w[n], st[n].o[dt][e]);
         }
       }
     }

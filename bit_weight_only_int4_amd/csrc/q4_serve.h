@@ -75,7 +75,7 @@ AttnPlan plan_attention(int32_t dtype, int64_t T, int64_t batch, int64_t heads, 
 hipError_t launch_attention(const AttnParams& p, hipStream_t s);
 template <int ND>
 hipError_t launch_attention_digits(const AttnParams& p, hipStream_t s);
-// (instantiated for 2 and 3 digits in q4_attention_d2.hip / q4_attention_d3.hip)
+// (instantiated for 3 and 4 digits in q4_attention_d3.hip / q4_attention_d4.hip)
 
 struct LogprobParams {
   const void* x;

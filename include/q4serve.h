@@ -125,9 +125,10 @@ q4_status q4_kv_dequant(const int8_t *k_cache, const int8_t *v_cache,
  * max_pages * page makes the outputs that see it NaN.
  *
  * Arithmetic: integer dot products of the 8-bit codes with q and p held as
- * fixed-point numbers of three 8-bit digits (fp32 queries; two digits for
- * 16-bit ones), summed exactly in int32 over each tile of 64 tokens; scales,
- * softmax statistics and sums over tiles in fp32.
+ * fixed-point numbers of four 8-bit digits (fp32 queries; three digits for
+ * 16-bit ones) below the largest of the query's row and of the tile, summed
+ * exactly in int32 over each tile of 64 tokens; scales, softmax statistics and
+ * sums over tiles in fp32.
  */
 q4_status q4_attention(const void *q, int64_t q_ts, int64_t q_hs, void *out,
                        int64_t o_ts, int64_t o_hs, int32_t dtype, int64_t T,
