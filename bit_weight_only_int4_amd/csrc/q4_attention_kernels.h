@@ -508,7 +508,8 @@ __device__ __forceinline__ void attend(const AttnParams& p, const Block& k, int 
     load_values(t, pg, cur);
     float sc[4][4];
     tile_scores<NS, ND>(cur.kd, qd, sc);
-    const float unit = q_unit * (cur.k_in ? cur.ks : nan), vs = cur.v_in ? cur.vs : nan;
+    const float unit = q_unit * (cur.k_in ? scale_or_nan(cur.ks) : nan);
+    const float vs = cur.v_in ? scale_or_nan(cur.vs) : nan;
     if constexpr (decltype(more)::value) {
       pg = check_pages<UNIFORM>(p, raw, k.keys, first_token(t + step));
       load_keys(t + step, pg, cur);

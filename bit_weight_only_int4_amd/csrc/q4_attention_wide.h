@@ -213,8 +213,12 @@ __global__ __launch_bounds__(kThreads, DT <= 8 ? 2 : 1) void attention_wide_kern
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
-    const float ks[2] = {in_next[0] ? ks_next[0] : nan, in_next[1] ? ks_next[1] : nan};
-    const float vs[2] = {in_next[0] ? vs_next[0] : nan, in_next[1] ? vs_next[1] : nan};
+    float ks[2], vs[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      ks[i] = in_next[i] ? scale_or_nan(ks_next[i]) : nan;
+      vs[i] = in_next[i] ? scale_or_nan(vs_next[i]) : nan;
+    }
     fetch_pair(t + 2, buf ^ 1);
     load_pair(t + 4);
     // A wave in its matrix instructions goes before one in its exponentials, so

@@ -204,7 +204,8 @@ struct Scale {
 
 __device__ __forceinline__ Scale grow_scale(float* at, uint32_t amax, bool fresh) {
   __shared__ uint32_t wave_max[kThreads / 64];
-  const float old = fresh ? 0.0f : *at;
+  // (-0 is 0: magnitudes are compared as bit patterns)
+  const float old = fresh ? 0.0f : __builtin_fabsf(scale_or_nan(*at));
   amax = wave_umax(amax);
   if ((threadIdx.x & 63) == 0) wave_max[threadIdx.x >> 6] = amax;
   __syncthreads();  // and every thread has read the old scale
@@ -398,7 +399,7 @@ __global__ __launch_bounds__(kThreads) void kv_dequant_kernel(KvCache c, T* __re
   const int64_t ph = blockIdx.x;
   const int dim = c.dim, page = c.page;
   const int64_t at = ph * ((int64_t)dim << c.page_log2);
-  const float sk = c.ks[ph], sv = c.vs[ph];
+  const float sk = scale_or_nan(c.ks[ph]), sv = scale_or_nan(c.vs[ph]);
   const int n16 = (dim << c.page_log2) >> 4;
   const u32x4v* k = (const u32x4v*)(c.k + at);
   const u32x4v* v = (const u32x4v*)(c.v + at);

@@ -39,6 +39,12 @@ __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b 
 __device__ __forceinline__ float bits_f32(uint32_t b) { return __builtin_bit_cast(float, b); }
 __device__ __forceinline__ uint32_t f32_bits(float f) { return __builtin_bit_cast(uint32_t, f); }
 
+// What a page's scale makes of its codes: a negative one is no scale, and NaN
+// like one that is (the kernels' maxima and digits take values of one sign).
+__device__ __forceinline__ float scale_or_nan(float s) {
+  return s >= 0.0f ? s : bits_f32(0x7fc00000u);
+}
+
 // Magnitudes are compared as their bit patterns, which order like the
 // numbers and put NaN above infinity, so that neither is lost in a maximum.
 __device__ __forceinline__ uint32_t wave_umax(uint32_t x) {

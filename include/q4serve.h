@@ -14,8 +14,9 @@
  *                  straight into a matrix operand)
  *   k_scale, v_scale  float [pages, kv_heads]
  * all contiguous, caches 16-byte aligned.  A scale covers one page of one
- * head: an element stands for code * scale, codes in [-127, 127].  page is
- * 16, 32, 64 or 128 tokens; head_dim a multiple of 16 up to 256.
+ * head: an element stands for code * scale, codes in [-127, 127], scale >= 0
+ * (a negative scale is none: its page's values are NaN in every function).
+ * page is 16, 32, 64 or 128 tokens; head_dim a multiple of 16 up to 256.
  *
  * Sequences are ragged and packed.  Sequence b (0 <= b < batch) owns the new
  * tokens cu_new[b] .. cu_new[b + 1] - 1 of this call (cu_new[0] = 0,
