@@ -171,6 +171,12 @@ __device__ __forceinline__ int32_t segment_page(const AttnParams& p, int32_t raw
   return token0 + 16 <= keys.lo || token0 >= keys.hi ? -2 : page;
 }
 
+// A page's scale in its keys' scores: one that is not finite has to show, and an
+// infinite one would make some of them -inf, weights of 0.
+__device__ __forceinline__ float key_scale(float s) {
+  return s < __builtin_inff() ? scale_or_nan(s) : bits_f32(0x7fc00000u);
+}
+
 // A lane's pages of a tile: of the keys that it loads, and of its 16 tokens
 // (the same where one page covers the tile; then it has a token that is seen).
 struct Pages {
@@ -508,7 +514,7 @@ __device__ __forceinline__ void attend(const AttnParams& p, const Block& k, int 
     load_values(t, pg, cur);
     float sc[4][4];
     tile_scores<NS, ND>(cur.kd, qd, sc);
-    const float unit = q_unit * (cur.k_in ? scale_or_nan(cur.ks) : nan);
+    const float unit = q_unit * (cur.k_in ? key_scale(cur.ks) : nan);
     const float vs = cur.v_in ? scale_or_nan(cur.vs) : nan;
     if constexpr (decltype(more)::value) {
       pg = check_pages<UNIFORM>(p, raw, k.keys, first_token(t + step));

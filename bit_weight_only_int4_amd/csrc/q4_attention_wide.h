@@ -216,7 +216,7 @@ __global__ __launch_bounds__(kThreads, DT <= 8 ? 2 : 1) void attention_wide_kern
     float ks[2], vs[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      ks[i] = in_next[i] ? scale_or_nan(ks_next[i]) : nan;
+      ks[i] = in_next[i] ? key_scale(ks_next[i]) : nan;
       vs[i] = in_next[i] ? scale_or_nan(vs_next[i]) : nan;
     }
     fetch_pair(t + 2, buf ^ 1);

@@ -123,7 +123,9 @@ q4_status q4_kv_dequant(const int8_t *k_cache, const int8_t *v_cache,
  * Positions at or past lengths[b] and outside the window are never read, so
  * their slots, pages and table entries may hold anything.  A visible
  * position whose page number is outside [0, pages) or whose position is past
- * max_pages * page makes the outputs that see it NaN.
+ * max_pages * page makes the outputs that see it NaN.  So does a page's key
+ * scale that is not finite; outputs that see a value scale that is not finite
+ * are not finite.
  *
  * Arithmetic: integer dot products of the 8-bit codes with q and p held as
  * fixed-point numbers of four 8-bit digits (fp32 queries; three digits for

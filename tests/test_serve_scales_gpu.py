@@ -1,6 +1,7 @@
 """Scales that are none: a negative one stands for NaN in every operator, -0
 for 0, whatever the page size and the number of rows (an imported cache may
-hold them; the append never makes them)."""
+hold them; the append never makes them).  And infinite ones, which the append
+makes of infinite elements: no query that sees one has a finite output."""
 import numpy as np
 import pytest
 import torch
@@ -39,6 +40,30 @@ MANY = [(1, 16, []), (1, 64, []), (3, 128, []), (250, 64, []), (70, 32, FILL), (
 def test_a_negative_scale_shows_where_it_is_seen(which, value, new, page, fill):
     shows_where_it_is_seen(which, value, page, new, fill)
     shows_where_it_is_seen(which, value, page, new, fill, dtype="bf16", window=page)
+
+
+@pytest.mark.parametrize("which", ["k", "v"])
+@pytest.mark.parametrize("new,page,fill", MANY)
+def test_an_infinite_scale_shows_where_it_is_seen(which, new, page, fill):
+    shows_where_it_is_seen(which, np.inf, page, new, fill)
+    shows_where_it_is_seen(which, np.inf, page, new, fill, dtype="f16", window=page)
+
+
+@pytest.mark.parametrize("page", [16, 64])
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+def test_an_appended_key_that_is_not_finite_shows(value, page):
+    """The first token of a page, its key infinite in one channel, under
+    queries of either sign there."""
+    need_gpu()
+    caches = q4.new_cache(3, 2, 64, page)
+    n = page + 1
+    k, q = torch.randn((n, 2, 64), device="cuda"), torch.randn((n, 4, 64), device="cuda")
+    k[page, 0, 9] = value
+    q[page, :2, 9] = torch.tensor([3.0, -3.0], device="cuda")
+    args = [*caches, i32([[2, 0]]), i32([0, n]), i32([n])]
+    q4.kv_append(k, k.nan_to_num(0.0, 0.0, 0.0), *args)
+    out = q4.attention(q, *args)
+    assert out[page, :2].isnan().all() and out[:page].isfinite().all() and out[page, 2:].isfinite().all()
 
 
 @pytest.mark.parametrize("new,page,fill", MANY)
