@@ -136,7 +136,7 @@ __device__ __forceinline__ void store_elem(void* p, int64_t i, float v, int32_t 
 struct Block {
   SeqSpan sp;
   int b, h;
-  int64_t row0, rows;  // first query row (token * group + head) and rows of the sequence
+  int64_t row0, rows;  // first query row (token * group + head) and the sequence's rows to compute
   int tile0, tiles;    // tiles of 64 positions that its queries see
   KeyRange keys;
 };
@@ -152,7 +152,9 @@ __device__ __forceinline__ Block block_of(const AttnParams& p, int b, int h, int
   k.h = h;
   k.b = b;
   k.sp = seq_span(p.c.cu_new, p.c.lengths, k.b, p.T);
-  k.rows = (int64_t)k.sp.n * p.group;
+  // of a sequence with more than max_new tokens, its last block holds rows past it
+  const int64_t rows = (int64_t)k.sp.n * p.group;
+  k.rows = rows < p.max_rows ? rows : p.max_rows;
   k.row0 = (int64_t)rb * p.block_rows;
   const int64_t last = k.row0 + p.block_rows < k.rows ? k.row0 + p.block_rows : k.rows;
   k.keys = key_range(k.sp.pos0 + row_token(p, k.row0),
