@@ -317,11 +317,13 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendParams p) {
       for (int i = o1 * chunks + tid; i < chunks << c.page_log2; i += kThreads)
         ((u32x4v*)cache)[i] = u32x4v{0, 0, 0, 0};
     } else if (s.grew) {
-      for (int i = tid; i < o0 * chunks; i += kThreads) {
-        u32x4v w = ((u32x4v*)cache)[i];
+      // both sides of the new tokens: one that is stored again has some behind it
+      for (int i = tid; i < (c.page - (o1 - o0)) * chunks; i += kThreads) {
+        u32x4v* at_i = (u32x4v*)cache + (i < o0 * chunks ? i : i + (o1 - o0) * chunks);
+        u32x4v w = *at_i;
 #pragma unroll
         for (int e = 0; e < 4; ++e) w[e] = recode(w[e], s.ratio);
-        ((u32x4v*)cache)[i] = w;
+        *at_i = w;
       }
     }
   } else {
@@ -377,8 +379,9 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendParams p) {
         *(u32x4v*)(cache + ((int64_t)d << c.page_log2) + 16 * (c_hi + ch)) = u32x4v{0, 0, 0, 0};
       }
     } else if (s.grew) {
-      for (int i = tid; i < c_lo * dim; i += kThreads) {
-        const int ch = i / dim, d = i - ch * dim;
+      const int old = (c.page >> 4) - (c_hi - c_lo);
+      for (int i = tid; i < old * dim; i += kThreads) {
+        const int k = i / dim, d = i - k * dim, ch = k < c_lo ? k : k + (c_hi - c_lo);
         u32x4v* dst = (u32x4v*)(cache + ((int64_t)d << c.page_log2) + 16 * ch);
         u32x4v q = *dst;
 #pragma unroll
