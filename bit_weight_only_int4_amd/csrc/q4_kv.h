@@ -53,6 +53,32 @@ Q4_HD int64_t pages_touched(int64_t n, int64_t page) {
   return n <= 0 ? 0 : (n - 1 + page - 1) / page + 1;
 }
 
+// Whether rows of `dim` elements at a_hs * h + a_ts * t and delta + b_hs * h +
+// b_ts * t (t < T, h < a_heads or b_heads; strides as the ABI admits them) have
+// an element in common.  Different token strides of several tokens count as
+// sharing.  Host code.
+inline bool rows_share(int64_t delta, int64_t T, int64_t dim, int64_t a_ts, int64_t a_hs,
+                       int64_t a_heads, int64_t b_ts, int64_t b_hs, int64_t b_heads) {
+  if (T <= 0 || a_heads <= 0 || b_heads <= 0) return false;
+  const int64_t a_len = (a_heads - 1) * a_hs + dim, b_len = (b_heads - 1) * b_hs + dim;
+  if (T == 1) a_ts = b_ts = a_len + b_len + (delta < 0 ? -delta : delta);  // no second token in reach
+  if (a_ts != b_ts) return true;
+  // usually the heads of one lie between those of the other's tokens
+  const int64_t in_token = ((delta % a_ts) + a_ts) % a_ts;
+  if (in_token >= a_len && in_token + b_len <= a_ts) return false;
+  for (int64_t a = 0; a < a_heads; ++a)
+    for (int64_t b = 0; b < b_heads; ++b) {
+      // tokens `near` and `near` + 1 later are the ones closest to it
+      const int64_t x = delta + b * b_hs - a * a_hs;
+      const int64_t near = -x / a_ts - (-x % a_ts < 0 ? 1 : 0);
+      for (int64_t i = near; i <= near + 1; ++i) {
+        const int64_t off = x + i * a_ts;
+        if (i > -T && i < T && off > -dim && off < dim) return true;
+      }
+    }
+  return false;
+}
+
 // Positions [lo, hi) that any of the queries at pos_min .. pos_max sees.
 struct KeyRange {
   int64_t lo, hi;

@@ -142,9 +142,15 @@ q4_status q4_kv_append(const void* k, int64_t k_ts, int64_t k_hs, const void* v,
   constexpr int n_out = sizeof(outs) / sizeof(outs[0]), n_in = sizeof(ins) / sizeof(ins[0]);
   for (int i = 0; i < n_out; ++i) {
     // queries turned in place may share a fused projection's rows with k and
-    // v: the spans interleave without an element in common
-    for (int j = 0; j < n_in; ++j)
-      if (!(i == n_out - 1 && in_place && j < 2) && overlap(outs[i], ins[j])) return Q4_ERR_ALIAS;
+    // v, where the spans interleave without an element in common
+    for (int j = 0; j < n_in; ++j) {
+      if (!overlap(outs[i], ins[j])) continue;
+      if (!(i == n_out - 1 && in_place && j < 2)) return Q4_ERR_ALIAS;
+      const int64_t delta = ((intptr_t)(j == 0 ? k : v) - (intptr_t)q) / e;
+      if (q4::rows_share(delta, T, head_dim, q_ts, q_hs, heads, j == 0 ? k_ts : v_ts,
+                         j == 0 ? k_hs : v_hs, kv_heads))
+        return Q4_ERR_ALIAS;
+    }
     for (int j = 0; j < i; ++j)
       if (overlap(outs[i], outs[j])) return Q4_ERR_ALIAS;
   }

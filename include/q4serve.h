@@ -50,7 +50,10 @@ extern "C" {
  *   k, v    [T, kv_heads, head_dim] of `dtype`; token stride *_ts and head
  *           stride *_hs in elements, head_dim contiguous
  *   q       [T, heads, head_dim] or NULL; q_out likewise, may be q itself
- *           (the same pointer and strides), else must not overlap an input
+ *           (the same pointer and strides), else must not overlap an input.
+ *           In place, the queries may lie in one array with k and v (rows of
+ *           a fused projection, heads of either interleaved with the others'),
+ *           of the same token stride and without an element in common
  *   inv_freq  float [rot / 2], or NULL with rot == 0 (no rotation)
  *   rot     even, 0 <= rot <= head_dim: elements of a head that turn.  Pair
  *           i is elements (i, i + rot / 2), or (2 i, 2 i + 1) if
