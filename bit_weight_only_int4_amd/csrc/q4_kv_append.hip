@@ -140,7 +140,7 @@ __device__ __forceinline__ void turn_unit(float (&x)[8], const float* cs, const 
 }
 
 // Queries of tokens t0 .. t0 + kTurn - 1, all heads.
-constexpr int kTurn = 4;
+constexpr int kTurn = 4;  // append_turn at most
 
 template <typename T>
 __device__ __forceinline__ void turn_queries(const AppendParams& p, int64_t t0, int n) {
@@ -234,7 +234,7 @@ __global__ __launch_bounds__(kThreads) void kv_append_kernel(AppendParams p) {
   id >>= 1;
   const int h = id % c.heads;
   id /= c.heads;
-  const int j = id % p.touched;
+  const int j = p.first + (int)(id % p.touched);
   const int b = id / p.touched;
   const SeqSpan sp = seq_span(c.cu_new, c.lengths, b, p.T);
   // new tokens of this page: slots o0 .. o1 - 1
@@ -468,18 +468,31 @@ hipError_t launch_kv_append(const AppendParams& in, int32_t dtype, int64_t max_n
                             hipStream_t s) {
   AppendParams p = in;
   p.max_new = max_new;
-  p.touched = (int32_t)pages_touched(max_new, p.c.page);
-  p.cache_blocks = (int32_t)((int64_t)p.batch * p.touched * p.c.heads * 2);
-  // a workgroup per token while that leaves CUs without work
-  p.turn = p.T >= 2048 ? kTurn : 1;
+  const int64_t touched = pages_touched(max_new, p.c.page);
+  p.turn = append_turn(p.T);
+  int64_t turns = p.q ? append_turns(p.T) : 0;
   const int64_t rows = max_new < p.c.page ? max_new : p.c.page;
-  const dim3 grid((unsigned)(p.cache_blocks + (p.q ? (p.T + p.turn - 1) / p.turn : 0)));
-  if (dtype == Q4_DTYPE_F32) return launch_append<float>(p, rows, grid, s);
-  if (dtype == Q4_DTYPE_F16) return launch_append<_Float16>(p, rows, grid, s);
-  return launch_append<bf16>(p, rows, grid, s);
+  // One launch, unless a loose max_new makes more workgroups than that may have
+  // (a loop over pages in the kernel costs it registers: 6000 tokens of prompts
+  // 73 -> 105 us).
+  const int64_t a_page = (int64_t)p.batch * p.c.heads * 2;
+  for (int64_t j = 0; j < touched; j += p.touched) {
+    const int64_t most = (kMaxGrid - turns) / a_page;
+    p.first = (int32_t)j;
+    p.touched = (int32_t)(touched - j < most ? touched - j : most);
+    p.cache_blocks = (int32_t)(a_page * p.touched);
+    const dim3 grid((unsigned)(p.cache_blocks + turns));
+    const hipError_t e = dtype == Q4_DTYPE_F32   ? launch_append<float>(p, rows, grid, s)
+                         : dtype == Q4_DTYPE_F16 ? launch_append<_Float16>(p, rows, grid, s)
+                                                 : launch_append<bf16>(p, rows, grid, s);
+    if (e != hipSuccess) return e;
+    turns = 0;  // the queries have turned
+  }
+  return hipSuccess;
 }
 
-hipError_t launch_kv_dequant(const KvCache& c, int32_t dtype, void* k, void* v, hipStream_t s) {
+static hipError_t launch_dequant_pages(const KvCache& c, int32_t dtype, void* k, void* v,
+                                       hipStream_t s) {
   const size_t lds = (size_t)c.dim * (c.page + 4);
   const dim3 grid((unsigned)(c.pages * c.heads));
   if (dtype == Q4_DTYPE_F32)
@@ -489,6 +502,23 @@ hipError_t launch_kv_dequant(const KvCache& c, int32_t dtype, void* k, void* v, 
   else
     hipLaunchKernelGGL(kv_dequant_kernel<bf16>, grid, dim3(kThreads), lds, s, c, (bf16*)k, (bf16*)v);
   return hipGetLastError();
+}
+
+hipError_t launch_kv_dequant(const KvCache& in, int32_t dtype, void* k, void* v, hipStream_t s) {
+  const int64_t step = kMaxGrid / in.heads;  // pages of one launch
+  const int64_t page = (int64_t)in.heads * in.page * in.dim, e = dtype == Q4_DTYPE_F32 ? 4 : 2;
+  for (int64_t p = 0; p < in.pages; p += step) {
+    KvCache c = in;
+    c.pages = in.pages - p < step ? in.pages - p : step;
+    c.k += p * page;
+    c.v += p * page;
+    c.ks += p * in.heads;
+    c.vs += p * in.heads;
+    const hipError_t err = launch_dequant_pages(c, dtype, (char*)k + p * page * e,
+                                                (char*)v + p * page * e, s);
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
 }
 
 }  // namespace q4

@@ -607,7 +607,13 @@ LogprobPlan plan_logprobs(int64_t M, int64_t V, int64_t top_k, int32_t dtype) {
   return pl;
 }
 
-hipError_t launch_logprobs(const LogprobParams& p, int32_t dtype, hipStream_t s) {
+// Rows of one launch: of more, the rest comes in further ones.
+static int64_t rows_at_once(int64_t M, int64_t blocks_a_row) {
+  const int64_t most = kMaxGrid / blocks_a_row;
+  return M < most ? M : most;
+}
+
+static hipError_t launch_rows(const LogprobParams& p, int32_t dtype, hipStream_t s) {
   const dim3 grid((unsigned)(p.M * p.splits));
   // A long row of its own workgroup is shared by eight waves while there are
   // few rows.  Registers leave a CU 24 waves: with 16 a row the next row could
@@ -632,9 +638,27 @@ hipError_t launch_logprobs(const LogprobParams& p, int32_t dtype, hipStream_t s)
   return hipGetLastError();
 }
 
-hipError_t launch_logprobs_backward(const LogprobBwdParams& p, int32_t dtype, hipStream_t s) {
-  const int64_t bytes = dtype == Q4_DTYPE_F32 ? 4 : 2;
-  const int64_t per_row = ceil_div(ceil_div(p.V * bytes, 16), kThreads * 4);
+hipError_t launch_logprobs(const LogprobParams& p, int32_t dtype, hipStream_t s) {
+  const int64_t e = dtype == Q4_DTYPE_F32 ? 4 : 2;
+  const int64_t step = rows_at_once(p.M, p.splits);  // (all of them where rows have parts)
+  for (int64_t m = 0; m < p.M; m += step) {
+    LogprobParams r = p;
+    r.M = p.M - m < step ? p.M - m : step;
+    r.x = (const char*)p.x + m * p.ld * e;
+    r.targets = p.targets ? p.targets + m : nullptr;
+    r.logprob = p.logprob ? p.logprob + m : nullptr;
+    r.entropy = p.entropy + m;
+    r.lse = p.lse + m;
+    r.top_ids = p.top_ids ? p.top_ids + m * p.top_k : nullptr;
+    r.top_lp = p.top_lp ? p.top_lp + m * p.top_k : nullptr;
+    const hipError_t err = launch_rows(r, dtype, s);
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
+}
+
+static hipError_t launch_backward_rows(const LogprobBwdParams& p, int32_t dtype, int64_t per_row,
+                                       hipStream_t s) {
   const dim3 grid((unsigned)(p.M * per_row));
   if (dtype == Q4_DTYPE_F32)
     hipLaunchKernelGGL(logprobs_backward_kernel<float>, grid, dim3(kThreads), 0, s, p, per_row);
@@ -643,6 +667,26 @@ hipError_t launch_logprobs_backward(const LogprobBwdParams& p, int32_t dtype, hi
   else
     hipLaunchKernelGGL(logprobs_backward_kernel<bf16>, grid, dim3(kThreads), 0, s, p, per_row);
   return hipGetLastError();
+}
+
+hipError_t launch_logprobs_backward(const LogprobBwdParams& p, int32_t dtype, hipStream_t s) {
+  const int64_t e = dtype == Q4_DTYPE_F32 ? 4 : 2;
+  const int64_t per_row = ceil_div(ceil_div(p.V * e, 16), kThreads * 4);
+  const int64_t step = rows_at_once(p.M, per_row);
+  for (int64_t m = 0; m < p.M; m += step) {
+    LogprobBwdParams r = p;
+    r.M = p.M - m < step ? p.M - m : step;
+    r.x = (const char*)p.x + m * p.ld * e;
+    r.dx = (char*)p.dx + m * p.ldd * e;
+    r.targets = p.targets ? p.targets + m : nullptr;
+    r.lse = p.lse + m;
+    r.entropy = p.entropy + m;
+    r.g_lp = p.g_lp ? p.g_lp + m : nullptr;
+    r.g_ent = p.g_ent ? p.g_ent + m : nullptr;
+    const hipError_t err = launch_backward_rows(r, dtype, per_row, s);
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
 }
 
 }  // namespace q4

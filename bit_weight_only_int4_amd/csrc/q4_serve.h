@@ -10,6 +10,12 @@
 
 namespace q4 {
 
+// Workgroups that one launch may have: a grid holds fewer than 2^32 threads,
+// and one of more is taken without an error and run in part (an append of 4200
+// sequences with the default max_new left most of them out).  In workgroups of
+// 256 threads; launches of more threads each have few of them.
+constexpr int64_t kMaxGrid = ((int64_t)1 << 24) - 1;
+
 struct KvCache {
   int8_t* k;
   int8_t* v;
@@ -35,12 +41,16 @@ struct AppendParams {
   int32_t batch, heads;
   const float* inv_freq;
   int32_t rot, interleaved;
-  int32_t touched;       // pages of one sequence that the launch covers
+  int32_t first, touched;  // pages of one sequence that the launch covers
   int32_t cache_blocks;  // workgroups that store; the rest turn queries,
   int32_t turn;          // so many tokens each
   int32_t k_vec, q_vec;  // rows of k, and of q and q_out, allow vector accesses
 };
 
+// Tokens of a workgroup that turns queries (one while that leaves CUs without
+// work), and such workgroups.
+inline int32_t append_turn(int64_t T) { return T >= 2048 ? 4 : 1; }
+inline int64_t append_turns(int64_t T) { return (T + append_turn(T) - 1) / append_turn(T); }
 hipError_t launch_kv_append(const AppendParams& p, int32_t dtype, int64_t max_new, hipStream_t s);
 hipError_t launch_kv_dequant(const KvCache& c, int32_t dtype, void* k, void* v, hipStream_t s);
 

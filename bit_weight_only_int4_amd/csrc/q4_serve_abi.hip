@@ -53,8 +53,8 @@ bool heads_ok(int64_t heads, int64_t kv_heads, int64_t dim) {
          dim >= 16 && dim <= 256 && dim % 16 == 0;
 }
 
-// workgroups of a launch: the grid's and the kernels' 32-bit arithmetic
-bool grid_ok(double blocks) { return blocks < 2147483648.0; }
+// workgroups of a launch
+bool grid_ok(double blocks) { return blocks <= (double)q4::kMaxGrid; }
 
 q4_status make_cache(int8_t* k, int8_t* v, float* ks, float* vs, int64_t pages, int64_t page,
                      int64_t kv_heads, int64_t dim, const int32_t* table, int64_t table_ld,
@@ -124,8 +124,8 @@ q4_status q4_kv_append(const void* k, int64_t k_ts, int64_t k_hs, const void* v,
   if (st != Q4_OK) return st;
   if (max_new > T) max_new = T;
   if (max_new < 1) return Q4_ERR_INVALID_ARG;
-  if (!grid_ok(2.0 * (double)batch * (double)q4::pages_touched(max_new, page) * (double)kv_heads +
-               (double)T))
+  // a launch has workgroups for one page of each sequence at the least, and for all queries
+  if (!grid_ok(2.0 * (double)batch * (double)kv_heads + (q ? (double)q4::append_turns(T) : 0.0)))
     return Q4_ERR_INVALID_ARG;
 
   const int64_t cache_n = pages * kv_heads * page * head_dim;
@@ -185,7 +185,7 @@ q4_status q4_kv_dequant(const int8_t* k_cache, const int8_t* v_cache, const floa
                         const float* v_scale, int64_t pages, int64_t kv_heads, int64_t page,
                         int64_t head_dim, int32_t dtype, void* k, void* v, void* stream) {
   if (!dtype_ok(dtype) || !size_ok(pages) || !page_ok(page) ||
-      !heads_ok(kv_heads, kv_heads, head_dim) || !grid_ok((double)pages * (double)kv_heads))
+      !heads_ok(kv_heads, kv_heads, head_dim))
     return Q4_ERR_INVALID_ARG;
   if (pages == 0) return Q4_OK;
   if (!k_cache || !v_cache || !k_scale || !v_scale || !k || !v) return Q4_ERR_INVALID_ARG;
@@ -263,7 +263,7 @@ q4_status q4_attention(const void* q, int64_t q_ts, int64_t q_hs, void* out, int
   const q4::AttnPlan pl = q4::plan_attention(dtype, T, batch, heads, kv_heads, head_dim, page,
                                              max_new, max_len, window);
   if (!grid_ok((double)batch * (double)kv_heads * (double)pl.row_blocks * (double)pl.splits) ||
-      !grid_ok((double)batch * (double)heads * (double)max_new))
+      (pl.splits > 1 && !grid_ok((double)batch * (double)kv_heads * (double)pl.max_rows)))
     return Q4_ERR_INVALID_ARG;
 
   const int64_t cache_n = pages * kv_heads * page * head_dim;
@@ -337,7 +337,6 @@ q4_status q4_token_logprobs(const void* logits, int64_t ld, int32_t dtype, int64
       !aligned(entropy, 4) || !aligned(lse, 4) || !aligned(top_ids, 8) || !aligned(top_logprobs, 4))
     return Q4_ERR_INVALID_ARG;
   const q4::LogprobPlan pl = q4::plan_logprobs(M, vocab, top_k, dtype);
-  if (!grid_ok((double)M * pl.splits)) return Q4_ERR_INVALID_ARG;
   Range outs[6] = {targets ? flat(logprob, M, 4) : Range{0, 0}, flat(entropy, M, 4),
                    flat(lse, M, 4), flat(top_ids, M * top_k, 8), flat(top_logprobs, M * top_k, 4),
                    Range{0, 0}};
@@ -391,7 +390,6 @@ q4_status q4_token_logprobs_backward(const void* logits, int64_t ld, int32_t dty
   if (!aligned(logits, e) || !aligned(dlogits, e) || !aligned(targets, 8) || !aligned(lse, 4) ||
       !aligned(entropy, 4) || !aligned(g_logprob, 4) || !aligned(g_entropy, 4))
     return Q4_ERR_INVALID_ARG;
-  if (!grid_ok((double)M * (double)(vocab * e / 16384 + 1))) return Q4_ERR_INVALID_ARG;
   const Range out = span(dlogits, M, ldd, 1, 0, vocab, e);
   const bool in_place = dlogits == logits && (ldd == ld || M == 1);
   const Range ins[] = {in_place ? Range{0, 0} : span(logits, M, ld, 1, 0, vocab, e),

@@ -117,7 +117,9 @@ q4_status q4_kv_dequant(const int8_t *k_cache, const int8_t *v_cache,
  *   q, out  [T, heads, head_dim] of `dtype` with token and head strides;
  *           out must not overlap an input
  *   max_new   upper bound of the new tokens of one sequence: queries past
- *           it are not computed, their outputs left as they are
+ *           it are not computed, their outputs left as they are.  With
+ *           batch it sizes the launch: of more than 2^24 - 1 workgroups the
+ *           call is refused (about 8000 sequences with max_new = T)
  *   max_len   upper bound of lengths: it sizes the launch and the
  *           workspace.  Positions past it are not attended.
  *   workspace   q4_attention_workspace_bytes(...) bytes, 16-byte aligned
