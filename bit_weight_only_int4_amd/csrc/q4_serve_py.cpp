@@ -12,8 +12,10 @@
 #include <c10/core/DeviceGuard.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdarg>
+#include <cstdint>
 #include <cstdio>
 #include <exception>
 #include <optional>
@@ -289,7 +291,9 @@ PyObject* attention(PyObject* const* a) {
   const double scale = given(a[8]) ? number(a[8]) : 1.0 / std::sqrt((double)c.dim);
   const int64_t window = integer(a[9]);
   const int64_t max_new = given(a[10]) ? integer(a[10]) : T;
-  const int64_t max_len = given(a[11]) ? integer(a[11]) : t.cols * c.page;
+  // the table's reach, as far as int32 lengths go
+  const int64_t reach = std::min<int64_t>(t.cols * c.page, INT32_MAX);
+  const int64_t max_len = given(a[11]) ? integer(a[11]) : reach;
   at::Tensor out;
   if (given(a[12])) {
     out = tensor(a[12], "out");
