@@ -148,7 +148,7 @@ struct Tables {
   const int32_t *table, *cu, *lengths;
 };
 
-Tables tables_of(PyObject* const* a, const at::Device& dev) {
+Tables tables_of(PyObject* const* a, int64_t T, const at::Device& dev) {
   const at::Tensor& t = tensor(a[0], "page_table");
   if (t.scalar_type() != at::kInt || t.dim() != 2 || (t.size(1) > 1 && t.stride(1) != 1))
     refuse("page_table must be int32 [batch, max_pages] with unit stride along its rows, got %s %s",
@@ -158,6 +158,7 @@ Tables tables_of(PyObject* const* a, const at::Device& dev) {
   r.batch = t.size(0);
   r.cols = t.size(1);
   r.ld = r.batch > 1 ? t.stride(0) : r.cols;
+  if (T > 0 && r.batch == 0) refuse("%lld new tokens of no sequence", (long long)T);
   r.table = (const int32_t*)t.data_ptr();
   r.cu = (const int32_t*)vector(tensor(a[1], "cu_new"), "cu_new", r.batch + 1, at::kInt, dev);
   r.lengths = (const int32_t*)vector(tensor(a[2], "lengths"), "lengths", r.batch, at::kInt, dev);
@@ -208,7 +209,7 @@ PyObject* kv_append(PyObject* const* a) {
   if (k.size(1) != c.heads || k.size(2) != c.dim || v.sizes() != k.sizes())
     refuse("k and v must be [T, %lld, %lld], got %s and %s", (long long)c.heads, (long long)c.dim,
            shape(k).c_str(), shape(v).c_str());
-  const Tables t = tables_of(a + 6, dev);
+  const Tables t = tables_of(a + 6, T, dev);
   at::Tensor q, q_out;
   int64_t heads = c.heads;
   if (given(a[9])) {
@@ -287,7 +288,7 @@ PyObject* attention(PyObject* const* a) {
   if (q.size(2) != c.dim || heads == 0 || heads % c.heads)
     refuse("q must be [T, a multiple of %lld, %lld], got %s", (long long)c.heads, (long long)c.dim,
            shape(q).c_str());
-  const Tables t = tables_of(a + 5, dev);
+  const Tables t = tables_of(a + 5, T, dev);
   const double scale = given(a[8]) ? number(a[8]) : 1.0 / std::sqrt((double)c.dim);
   const int64_t window = integer(a[9]);
   const int64_t max_new = given(a[10]) ? integer(a[10]) : T;
@@ -300,6 +301,10 @@ PyObject* attention(PyObject* const* a) {
     check_rows(out, "out", q.scalar_type(), dev);
     if (out.sizes() != q.sizes())
       refuse("out must be %s, got %s", shape(q).c_str(), shape(out).c_str());
+  } else if (max_new >= 0 && max_new < T && max_new * t.batch < T) {
+    // queries past max_new are left alone: a new tensor has nothing there
+    refuse("max_new = %lld leaves out some of %lld new tokens of %lld sequences; give a bound, or out",
+           (long long)max_new, (long long)T, (long long)t.batch);
   }
   on_gpu(dev, "q");
   const c10::DeviceGuard guard(dev);

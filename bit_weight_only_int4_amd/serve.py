@@ -141,7 +141,9 @@ def attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, k_s
     sequences' cached tokens up to their own position (and, with window > 0,
     the last ``window`` of those).  ``softmax_scale`` defaults to head_dim **
     -0.5; ``max_new`` and ``max_len`` bound the new tokens and the length of a
-    sequence (default: T and the page table's reach) and size the launch."""
+    sequence (default: T and the page table's reach) and size the launch: rows
+    past max_new and rows of no sequence are left as they are in ``out`` and
+    undefined in a new tensor."""
     return (_module or _native()).attention(
         q, k_cache, v_cache, k_scale, v_scale, page_table, cu_new, lengths, softmax_scale, window,
         max_new, max_len, out, workspace, _stream(q))

@@ -1,0 +1,25 @@
+"""What the binding of the decode-side operators does with arguments that are
+no tensors, raise, or leave rows of a new output without a value, and with its
+outputs' memory."""
+import pytest
+import torch
+
+import bit_weight_only_int4_amd as q4
+from tests.test_serve_abi import binding_args, i32
+
+
+@pytest.mark.parametrize("op", ["kv_append", "attention"])
+def test_new_tokens_without_a_sequence_are_refused(op):
+    """Their rows of a new output would hold whatever its memory held."""
+    none = dict(page_table=torch.zeros((0, 2), dtype=torch.int32), cu_new=i32(0), lengths=torch.zeros(0, dtype=torch.int32))
+    with pytest.raises(ValueError, match="sequence"):
+        getattr(q4, op)(**binding_args(op, **none))
+
+
+def test_a_bound_that_leaves_rows_of_a_new_output_out_is_refused():
+    # 3 new tokens of one sequence
+    with pytest.raises(ValueError, match="max_new"):
+        q4.attention(**binding_args("attention", max_new=2))
+    for kw in (dict(max_new=3), dict(max_new=2, out=torch.zeros((3, 4, 64)))):
+        with pytest.raises(ValueError, match="must be a device tensor"):
+            q4.attention(**binding_args("attention", **kw))
