@@ -81,9 +81,9 @@ def _native():
 
 
 def _stream(t: torch.Tensor) -> int:
-    """The current stream of the tensor's device (0 for a host tensor, which
-    is refused later)."""
-    d = t.get_device()
+    """The current stream of the tensor's device (0 for a host tensor and for
+    what is no tensor, which are refused later)."""
+    d = t.get_device() if isinstance(t, torch.Tensor) else -1
     return _raw_stream(d) if d >= 0 else 0
 
 

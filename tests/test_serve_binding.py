@@ -23,3 +23,11 @@ def test_a_bound_that_leaves_rows_of_a_new_output_out_is_refused():
     for kw in (dict(max_new=3), dict(max_new=2, out=torch.zeros((3, 4, 64)))):
         with pytest.raises(ValueError, match="must be a device tensor"):
             q4.attention(**binding_args("attention", **kw))
+
+
+@pytest.mark.parametrize("op,name", [("kv_append", "k"), ("attention", "q"), ("kv_dequant", "k_cache"), ("token_logprobs", "logits"),
+                                     ("token_logprobs_backward", "logits")])
+@pytest.mark.parametrize("value", [[1.0], None, 3])
+def test_a_first_argument_that_is_no_tensor(op, name, value):
+    with pytest.raises(ValueError, match=f"{name} must be a tensor"):
+        getattr(q4, op)(**binding_args(op, **{name: value}))
