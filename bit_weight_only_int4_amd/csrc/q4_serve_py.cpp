@@ -239,6 +239,7 @@ PyObject* kv_append(PyObject* const* a) {
              (long long)(c.dim / 2));
   }
   const int interleaved = PyObject_IsTrue(a[12]);
+  if (interleaved < 0) throw PyFailed{};
   const int64_t max_new = given(a[13]) ? integer(a[13]) : T;
   on_gpu(dev, "k");
   const c10::DeviceGuard guard(dev);

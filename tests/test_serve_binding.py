@@ -31,3 +31,13 @@ def test_a_bound_that_leaves_rows_of_a_new_output_out_is_refused():
 def test_a_first_argument_that_is_no_tensor(op, name, value):
     with pytest.raises(ValueError, match=f"{name} must be a tensor"):
         getattr(q4, op)(**binding_args(op, **{name: value}))
+
+
+class Raises:
+    def __bool__(self):
+        raise KeyError("neither")
+
+
+def test_an_argument_whose_truth_raises():
+    with pytest.raises(KeyError, match="neither"):
+        q4.kv_append(**binding_args("kv_append", interleaved=Raises()))
