@@ -265,9 +265,8 @@ PyObject* kv_dequant(PyObject* const* a) {
   const at::ScalarType type = code == Q4_DTYPE_F32 ? at::kFloat : code == Q4_DTYPE_F16 ? at::kHalf : at::kBFloat16;
   on_gpu(dev, "k_cache");
   const c10::DeviceGuard guard(dev);
-  // one allocation for both
-  const at::Tensor both = at::empty({2, c.pages, c.heads, c.page, c.dim}, first.options().dtype(type));
-  at::Tensor k = both.select(0, 0), v = both.select(0, 1);
+  const at::Tensor k = at::empty({c.pages, c.heads, c.page, c.dim}, first.options().dtype(type));
+  const at::Tensor v = at::empty(k.sizes(), k.options());
   check(q4_kv_dequant(c.k, c.v, c.ks, c.vs, c.pages, c.heads, c.page, c.dim, (int32_t)code,
                       k.data_ptr(), v.data_ptr(), stream_of(a[5])),
         "q4_kv_dequant");
@@ -345,27 +344,30 @@ PyObject* token_logprobs(PyObject* const* a) {
   const int64_t* targets = targets_of(a[1], M, dev);
   on_gpu(dev, "logits");
   const c10::DeviceGuard guard(dev);
+  // tensors of their own: views of one would share its version counter, and an
+  // in-place change of one would spoil what autograd saved of another
   const at::TensorOptions f32 = x.options().dtype(at::kFloat);
-  // log probabilities, entropies and log sums, then the alternatives' values
-  const at::Tensor stats = at::empty({M * (3 + k)}, f32);
+  const at::Tensor logprob = targets ? at::empty({M}, f32) : at::Tensor();
+  const at::Tensor entropy = at::empty({M}, f32), lse = at::empty({M}, f32), top = at::empty({M, k}, f32);
   const at::Tensor ids = at::empty({M, k}, x.options().dtype(at::kLong));
-  float* s = (float*)stats.data_ptr();
   const Workspace ws(a[3], given(a[3]) ? 0 : q4_token_logprobs_workspace_bytes(M, V, k, dtype), x.options());
-  check(q4_token_logprobs(x.data_ptr(), ld, dtype, M, V, targets, k, targets ? s : nullptr, s + M,
-                          s + 2 * M, (int64_t*)ids.data_ptr(), s + 3 * M, ws.p, ws.n, stream_of(a[4])),
+  check(q4_token_logprobs(x.data_ptr(), ld, dtype, M, V, targets, k,
+                          targets ? (float*)logprob.data_ptr() : nullptr, (float*)entropy.data_ptr(),
+                          (float*)lse.data_ptr(), (int64_t*)ids.data_ptr(), (float*)top.data_ptr(),
+                          ws.p, ws.n, stream_of(a[4])),
         "q4_token_logprobs");
   PyObject* r = PyTuple_New(5);
   if (!r) throw PyFailed{};
   if (targets) {
-    PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(stats.narrow(0, 0, M)));
+    PyTuple_SET_ITEM(r, 0, THPVariable_Wrap(logprob));
   } else {
     Py_INCREF(Py_None);
     PyTuple_SET_ITEM(r, 0, Py_None);
   }
-  PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(stats.narrow(0, M, M)));
-  PyTuple_SET_ITEM(r, 2, THPVariable_Wrap(stats.narrow(0, 2 * M, M)));
+  PyTuple_SET_ITEM(r, 1, THPVariable_Wrap(entropy));
+  PyTuple_SET_ITEM(r, 2, THPVariable_Wrap(lse));
   PyTuple_SET_ITEM(r, 3, THPVariable_Wrap(ids));
-  PyTuple_SET_ITEM(r, 4, THPVariable_Wrap(stats.narrow(0, 3 * M, M * k).view({M, k})));
+  PyTuple_SET_ITEM(r, 4, THPVariable_Wrap(top));
   return r;
 }
 

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 import bit_weight_only_int4_amd as q4
+from tests.gpu_util import need_gpu
 from tests.test_serve_abi import binding_args, i32
 
 
@@ -41,3 +42,29 @@ class Raises:
 def test_an_argument_whose_truth_raises():
     with pytest.raises(KeyError, match="neither"):
         q4.kv_append(**binding_args("kv_append", interleaved=Raises()))
+
+
+def own_memory(tensors):
+    """No two share storage or a version counter."""
+    assert len({t.untyped_storage().data_ptr() for t in tensors}) == len(tensors)
+    assert all(t._base is None and t.storage_offset() == 0 for t in tensors)
+    for i, t in enumerate(tensors):
+        before = [x._version for x in tensors]
+        t.add_(1)
+        assert [x._version - v for x, v in zip(tensors, before)] == [j == i for j in range(len(tensors))]
+
+
+@pytest.mark.gpu
+def test_outputs_are_tensors_of_their_own():
+    """An in-place change of one does not touch the others, nor what autograd
+    saved of them, and none keeps another's memory."""
+    need_gpu()
+    for rows in (3, 400):
+        r = q4.token_logprobs(torch.randn((rows, 3000), device="cuda"), torch.zeros(rows, dtype=torch.int64, device="cuda"), top_k=4)
+        own_memory(list(r))
+    weight = torch.ones(400, device="cuda", requires_grad=True)
+    loss = (r.logprob * weight).sum()  # saves logprob
+    r.entropy.mul_(2)
+    loss.backward()
+    assert torch.equal(weight.grad, r.logprob)
+    own_memory(list(q4.kv_dequant(*q4.new_cache(3, 2, 64, 16))))
