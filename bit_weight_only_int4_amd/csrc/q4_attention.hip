@@ -138,17 +138,20 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // longer way to the first key cost more than the sharing gives.  Bf16, 32 query
 // and 8 kv heads of 128, 16-row workgroups against wide ones, us:
 //   new tokens x sequences over positions   rows   rows x tiles   16-row   wide
-//   128 x 1 over 1000                       4096          2^16      11.9   21.8
-//   64 x 1 over 4000                        2048          2^17      22.2   26.0
-//   64 x 4 over 1000                        8192          2^17      18.2   25.2
-//   128 x 1 over 4000                       4096          2^18      33.5   33.4
-//   64 x 1 over 16000                       2048          2^19      54.1   40.8
-//   32 x 4 over 16000                       4096          2^20       100   67.9
-//   256 x 4 over 256                       32768          2^17      31.2   20.4
-//   64 x 64 over 64                       131072          2^17       105   50.4
-//   16 x 64 over 2000                      32768          2^20       165    105
-//   12 x 16 over 4000                       6144          2^19      53.9   43.3
-//   8 x 256 over 100 (32 rows a head)      65536          2^17      61.6   78.1
+//   128 x 1 over 1000                       4096          2^16      12.5   29.8
+//   64 x 1 over 4000                        2048          2^17      24.5   31.3
+//   64 x 4 over 1000                        8192          2^17      19.0   30.6
+//   128 x 1 over 4000                       4096          2^18      34.5   39.0
+//   64 x 1 over 16000                       2048          2^19      56.7   49.1
+//   32 x 4 over 16000                       4096          2^20       105   82.4
+//   256 x 4 over 256                       32768          2^17      32.3   21.9
+//   64 x 64 over 64                       131072          2^17       109   51.9
+//   16 x 64 over 2000                      32768          2^20       160    127
+//   12 x 16 over 4000                       6144          2^19      57.2   48.3
+//   8 x 256 over 100 (32 rows a head)      65536          2^17      61.7   83.6
+// (the fourth is 63 tiles, just below the limit).  Fp32, the same: 128 x 1 over
+// 4000 36.4 and 43.7, 64 x 1 over 16000 60.6 and 55.3, 256 x 4 over 256 31.6 and
+// 24.4, 64 x 64 over 64 99.5 and 65.0, 12 x 16 over 4000 58.8 and 54.6.
 //
 // 128 rows a workgroup of the wide kernel, except for fp32 queries up to heads
 // of 192: two row blocks of four digits a wave leave no registers there.  64
@@ -160,9 +163,9 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // each at least kMinTiles tiles, where row blocks alone do not give every CU
 // one (kTargetBlocks); and, where they do, to at most kRagged, each at least
 // kRaggedTiles tiles, as sequences differ in length and the longest would run
-// alone at the end (64 sequences of 500 to 8000 tokens, 8 kv heads of 128: 104
-// us with one, 81 with four; of 9000 tokens each, where nothing is gained, 204
-// and 212).  Equal pieces for all workgroups, cut from the tiles of all
+// alone at the end (64 sequences of 500 to 8000 tokens, 8 kv heads of 128, fp32:
+// 103 us with one, 79 with four; of 9000 tokens each, where nothing is gained,
+// 201 and 212).  Equal pieces for all workgroups, cut from the tiles of all
 // sequences in a row, were measured and not kept: the longer way to the first
 // key and the second launch cost what the balance gave (84 and 231 us).
 // max_len and the window bound the tiles: neither the grid nor the workspace

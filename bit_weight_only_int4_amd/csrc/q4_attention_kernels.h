@@ -17,8 +17,8 @@
 // to reach past the type's bits by what elements lie apart: 16-bit queries
 // take three (23 bits), fp32 ones four (31).  With one fewer, which was
 // measured first, a query channel 200 times the others cost 16-bit outputs
-// 4e-3 of themselves and fp32 ones 1e-5, a first token with nine tenths of the
-// weight and no value 7e-3 and 3e-5; now 1e-5 and 5e-8, 3e-5 and 1e-7.  Its
+// 3e-3 of themselves and fp32 ones 2e-5, a first token with nine tenths of the
+// weight and no value 5e-3 and 2e-5; now 2e-5 and 5e-8, 2e-5 and 8e-8.  Its
 // price is in the prompt chunks, which the vector unit bounds (2890 tokens
 // over up to 5441: bf16 217 to 267 us, fp32 283 to 338); decode steps wait for
 // memory (64 sequences of 500 to 8000: 78 to 79).
@@ -435,8 +435,8 @@ struct Tile {
 // lane's column state.  The next tile's keys and page numbers load while this
 // one's scores become probabilities, its values while its scores form.  Two or
 // three waves share a SIMD.  One wave per SIMD with whole tiles in two register
-// buffers took 93 us where this takes 84 (64 sequences of 500 to 8000 tokens,
-// 8 kv heads of 128).
+// buffers took 93 us where this took 84 (three digits, 64 sequences of 500 to
+// 8000 tokens, 8 kv heads of 128).
 template <int DT, int ND, bool UNIFORM>
 __device__ __forceinline__ void attend(const AttnParams& p, const Block& k, int t, int t_end,
                                        int step, Column<DT>& st) {

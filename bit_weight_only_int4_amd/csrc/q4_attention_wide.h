@@ -222,7 +222,8 @@ __global__ __launch_bounds__(kThreads, DT <= 8 ? 2 : 1) void attention_wide_kern
     fetch_pair(t + 2, buf ^ 1);
     load_pair(t + 4);
     // A wave in its matrix instructions goes before one in its exponentials, so
-    // that the two units are busy at once (4% here)
+    // that the two units are busy at once (2890 tokens over up to 5441, bf16: 269
+    // us, 278 without it)
     __builtin_amdgcn_s_setprio(0);
     const int64_t token0 = (int64_t)(k.tile0 + t) * kTile;
     if (idle || token0 >= some.hi || token0 + 2 * kTile <= some.lo) continue;

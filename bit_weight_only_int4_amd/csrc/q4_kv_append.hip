@@ -7,7 +7,7 @@
 // page's new scale, together with what the page held if the scale grew.  A
 // thread's share of K is 4 pairs of a token (dword stores of codes), of V 16
 // tokens of a column, so that neither passes through LDS: with the rows kept
-// there a prompt of 6000 tokens took 103 us, the turning of its queries, in
+// there prompts of 6531 tokens took 103 us, the turning of their queries, in
 // the rest of the grid, being held to the same 34 KB of LDS a workgroup.
 // Bound by HBM for prompts (each element is read and written once), by the
 // chain table -> row -> maximum -> store for decode steps.
@@ -473,7 +473,7 @@ hipError_t launch_kv_append(const AppendParams& in, int32_t dtype, int64_t max_n
   int64_t turns = p.q ? append_turns(p.T) : 0;
   const int64_t rows = max_new < p.c.page ? max_new : p.c.page;
   // One launch, unless a loose max_new makes more workgroups than that may have
-  // (a loop over pages in the kernel costs it registers: 6000 tokens of prompts
+  // (a loop over pages in the kernel costs it registers: 6531 tokens of prompts
   // 73 -> 105 us).
   const int64_t a_page = (int64_t)p.batch * p.c.heads * 2;
   for (int64_t j = 0; j < touched; j += p.touched) {
