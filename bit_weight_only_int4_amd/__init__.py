@@ -12,11 +12,18 @@ the seeded synthetic workloads (``workloads``).
 Beside the layer, ``serve`` has what a decoder runs between its linears: a
 paged 8-bit key/value cache (``kv_append``), attention over it
 (``attention``), and log probabilities of the head's logits with their
-gradient (``token_logprobs``), behind ``include/q4serve.h``.
+gradient (``token_logprobs``), behind ``include/q4serve.h``.  ``mixture`` has
+the layer's form for mixtures of experts (``route``, ``experts``) and the loss
+at the packed head without its logits (``head_cross_entropy``), with their
+gradients, behind ``include/q4experts.h``.
 """
 from .q4linear import (Q4Error, backward_workspace_bytes, dequant,  # noqa: F401
                        library_path, lib, linear, linear_backward, requant,
                        unpack_codes, workspace_bytes)
+from .mixture import (HeadLoss, Route, experts, experts_backward,  # noqa: F401
+                      experts_backward_workspace_bytes, experts_workspace_bytes, head_cross_entropy,
+                      head_cross_entropy_backward, head_cross_entropy_backward_workspace_bytes,
+                      head_cross_entropy_workspace_bytes, route, route_backward)
 from .serve import (TokenLogprobs, attention, attention_workspace_bytes,  # noqa: F401
                     kv_append, kv_dequant, new_cache, token_logprobs,
                     token_logprobs_backward)

@@ -1,6 +1,6 @@
 """Build the gfx950 HIP library ``libq4linear.so`` in-tree, and the native
-half of the Python binding ``serve`` (``_serve_native.so``: host code, against
-torch's headers) beside it.
+half of the Python bindings ``serve`` and ``mixture`` (``_serve_native.so``: host
+code, against torch's headers) beside it.
 
 Every source under ``csrc/`` is compiled with hipcc for gfx950 only, in
 parallel, then linked into one shared library beside this file.  No
@@ -38,8 +38,9 @@ CFLAGS = [
 ]
 
 
-# sources of the operators around the layer (include/q4serve.h)
-SERVE = ("q4serve.h", "q4_serve", "q4_kv", "q4_attention", "q4_logprobs")
+# sources of the operators around the layer (include/q4serve.h, include/q4experts.h)
+SERVE = ("q4serve.h", "q4_serve", "q4_kv", "q4_attention", "q4_logprobs", "q4experts.h",
+         "q4_experts", "q4_route")
 
 
 def _digest(files) -> str:

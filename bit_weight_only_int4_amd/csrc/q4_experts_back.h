@@ -1,0 +1,360 @@
+// q4_experts_back.h -- the input gradient through packed 4-bit matrices for
+// many rows, on MFMA; instantiated by q4_experts_back_*.hip.
+//
+//   z[r, k] = sum_n (d[r, n] s[g(k), n]) c[n, k]
+//
+// contracted over the rows n of the packed matrix.  The scale of a column's
+// group belongs to the row operand here: d times the scales of the tile's
+// group is formed in fp32 on the way into LDS and split into binary16 parts
+// there (d against its row's largest magnitude, the scales against their
+// matrix's), so codes stay exact integers.  128 columns of one group need one
+// such operand; with groups of 32 or 64 each 32 columns have their own (NG = 4).
+//
+// Codes lie along k, the contraction runs along n: a thread takes a word (8 k)
+// of four rows n, turns its 4 x 8 nibbles around in registers (12 operations)
+// and writes 16 bits for each k, so LDS holds the tile packed along n and a
+// wave unpacks it as the forward product does.  Within each 32 columns the order
+// is (k % 4 word, k in word) so that the writes spread over the banks.
+//
+// Tiles of BM rows by 128 columns, four waves of BM/2 x 64; the next step's
+// loads are in registers while a step's products run.
+#pragma once
+
+#include "q4_experts.h"
+#include "q4_experts_device.h"
+#include "q4_experts_gemm.h"
+
+namespace q4 {
+
+template <int P, int BM, int NG>
+struct BackTile {
+  static constexpr int kN = NG == 1 ? 64 : 32;  // n of a step
+  static constexpr int kPart = BM * kN * 2;     // bytes of one part of one operand
+  static constexpr int kA = NG * P * kPart;
+  static constexpr int kB = 128 * kN / 2;
+  static constexpr int kStage = kA + kB;
+  static constexpr int kStages = 2 * kStage <= 76 * 1024 ? 2 : 1;
+};
+
+// Words of rows n .. n + 3 at the same 8 k, as 8 half words: element i holds
+// nibble i of the four rows, the first row lowest.  Pairs (0, 4), (1, 5), (2,
+// 6), (3, 7) share a register: low half first.
+__device__ __forceinline__ void turn_words(const uint32_t (&w)[4], uint32_t (&t)[4]) {
+  constexpr uint32_t m = 0x0F0F0F0Fu;
+  const uint32_t e01 = (w[0] & m) | ((w[1] << 4) & ~m), e23 = (w[2] & m) | ((w[3] << 4) & ~m);
+  const uint32_t o01 = ((w[0] >> 4) & m) | (w[1] & ~m), o23 = ((w[2] >> 4) & m) | (w[3] & ~m);
+  // bytes j of the e's are nibble 2 j of two rows each, of the o's nibble 2 j + 1
+  t[0] = __builtin_amdgcn_perm(e23, e01, 0x06020400u);  // nibbles 0 and 4
+  t[1] = __builtin_amdgcn_perm(o23, o01, 0x06020400u);  // 1, 5
+  t[2] = __builtin_amdgcn_perm(e23, e01, 0x07030501u);  // 2, 6
+  t[3] = __builtin_amdgcn_perm(o23, o01, 0x07030501u);  // 3, 7
+}
+
+template <int P, typename T, int BM, int NG, bool GATE>
+__global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
+  typedef BackTile<P, BM, NG> L;
+  constexpr int RB = BM / 64, NS = L::kN, S = L::kStages;
+  constexpr int kChunks = NS / 8;            // 16-byte pieces of a row
+  constexpr int kPasses = BM * kChunks / 256;  // rows of a thread
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  __shared__ int32_t sh_slot[BM], sh_exp[BM];
+  __shared__ float sh_weight[GATE ? BM : 1];
+
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wr = w >> 1, wc = w & 1, c = lane & 31, q = lane >> 5;
+
+  const int32_t row_tiles = p.tiles ? *p.n_tiles : p.row_tiles;
+  const uint32_t total = (uint32_t)row_tiles * (uint32_t)p.col_tiles * (uint32_t)p.splits;
+  if (blockIdx.x >= total) return;
+  uint32_t at = xcd_swizzle(blockIdx.x, total);
+  int mt, ct, split = 0, expert = 0, first, rows;
+  if (p.tiles) {
+    mt = (int)(at / (uint32_t)p.col_tiles);
+    ct = (int)(at % (uint32_t)p.col_tiles);
+    const Tile t = p.tiles[mt];
+    expert = t.expert;
+    first = t.first;
+    rows = t.rows;
+  } else {
+    // a split's rows of the matrix stay with one XCD
+    const uint32_t plane = (uint32_t)row_tiles * (uint32_t)p.col_tiles;
+    split = (int)(at / plane);
+    at %= plane;
+    mt = (int)(at % (uint32_t)row_tiles);
+    ct = (int)(at / (uint32_t)row_tiles);
+    first = mt * BM;
+    rows = (int)(p.M - first < BM ? p.M - first : BM);
+  }
+  const int64_t K = p.w.K, N = p.w.N, ldq = K >> 1;
+  const int64_t k0 = (int64_t)ct * 128;
+  const int s_exp = top_exponent(p.s_bits[expert]);
+  // this split's rows of the matrix
+  const int64_t per = ((p.n_rows + p.splits - 1) / p.splits + NS - 1) / NS * NS;
+  const int64_t nb = per * split < p.n_rows ? per * split : p.n_rows;
+  const int64_t ne = nb + per < p.n_rows ? nb + per : p.n_rows;
+  const int steps = (int)((ne - nb + NS - 1) / NS);
+
+  auto row_of = [&](int r) { return r < rows ? r : rows - 1; };
+  if (tid < BM) {
+    const int r = row_of(tid);
+    const int32_t slot = p.slots ? p.slots[first + r] : first + r;
+    const int64_t dr = p.slots ? slot / p.slots_per_row : slot;
+    sh_slot[tid] = tid < rows ? slot : -1;
+    sh_exp[tid] = top_exponent(p.d_bits[dr]);
+    if constexpr (GATE) sh_weight[tid] = p.weights[slot];
+  }
+
+  // this thread's part of the row operand: 8 n of kPasses rows
+  const int chunk = tid % kChunks, arow = tid / kChunks;
+  const T* dsrc[kPasses];
+  int de[kPasses];
+#pragma unroll
+  for (int i = 0; i < kPasses; ++i) {
+    const int r = row_of(arow + i * (256 / kChunks));
+    const int32_t slot = p.slots ? p.slots[first + r] : first + r;
+    const int64_t dr = p.slots ? slot / p.slots_per_row : slot;
+    dsrc[i] = (const T*)p.d + dr * p.ldd;
+    de[i] = -top_exponent(p.d_bits[dr]);
+  }
+  const float* scales = p.w.scales + expert * p.w.expert_scales + p.n0;
+  int64_t group_at[NG];
+#pragma unroll
+  for (int g = 0; g < NG; ++g) {
+    const int64_t gr = p.w.group ? (k0 + g * 32) / p.w.group : 0;
+    group_at[g] = (gr < p.w.G ? gr : p.w.G - 1) * N;
+  }
+  // and of the codes: a word of four rows
+  const int kw = tid & 15, u = tid >> 4;
+  const bool codes_mine = u < NS / 4;
+  const int64_t kword = k0 + kw * 8 < K ? k0 / 8 + kw : 0;
+  const uint8_t* codes = p.w.qw + expert * p.w.expert_bytes + p.n0 * ldq + kword * 4;
+
+  const bool d_vec = p.d_vec != 0;
+  struct Fetch {
+    float d[kPasses][8], s[NG][8];
+    uint32_t w[4];
+  } f;
+  auto fetch = [&](int step) {
+    const int64_t n = nb + (int64_t)step * NS + chunk * 8;
+    const bool full = n + 8 <= ne;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i) {
+      if (full && d_vec) {
+        constexpr int v = 16 / sizeof(T);
+        typedef T tv __attribute__((ext_vector_type(v)));
+#pragma unroll
+        for (int j = 0; j < 8 / v; ++j) {
+          const tv x = *(const tv*)(dsrc[i] + n + j * v);
+#pragma unroll
+          for (int e = 0; e < v; ++e) f.d[i][j * v + e] = to_f32(x[e]);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f.d[i][e] = n + e < ne ? to_f32(dsrc[i][n + e]) : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      const float* s = scales + group_at[g] + n;
+      if (full) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const f32x4_a4 x = *(const f32x4_a4*)(s + 4 * j);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) f.s[g][j * 4 + e] = x[e];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f.s[g][e] = n + e < ne ? s[e] : 0.0f;
+      }
+    }
+    if (codes_mine) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t r = nb + (int64_t)step * NS + 4 * u + i;
+        // (rows past the end: any codes, the other operand is 0)
+        f.w[i] = *(const uint32_t*)(codes + (r < ne ? r : ne - 1) * ldq);
+      }
+    }
+  };
+  auto turn_of = [](int row) { return NS == 64 ? (row >> 1) & 7 : (row >> 2) & 3; };
+  auto store = [&](int step) {
+    uint8_t* base = smem + (S == 2 ? (step & 1) * L::kStage : 0);
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      float s[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[e] = __builtin_ldexpf(f.s[g][operand_nibble(e)], 15 - s_exp);
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+        const int row = arow + i * (256 / kChunks);
+        h8 hi, lo;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float x = settled(__builtin_ldexpf(f.d[i][operand_nibble(e)], de[i]) * s[e]);
+          hi[e] = part_hi(x);
+          if constexpr (P == 2) lo[e] = part_lo(x, hi[e]);
+        }
+        uint8_t* dst = base + g * P * L::kPart + row * (NS * 2) + ((chunk ^ turn_of(row)) * 16);
+        *(h8*)dst = hi;
+        if constexpr (P == 2) *(h8*)(dst + L::kPart) = lo;
+      }
+    }
+    if (codes_mine) {
+      uint32_t t[4];
+      turn_words(f.w, t);
+      // n word u / 2, half u % 2, of column (kw, k in word)
+      uint8_t* dst = base + L::kA + ((kw >> 2) * 32 + (kw & 3)) * (NS / 2) + (u >> 1) * 4 + (u & 1) * 2;
+      const int flip = p.nibble_order == Q4_ORDER_LOW_FIRST ? 0 : 1;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        *(uint16_t*)(dst + (i ^ flip) * 4 * (NS / 2)) = (uint16_t)t[i];
+        *(uint16_t*)(dst + ((i + 4) ^ flip) * 4 * (NS / 2)) = (uint16_t)(t[i] >> 16);
+      }
+    }
+  };
+
+  f32x16 acc[RB][2];
+#pragma unroll
+  for (int r = 0; r < RB; ++r)
+#pragma unroll
+    for (int b = 0; b < 2; ++b) acc[r][b] = f32x16{};
+  const Magic magic = Magic::make();
+  auto products = [&](int step) {
+    const uint8_t* base = smem + (S == 2 ? (step & 1) * L::kStage : 0);
+#pragma unroll
+    for (int h = 0; h < NS / 32; ++h) {
+      uint32_t words[2][2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const u32x2 x = *(const u32x2*)(base + L::kA + (wc * 64 + b * 32 + c) * (NS / 2) + h * 16 + q * 8);
+        words[b][0] = x[0];
+        words[b][1] = x[1];
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const h8 bo[2] = {codes_of(words[0][j], magic), codes_of(words[1][j], magic)};
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+          const int row = wr * (BM / 2) + r * 32 + c;
+          const int at_ = row * (NS * 2) + (((h * 4 + q * 2 + j) ^ turn_of(row)) * 16);
+#pragma unroll
+          for (int pc = 0; pc < P; ++pc) {
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const int g = NG == 1 ? 0 : wc * 2 + b;
+              const h8 a = *(const h8*)(base + (g * P + pc) * L::kPart + at_);
+              acc[r][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, bo[b], acc[r][b], 0, 0, 0);
+            }
+          }
+        }
+      }
+    }
+  };
+
+  if (steps > 0) {
+    fetch(0);
+    if constexpr (S == 2) {
+      store(0);
+      if (steps > 1) fetch(1);
+      lds_barrier();
+      for (int st = 0; st < steps; ++st) {
+        products(st);
+        if (st + 1 < steps) store(st + 1);
+        if (st + 2 < steps) fetch(st + 2);
+        lds_barrier();
+      }
+    } else {
+      for (int st = 0; st < steps; ++st) {
+        lds_barrier();
+        store(st);
+        lds_barrier();
+        if (st + 1 < steps) fetch(st + 1);
+        products(st);
+      }
+    }
+  } else {
+    lds_barrier();
+  }
+  settle(acc);
+
+  // ---- results -------------------------------------------------------------
+#pragma unroll
+  for (int r = 0; r < RB; ++r) {
+    const int r0 = wr * (BM / 2) + r * 32 + 4 * q;
+    if constexpr (GATE) {
+      float dot[16], top[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) dot[i] = top[i] = 0.0f;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int64_t k = k0 + wc * 64 + b * 32 + (c & 3) * 8 + (c >> 2);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int row = r0 + 8 * (i >> 2) + (i & 3), slot = sh_slot[row];
+          if (slot < 0 || k >= K) continue;
+          const float z = __builtin_ldexpf(acc[r][b][i], sh_exp[row] + s_exp - 15);
+          const float* pre = p.pre + (int64_t)slot * 2 * K + k;
+          const float g = pre[0], up = pre[K];
+          const float sig = sigmoid(g), silu = g * sig;
+          dot[i] = __builtin_fmaf(silu * up, z, dot[i]);
+          const float dh = sh_weight[row] * z;
+          const float dg = dh * up * sig * __builtin_fmaf(g, sigmoid(-g), 1.0f), du = dh * silu;
+          float* dst = p.dpre + (int64_t)slot * 2 * K + k;
+          dst[0] = dg;
+          dst[K] = du;
+          const uint32_t m = umax(finite_bits(dg), finite_bits(du));
+          top[i] = bits_f32(umax(f32_bits(top[i]), m));
+        }
+      }
+      const float sum = reduce16(dot, lane, [](float x, float y) { return x + y; });
+      const float most = reduce16(top, lane, [](float x, float y) { return x > y ? x : y; });
+      if ((lane & 16) == 0) {
+        const int i = lane & 15, row = r0 + 8 * (i >> 2) + (i & 3), slot = sh_slot[row];
+        if (slot >= 0) {
+          p.dw_part[((int64_t)slot * p.col_tiles + ct) * 2 + wc] = sum;
+          atomicMax(p.dpre_bits + slot, f32_bits(most));
+        }
+      }
+    } else {
+      float* out = p.out + (int64_t)split * p.M * p.out_ld;
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int64_t k = k0 + wc * 64 + b * 32 + (c & 3) * 8 + (c >> 2);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int row = r0 + 8 * (i >> 2) + (i & 3), slot = sh_slot[row];
+          if (slot < 0 || k >= K) continue;
+          const float z = __builtin_ldexpf(acc[r][b][i], sh_exp[row] + s_exp - 15);
+          float* dst = out + (int64_t)slot * p.out_ld + k;
+          *dst = p.accumulate ? *dst + z : z;
+        }
+      }
+    }
+  }
+}
+
+template <int P, typename T, int BM, bool GATE>
+hipError_t launch_back_tile(const BackParams& p, hipStream_t s) {
+  const dim3 grid((uint32_t)((int64_t)p.row_tiles * p.col_tiles * p.splits));
+#define Q4_BACK(NG)                                                                          \
+  do {                                                                                       \
+    typedef BackTile<P, BM, NG> L;                                                           \
+    constexpr int lds = L::kStages * L::kStage;                                              \
+    if (lds > 64 * 1024) {                                                                   \
+      const hipError_t e = hipFuncSetAttribute((const void*)back_kernel<P, T, BM, NG, GATE>,  \
+                                               hipFuncAttributeMaxDynamicSharedMemorySize, lds); \
+      if (e != hipSuccess) return e;                                                         \
+    }                                                                                        \
+    hipLaunchKernelGGL((back_kernel<P, T, BM, NG, GATE>), grid, dim3(256), lds, s, p);       \
+  } while (0)
+  if (p.w.group % 128 == 0)
+    Q4_BACK(1);
+  else
+    Q4_BACK(4);
+#undef Q4_BACK
+  return hipGetLastError();
+}
+
+}  // namespace q4

@@ -1,0 +1,38 @@
+// q4_experts_back.hip -- the choice of a tile for input gradients of many rows
+// (q4_experts_back.h).
+#include "q4_experts_back.h"
+
+namespace q4 {
+
+#define Q4_TILES(P, T, GATE)                                                            \
+  extern template hipError_t launch_back_tile<P, T, 64, GATE>(const BackParams&, hipStream_t); \
+  extern template hipError_t launch_back_tile<P, T, 128, GATE>(const BackParams&, hipStream_t);
+Q4_TILES(2, _Float16, true)
+Q4_TILES(2, bf16, true)
+Q4_TILES(2, float, true)
+Q4_TILES(1, float, false)
+Q4_TILES(2, float, false)
+#undef Q4_TILES
+
+namespace {
+template <int P, typename T, bool GATE>
+hipError_t by_tile(const BackParams& p, int32_t tile_rows, hipStream_t s) {
+  return tile_rows == 128 ? launch_back_tile<P, T, 128, GATE>(p, s) : launch_back_tile<P, T, 64, GATE>(p, s);
+}
+}  // namespace
+
+hipError_t launch_back(const BackParams& in, int32_t tile_rows, bool gate, hipStream_t s) {
+  BackParams p = in;
+  const int64_t e = p.d_dtype == Q4_DTYPE_F32 ? 4 : 2;
+  p.d_vec = reinterpret_cast<uintptr_t>(p.d) % 16 == 0 && p.ldd * e % 16 == 0;
+  if (!gate)
+    return p.parts == 2 ? by_tile<2, float, false>(p, tile_rows, s) : by_tile<1, float, false>(p, tile_rows, s);
+  // two parts whatever the type: the gradient of the weights is fp32
+  switch (p.d_dtype) {
+    case Q4_DTYPE_F32: return by_tile<2, float, true>(p, tile_rows, s);
+    case Q4_DTYPE_F16: return by_tile<2, _Float16, true>(p, tile_rows, s);
+    default: return by_tile<2, bf16, true>(p, tile_rows, s);
+  }
+}
+
+}  // namespace q4

@@ -1,0 +1,9 @@
+// The tiles of q4_experts_gemm.h with activations of 2 binary16 part(s), for the experts.
+#include "q4_experts_gemm.h"
+
+namespace q4 {
+template hipError_t launch_gemm_tile<2, 64, kGatedRows>(const GemmParams&, hipStream_t);
+template hipError_t launch_gemm_tile<2, 128, kGatedRows>(const GemmParams&, hipStream_t);
+template hipError_t launch_gemm_tile<2, 64, kPlainRows>(const GemmParams&, hipStream_t);
+template hipError_t launch_gemm_tile<2, 128, kPlainRows>(const GemmParams&, hipStream_t);
+}  // namespace q4

@@ -1,0 +1,361 @@
+// q4_experts_rows.hip -- what goes on around the matrix kernels of packed
+// experts: rows listed by expert, activations split into binary16 parts, sums
+// over a token's slots, largest magnitudes, and the head's last steps.  All of them read their input once or twice and are bound by HBM, or
+// by their launch where rows are few.
+#include <hip/hip_runtime.h>
+
+#include "q4_experts.h"
+#include "q4_experts_device.h"
+
+namespace q4 {
+namespace {
+
+__device__ __forceinline__ uint32_t block_umax(uint32_t v, uint32_t* sh) {
+  v = wave_umax(v);
+  const int w = threadIdx.x >> 6, nw = blockDim.x >> 6;
+  if ((threadIdx.x & 63) == 0) sh[w] = v;
+  __syncthreads();
+  for (int i = 0; i < nw; ++i) v = umax(v, sh[i]);
+  __syncthreads();
+  return v;
+}
+
+// Eight elements of a row from k, zeros past K.
+template <typename T>
+__device__ __forceinline__ void load8(const T* row, int64_t k, int64_t K, bool vec, float (&v)[8]) {
+  if (vec) {  // K is a multiple of 8
+    if constexpr (sizeof(T) == 4) {
+      const f32x4 a = *(const f32x4*)(row + k), b = *(const f32x4*)(row + k + 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
+    } else {
+      typedef T t8 __attribute__((ext_vector_type(8)));
+      const t8 a = *(const t8*)(row + k);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = (float)a[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = k + i < K ? to_f32(row[k + i]) : 0.0f;
+  }
+}
+
+// ---- rows by expert --------------------------------------------------------
+
+// One workgroup: a histogram of the ids, its prefix sums (rows and tiles), and
+// the slots scattered behind their expert's start.  The order within an expert
+// is that of arrival and changes nothing: a row's result does not depend on its
+// place in a tile.
+constexpr int kListThreads = 1024;
+__global__ void __launch_bounds__(kListThreads)
+lists_kernel(const int32_t* __restrict__ ids, int32_t n, int32_t experts, int32_t tile_rows,
+             const RowLists r) {
+  __shared__ int32_t count[kMaxExperts], next[kMaxExperts];
+  __shared__ int32_t wave_rows[kListThreads / 64], wave_tiles[kListThreads / 64];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+  count[tid] = 0;
+  __syncthreads();
+  for (int64_t i = tid; i < n; i += kListThreads) {
+    const int32_t id = ids[i];
+    if (id_ok(id, experts)) atomicAdd(&count[id], 1);
+  }
+  __syncthreads();
+  // thread e: expert e
+  const int32_t c = count[tid], mine = (c + tile_rows - 1) / tile_rows;
+  int32_t rows = c, tiles = mine;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int32_t a = __shfl_up(rows, d, 64), b = __shfl_up(tiles, d, 64);
+    if (lane >= d) rows += a, tiles += b;
+  }
+  if (lane == 63) wave_rows[w] = rows, wave_tiles[w] = tiles;
+  __syncthreads();
+  int32_t rows0 = 0, tiles0 = 0, all = 0;
+  for (int i = 0; i < kListThreads / 64; ++i) {
+    if (i < w) rows0 += wave_rows[i], tiles0 += wave_tiles[i];
+    all += wave_tiles[i];
+  }
+  rows0 += rows - c;
+  tiles0 += tiles - mine;
+  next[tid] = rows0;
+  for (int32_t i = 0; i < mine; ++i) {
+    const int32_t left = c - i * tile_rows;
+    r.tiles[tiles0 + i] = Tile{tid, rows0 + i * tile_rows, left < tile_rows ? left : tile_rows, 0};
+  }
+  if (tid == 0) *r.n_tiles = all;
+  __syncthreads();
+  for (int64_t i = tid; i < n; i += kListThreads) {
+    const int32_t id = ids[i];
+    if (id_ok(id, experts)) r.slots[atomicAdd(&next[id], 1)] = (int32_t)i;
+  }
+}
+
+// ---- activations into binary16 parts -----------------------------------------
+
+// A workgroup a row: its largest magnitude, then every word of 8 elements in
+// the order of the codes' operands.
+template <typename T>
+__global__ void __launch_bounds__(256)
+split_kernel(const T* __restrict__ x, int64_t ldx, int64_t K, int32_t order,
+             const int32_t* __restrict__ ids, int32_t experts, const SplitRows r, bool vec) {
+  __shared__ uint32_t sh[4];
+  const int tid = threadIdx.x;
+  const int64_t row = blockIdx.x;
+  if (ids && !id_ok(ids[row], experts)) return;
+  const T* src = x + row * ldx;
+  uint32_t m = 0;
+  for (int64_t k = 8 * tid; k < K; k += 8 * 256) {
+    float v[8];
+    load8(src, k, K, vec, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = umax(m, finite_bits(v[i]));
+  }
+  const int e = row_exponent(block_umax(m, sh));
+  if (tid == 0) r.e[row] = e;
+  for (int64_t k = 8 * tid; k < r.Kp; k += 8 * 256) {
+    float v[8];
+    if (k < K) {
+      load8(src, k, K, vec, v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+    }
+    h8 hi, lo;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int nib = operand_nibble(i);
+      const float s = settled(__builtin_ldexpf(order == Q4_ORDER_LOW_FIRST ? v[nib] : v[nib ^ 1], e));
+      hi[i] = part_hi(s);
+      lo[i] = part_lo(s, hi[i]);
+    }
+    *(h8*)(r.a + row * r.Kp + k) = hi;
+    if (r.parts == 2) *(h8*)(r.a + (r.rows + row) * r.Kp + k) = lo;
+  }
+}
+
+// ---- sums over a token's slots -------------------------------------------------
+
+template <typename T>
+__global__ void __launch_bounds__(256) combine_kernel(const CombineParams p, bool vec) {
+  const int64_t n = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+  if (n >= p.N) return;  // N is a multiple of 8
+  for (int64_t t = blockIdx.y; t < p.T; t += gridDim.y) {
+    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    bool bad = false;
+    for (int j = 0; j < p.top_k; ++j) {
+      const int64_t slot = t * p.top_k + j;
+      const int32_t id = p.ids[slot];
+      bad |= id >= p.experts;
+      if (!id_ok(id, p.experts)) continue;
+      const float w = p.weights ? p.weights[slot] : 1.0f;
+      const f32x4 y = *(const f32x4*)(p.y + slot * p.N + n);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) sum[i] = __builtin_fmaf(w, y[i], sum[i]);
+    }
+    if (bad) sum = f32x4{} + bits_f32(0x7fc00000u);
+    T* dst = (T*)p.out + t * p.ldo + n;
+    typedef T t4 __attribute__((ext_vector_type(4)));
+    if (vec) {
+      t4 v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = from_f32<T>(sum[i]);
+      *(t4*)dst = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dst[i] = from_f32<T>(sum[i]);
+    }
+  }
+}
+
+// ---- largest magnitudes ----------------------------------------------------------
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+row_bits_kernel(const T* __restrict__ x, int64_t ldx, int64_t rows, int64_t K, uint32_t* bits,
+                uint32_t* zero, int64_t zeros, bool vec) {
+  __shared__ uint32_t sh[4];
+  const int64_t row = blockIdx.x;
+  if (row >= rows) {
+    const int64_t i = (row - rows) * 256 + threadIdx.x;
+    if (i < zeros) zero[i] = 0;
+    return;
+  }
+  uint32_t m = 0;
+  for (int64_t k = 8 * (int64_t)threadIdx.x; k < K; k += 8 * 256) {
+    float v[8];
+    load8(x + row * ldx, k, K, vec, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = umax(m, finite_bits(v[i]));
+  }
+  m = block_umax(m, sh);
+  if (threadIdx.x == 0) bits[row] = m;
+}
+
+constexpr int kScaleRun = 8192;  // scales of a workgroup
+__global__ void __launch_bounds__(256)
+scale_bits_kernel(const float* __restrict__ s, int64_t n, uint32_t* bits) {
+  __shared__ uint32_t sh[4];
+  const float* src = s + (int64_t)blockIdx.y * n;
+  const int64_t at = (int64_t)blockIdx.x * kScaleRun;
+  const int64_t end = at + kScaleRun < n ? at + kScaleRun : n;
+  uint32_t m = 0;
+  for (int64_t i = at + threadIdx.x; i < end; i += 256) m = umax(m, finite_bits(src[i]));
+  m = block_umax(m, sh);
+  if (threadIdx.x == 0) atomicMax(bits + blockIdx.y, m);
+}
+
+__global__ void __launch_bounds__(256)
+gate_sums_kernel(const float* __restrict__ part, int32_t parts, const int32_t* __restrict__ ids,
+                 int64_t n, int32_t experts, float* dweights) {
+  const int64_t slot = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (slot >= n) return;
+  const int32_t id = ids[slot];
+  float s = 0.0f;
+  if (id_ok(id, experts))
+    for (int i = 0; i < parts; ++i) s += part[slot * parts + i];
+  if (id >= experts) s = bits_f32(0x7fc00000u);
+  dweights[slot] = s;
+}
+
+// ---- the head's last steps -------------------------------------------------------
+
+// A wave a row: parts (maximum, sum of e^(z - maximum)) of the vocabulary's
+// tiles joined, and the loss.
+__global__ void __launch_bounds__(256) head_finish_kernel(const HeadFinish p) {
+  const int lane = threadIdx.x & 63;
+  const int64_t m = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (m >= p.M) return;
+  const float* st = p.stats + m * p.parts * 2;
+  float top = -__builtin_inff();
+  bool nan = false;
+  for (int i = lane; i < p.parts; i += 64) {
+    const float v = st[2 * i];
+    nan |= v != v || st[2 * i + 1] != st[2 * i + 1];
+    top = v > top ? v : top;
+  }
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) {
+    const float o = __shfl_xor(top, d, 64);
+    top = o > top ? o : top;
+  }
+  nan = __any(nan);
+  float sum = 0.0f;
+  for (int i = lane; i < p.parts; i += 64) {
+    const float y = (st[2 * i] - top) * kLog2e;
+    sum += st[2 * i] == top ? st[2 * i + 1] : exp2_fast(y) * st[2 * i + 1];
+  }
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, 64);
+  if (lane != 0) return;
+  float lse = top + log2_fast(sum) * kLn2;
+  if (nan || top == __builtin_inff()) lse = bits_f32(0x7fc00000u);
+  p.lse[m] = lse;
+  const int64_t t = p.targets[m];
+  p.loss[m] = t < 0 ? 0.0f : t >= p.V ? bits_f32(0x7fc00000u) : lse - p.chosen[m];
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+head_store_kernel(const float* __restrict__ acc, int32_t splits, int64_t M, int64_t K,
+                  const int64_t* __restrict__ targets, int64_t V, T* dx, int64_t lddx) {
+  const int64_t k = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (k >= K) return;
+  for (int64_t m = blockIdx.y; m < M; m += gridDim.y) {
+    const int64_t t = targets[m];
+    float v = 0.0f;
+    for (int i = 0; i < splits; ++i) v += acc[(i * M + m) * K + k];
+    v = t < 0 ? 0.0f : t >= V ? bits_f32(0x7fc00000u) : v;
+    dx[m * lddx + k] = from_f32<T>(v);
+  }
+}
+
+bool aligned16(const void* p, int64_t ld, int64_t e) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * e % 16 == 0;
+}
+
+constexpr int64_t kGridY = 65535;
+
+}  // namespace
+
+hipError_t launch_lists(const int32_t* ids, int64_t n, int64_t experts, int32_t tile_rows,
+                        const RowLists& r, hipStream_t s) {
+  static_assert(kMaxExperts == kListThreads, "a thread an expert");
+  hipLaunchKernelGGL(lists_kernel, dim3(1), dim3(kListThreads), 0, s, ids, (int32_t)n,
+                     (int32_t)experts, tile_rows, r);
+  return hipGetLastError();
+}
+
+hipError_t launch_split(const void* x, int64_t ldx, int32_t dtype, int64_t K,
+                        int32_t nibble_order, const int32_t* ids, int64_t experts,
+                        const SplitRows& r, hipStream_t s) {
+  const dim3 grid((uint32_t)r.rows);
+  if (dtype == Q4_DTYPE_F32)
+    hipLaunchKernelGGL(split_kernel<float>, grid, dim3(256), 0, s, (const float*)x, ldx, K, nibble_order, ids, (int32_t)experts, r, aligned16(x, ldx, 4));
+  else if (dtype == Q4_DTYPE_F16)
+    hipLaunchKernelGGL(split_kernel<_Float16>, grid, dim3(256), 0, s, (const _Float16*)x, ldx, K, nibble_order, ids, (int32_t)experts, r, aligned16(x, ldx, 2));
+  else
+    hipLaunchKernelGGL(split_kernel<bf16>, grid, dim3(256), 0, s, (const bf16*)x, ldx, K, nibble_order, ids, (int32_t)experts, r, aligned16(x, ldx, 2));
+  return hipGetLastError();
+}
+
+hipError_t launch_combine(const CombineParams& p, int32_t dtype, hipStream_t s) {
+  const dim3 grid((uint32_t)((p.N + 1023) / 1024), (uint32_t)(p.T < kGridY ? p.T : kGridY));
+  if (dtype == Q4_DTYPE_F32)
+    hipLaunchKernelGGL(combine_kernel<float>, grid, dim3(256), 0, s, p, aligned16(p.out, p.ldo, 4));
+  else if (dtype == Q4_DTYPE_F16)
+    hipLaunchKernelGGL(combine_kernel<_Float16>, grid, dim3(256), 0, s, p, aligned16(p.out, p.ldo, 2));
+  else
+    hipLaunchKernelGGL(combine_kernel<bf16>, grid, dim3(256), 0, s, p, aligned16(p.out, p.ldo, 2));
+  return hipGetLastError();
+}
+
+hipError_t launch_row_bits(const void* x, int64_t ldx, int32_t dtype, int64_t rows, int64_t K,
+                           uint32_t* bits, uint32_t* zero, int64_t zeros, hipStream_t s) {
+  const dim3 grid((uint32_t)(rows + (zeros + 255) / 256));
+  if (dtype == Q4_DTYPE_F32)
+    hipLaunchKernelGGL(row_bits_kernel<float>, grid, dim3(256), 0, s, (const float*)x, ldx, rows, K,
+                       bits, zero, zeros, aligned16(x, ldx, 4));
+  else if (dtype == Q4_DTYPE_F16)
+    hipLaunchKernelGGL(row_bits_kernel<_Float16>, grid, dim3(256), 0, s, (const _Float16*)x, ldx,
+                       rows, K, bits, zero, zeros, aligned16(x, ldx, 2));
+  else
+    hipLaunchKernelGGL(row_bits_kernel<bf16>, grid, dim3(256), 0, s, (const bf16*)x, ldx, rows, K,
+                       bits, zero, zeros, aligned16(x, ldx, 2));
+  return hipGetLastError();
+}
+
+hipError_t launch_scale_bits(const float* sc, int64_t per_expert, int64_t experts, uint32_t* bits,
+                             hipStream_t s) {
+  const dim3 grid((uint32_t)((per_expert + kScaleRun - 1) / kScaleRun), (uint32_t)experts);
+  hipLaunchKernelGGL(scale_bits_kernel, grid, dim3(256), 0, s, sc, per_expert, bits);
+  return hipGetLastError();
+}
+
+hipError_t launch_gate_sums(const float* part, int32_t parts, const int32_t* ids, int64_t n,
+                            int64_t experts, float* dweights, hipStream_t s) {
+  hipLaunchKernelGGL(gate_sums_kernel, dim3((uint32_t)((n + 255) / 256)), dim3(256), 0, s, part,
+                     parts, ids, n, (int32_t)experts, dweights);
+  return hipGetLastError();
+}
+
+hipError_t launch_head_finish(const HeadFinish& p, hipStream_t s) {
+  hipLaunchKernelGGL(head_finish_kernel, dim3((uint32_t)((p.M + 3) / 4)), dim3(256), 0, s, p);
+  return hipGetLastError();
+}
+
+hipError_t launch_head_store(const float* acc, int32_t splits, int64_t M, int64_t K, const int64_t* targets,
+                             int64_t V, void* dx, int64_t lddx, int32_t dtype, hipStream_t s) {
+  const dim3 grid((uint32_t)((K + 255) / 256), (uint32_t)(M < kGridY ? M : kGridY));
+  if (dtype == Q4_DTYPE_F32)
+    hipLaunchKernelGGL(head_store_kernel<float>, grid, dim3(256), 0, s, acc, splits, M, K, targets, V,
+                       (float*)dx, lddx);
+  else if (dtype == Q4_DTYPE_F16)
+    hipLaunchKernelGGL(head_store_kernel<_Float16>, grid, dim3(256), 0, s, acc, splits, M, K, targets, V,
+                       (_Float16*)dx, lddx);
+  else
+    hipLaunchKernelGGL(head_store_kernel<bf16>, grid, dim3(256), 0, s, acc, splits, M, K, targets, V,
+                       (bf16*)dx, lddx);
+  return hipGetLastError();
+}
+
+}  // namespace q4

@@ -1,6 +1,7 @@
-// q4_serve_py.cpp -- the native half of the Python binding of q4serve.h: it
+// q4_serve_py.cpp -- the native half of the Python bindings of q4serve.h and
+// (q4_experts_py.h) q4experts.h: it
 // checks tensors against the sizes the kernels will use, allocates outputs and
-// workspaces, and calls the C ABI.  serve.py holds the public functions and
+// workspaces, and calls the C ABI.  serve.py and mixture.py hold the public functions and
 // their documentation; each passes its arguments on by position.
 //
 // In C++ because of latency: a decode step makes several calls whose kernels
@@ -21,6 +22,7 @@
 #include <optional>
 #include <string>
 
+#include "q4experts.h"
 #include "q4serve.h"
 
 namespace {
@@ -402,6 +404,12 @@ PyObject* token_logprobs_backward(PyObject* const* a) {
   return THPVariable_Wrap(dx);
 }
 
+}  // namespace
+
+#include "q4_experts_py.h"
+
+namespace {
+
 // No C++ exception leaves: each becomes a Python error.
 template <PyObject* (*F)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -439,6 +447,12 @@ PyMethodDef methods[] = {Q4_METHOD(kv_append, 15),
                          Q4_METHOD(attention, 15),
                          Q4_METHOD(token_logprobs, 5),
                          Q4_METHOD(token_logprobs_backward, 8),
+                         Q4_METHOD(route, 9),
+                         Q4_METHOD(route_backward, 8),
+                         Q4_METHOD(experts, 13),
+                         Q4_METHOD(experts_backward, 13),
+                         Q4_METHOD(head_cross_entropy, 8),
+                         Q4_METHOD(head_cross_entropy_backward, 11),
                          {"set_error", set_error, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 
