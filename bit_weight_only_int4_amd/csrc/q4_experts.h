@@ -116,8 +116,8 @@ struct GemmParams {
 int32_t gemm_tile_rows(int64_t n, int64_t experts);
 hipError_t launch_gemm(const GemmParams& p, int32_t tile_rows, Epilogue epi, hipStream_t s);
 
-// Few rows per expert: 16 rows of binary16 operands a tile, weights straight
-// from memory into the matrix operands.
+// Few rows per expert: up to 16 rows of binary16 operands a tile, weights
+// straight from memory into the matrix operands.
 struct FewParams {
   Packed w;
   const void* x;          // rows of dtype
@@ -136,8 +136,9 @@ struct FewParams {
   float* pre;
   int64_t width;
 };
-constexpr int kFewDirect = 512;  // slots up to which workgroups find their rows themselves
-hipError_t launch_few(const FewParams& p, bool gated, hipStream_t s);
+constexpr int64_t kFewDepth = 8192;  // of their rows, at most
+constexpr int kFewDirect = 64;  // slots up to which workgroups find their rows themselves
+hipError_t launch_few(const FewParams& p, int32_t tile_rows, bool gated, hipStream_t s);
 
 // out[t] = sum_j weights[t, j] y[t * top_k + j]; weights NULL: all 1
 struct CombineParams {

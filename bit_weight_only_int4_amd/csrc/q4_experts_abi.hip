@@ -40,7 +40,7 @@ bool apart(const Range (&outs)[NO], const Range (&ins)[NI]) {
 }
 
 constexpr int64_t kMaxRows = (int64_t)1 << 24;   // rows, slots
-constexpr int64_t kMaxDepth = (int64_t)1 << 16;  // hidden, width
+constexpr int64_t kMaxDepth = (int64_t)1 << 15;  // hidden, width
 constexpr int64_t kMaxVocab = (int64_t)1 << 30;
 constexpr int64_t kMaxPitch = (int64_t)1 << 37;
 
@@ -115,10 +115,13 @@ ExpertsPlan plan_experts(void* ws, int32_t dtype, int64_t T, int64_t H, int64_t 
   p.n = T * k;
   const int32_t parts = parts_of(dtype);
   // up to 16 rows an expert on average the weights' bytes count, not the products
-  p.few = p.n <= 16 * E;
+  p.few = p.n <= 16 * E && H <= q4::kFewDepth && W <= q4::kFewDepth;
   p.direct = p.few && p.n <= q4::kFewDirect;
-  p.tile_rows = p.few ? 16 / parts : q4::gemm_tile_rows(p.n, E);
-  p.bound = q4::tile_bound(p.n, E, p.tile_rows);
+  // (a token is in an expert's list once, as a rule: more tiles hold the others;
+  // rows of more than 4096 share LDS by eight)
+  const int64_t most = (H > 4096 || W > 4096 ? 8 : 16) / parts, few_rows = T < most ? T : most;
+  p.tile_rows = p.few ? (int32_t)few_rows : q4::gemm_tile_rows(p.n, E);
+  p.bound = p.n ? q4::tile_bound(p.n, E, p.tile_rows) : 0;
   p.h = c.take<float>(p.n * W);
   p.y = c.take<float>(p.n * H);
   if (!p.direct) p.lists = take_lists(c, p.n, E, p.tile_rows);
@@ -348,7 +351,7 @@ q4_status q4_experts(const void* x, int64_t ldx, int32_t dtype, int64_t T, int64
     f.out_ld = width;
     f.pre = pre;
     f.width = width;
-    if (err == hipSuccess) err = q4::launch_few(f, true, s);
+    if (err == hipSuccess) err = q4::launch_few(f, pl.tile_rows, true, s);
     f.w = dn;
     f.x = pl.h;
     f.ldx = width;
@@ -357,7 +360,7 @@ q4_status q4_experts(const void* x, int64_t ldx, int32_t dtype, int64_t T, int64
     f.out = pl.y;
     f.out_ld = hidden;
     f.pre = nullptr;
-    if (err == hipSuccess) err = q4::launch_few(f, false, s);
+    if (err == hipSuccess) err = q4::launch_few(f, pl.tile_rows, false, s);
   } else {
     if (err == hipSuccess)
       err = q4::launch_split(x, ldx, dtype, hidden, nibble_order, nullptr, 0, pl.xs, s);

@@ -68,6 +68,13 @@ __device__ __forceinline__ bool id_ok(int32_t id, int32_t experts) {
   return (uint32_t)id < (uint32_t)experts;
 }
 
+// A barrier for what the waves exchange in LDS; loads stay under way.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // MFMA results read after a loop: the compiler's own waits count only from
 // within the block (a 16x16x32 product read right after a loop's last one came
 // back unfinished here), so the wait is spelled out.

@@ -1,0 +1,6 @@
+// Kernels of q4_experts_few.h.
+#include "q4_experts_few.h"
+
+namespace q4 {
+template hipError_t few_scales<1, _Float16, true>(const FewParams&, int32_t, hipStream_t);
+}  // namespace q4

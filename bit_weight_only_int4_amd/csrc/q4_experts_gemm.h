@@ -47,12 +47,6 @@ __device__ __forceinline__ void wait_loads() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
 
-__device__ __forceinline__ void lds_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
 // Maximum or sum over the 32 lanes of a half for 16 values: each step halves
 // the values a lane holds, so 16 exchanges do where 80 would.  Lane l ends with
 // value (l & 15) for lanes 0..15 of its half (and again for 16..31).
