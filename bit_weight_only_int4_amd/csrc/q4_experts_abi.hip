@@ -135,7 +135,7 @@ ExpertsPlan plan_experts(void* ws, int32_t dtype, int64_t T, int64_t H, int64_t 
 
 bool experts_grid_ok(const ExpertsPlan& p, int64_t H, int64_t W) {
   const int64_t most = H > 2 * W ? H : 2 * W;
-  const int64_t cols = p.few ? (most + 31) / 32 : (most + 127) / 128;
+  const int64_t cols = p.few ? (most + 255) / 256 * 8 : (most + 127) / 128;
   return (double)(p.direct ? p.n : p.bound) * (double)cols <= (double)(q4::kMaxGrid / 2);
 }
 

@@ -108,7 +108,7 @@ inline uint32_t divisor(uint32_t d) { return (uint32_t)((((uint64_t)1 << 31) + d
 __device__ __forceinline__ int quotient(int x, uint32_t div) { return (int)__umulhi((uint32_t)x * 2, div); }
 
 struct FewShape {
-  int32_t col_groups, tile_rows;
+  int32_t col_groups, xcd_groups, tile_rows;
   uint32_t group_div;  // steps of 32 k in a group
   uint32_t slot_div;   // slots of a row
   int32_t vec;
@@ -123,7 +123,8 @@ __device__ __forceinline__ void fetch_at_once(FewParams& p, FewShape& f) {
                  "+s"(p.nibble_order), "+s"(p.n), "+s"(p.experts), "+s"(p.out));
   asm volatile(""
                : "+s"(p.ids), "+s"(p.slots), "+s"(p.tiles), "+s"(p.n_tiles), "+s"(p.out_ld),
-                 "+s"(p.pre), "+s"(p.width), "+s"(f.col_groups), "+s"(f.tile_rows),
+                 "+s"(p.pre), "+s"(p.width), "+s"(f.col_groups), "+s"(f.xcd_groups),
+                 "+s"(f.tile_rows),
                  "+s"(f.group_div), "+s"(f.slot_div), "+s"(f.vec));
 }
 
@@ -144,8 +145,12 @@ few_kernel(const FewParams pa, const FewShape fa) {
   const int w = __builtin_amdgcn_readfirstlane((tid >> 6) % NW);
   const int cs = __builtin_amdgcn_readfirstlane((tid >> 6) / NW);
   const int n16 = lane & 15, q = lane >> 4;
-  const int cg0 = (int)(blockIdx.x % (uint32_t)f.col_groups) * CG;
-  const int tile = (int)(blockIdx.x / (uint32_t)f.col_groups);
+  // neighbouring columns share cache lines of scales: an XCD (workgroups go to
+  // the eight in turn) takes an eighth of the column groups of every tile
+  const int cg = (int)(blockIdx.x % 8u) * f.xcd_groups + (int)(blockIdx.x / 8u) % f.xcd_groups;
+  const int tile = (int)(blockIdx.x / 8u) / f.xcd_groups;
+  if (cg >= f.col_groups) return;
+  const int cg0 = cg * CG;
 
   // the tile's expert and slots (lane r has the r-th)
   int expert, rows, slot = 0;
@@ -393,11 +398,12 @@ hipError_t few_blocks(const FewParams& p, int32_t tile_rows, hipStream_t s) {
   const int cg = even && nw < 16 && cols * busy >= 4 * 4 * 256 ? 4 : 1;
   FewShape f;
   f.col_groups = (int32_t)((cols + cg - 1) / cg);
+  f.xcd_groups = (f.col_groups + 7) / 8;
   f.tile_rows = tile_rows;
   f.group_div = divisor(p.w.group ? p.w.group / 32 : 1);
   f.slot_div = divisor(p.slots_per_row);
   f.vec = reinterpret_cast<uintptr_t>(p.x) % 4 == 0 && p.ldx * sizeof(T) % 4 == 0;
-  const dim3 grid((uint32_t)(f.col_groups * tiles));
+  const dim3 grid((uint32_t)(8 * f.xcd_groups * tiles));
   const int stage = nw * tile_rows * P * kPitch * 2, join = nw * (16 / P) * (cg * 32 + 1) * 4;
   const int lds = stage > join ? stage : join;
 #define Q4_FEW(NW, CG, CS, EVEN)                                                                  \

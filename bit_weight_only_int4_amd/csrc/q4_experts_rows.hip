@@ -135,23 +135,37 @@ split_kernel(const T* __restrict__ x, int64_t ldx, int64_t K, int32_t order,
 
 // ---- sums over a token's slots -------------------------------------------------
 
+// Eight slots' loads are under way at once; a lane has a slot's id and weight.
 template <typename T>
 __global__ void __launch_bounds__(256) combine_kernel(const CombineParams p, bool vec) {
   const int64_t n = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
-  if (n >= p.N) return;  // N is a multiple of 8
+  const int lane = threadIdx.x & 63;
+  const bool in = n < p.N;  // N is a multiple of 8
   for (int64_t t = blockIdx.y; t < p.T; t += gridDim.y) {
-    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-    bool bad = false;
-    for (int j = 0; j < p.top_k; ++j) {
-      const int64_t slot = t * p.top_k + j;
-      const int32_t id = p.ids[slot];
-      bad |= id >= p.experts;
-      if (!id_ok(id, p.experts)) continue;
-      const float w = p.weights ? p.weights[slot] : 1.0f;
-      const f32x4 y = *(const f32x4*)(p.y + slot * p.N + n);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) sum[i] = __builtin_fmaf(w, y[i], sum[i]);
+    int32_t id = -1;
+    float w = 0.0f;
+    if (lane < p.top_k) {
+      id = p.ids[t * p.top_k + lane];
+      w = p.weights ? p.weights[t * p.top_k + lane] : 1.0f;
     }
+    const bool bad = __any(id >= p.experts);
+    const uint64_t used = __ballot(id_ok(id, p.experts));
+    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j0 = 0; j0 < p.top_k; j0 += 8) {
+      f32x4 y[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (in && (used >> (j0 + j) & 1)) y[j] = *(const f32x4*)(p.y + (t * p.top_k + j0 + j) * p.N + n);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (!(used >> (j0 + j) & 1)) continue;
+        const float wj = bits_f32((uint32_t)__builtin_amdgcn_readlane((int)f32_bits(w), j0 + j));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sum[i] = __builtin_fmaf(wj, y[j][i], sum[i]);
+      }
+    }
+    if (!in) continue;
     if (bad) sum = f32x4{} + bits_f32(0x7fc00000u);
     T* dst = (T*)p.out + t * p.ldo + n;
     typedef T t4 __attribute__((ext_vector_type(4)));
