@@ -16,7 +16,7 @@
 // wave unpacks it as the forward product does.  Within each 32 columns the order
 // is (k % 4 word, k in word) so that the writes spread over the banks.
 //
-// Tiles of BM rows by 128 columns, four waves of BM/2 x 64; the next step's
+// Tiles of BM rows by 128 columns, four waves of BM/2 x 64; the next steps'
 // loads are in registers while a step's products run.
 #pragma once
 
@@ -77,12 +77,12 @@ __global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
     first = t.first;
     rows = t.rows;
   } else {
-    // a split's rows of the matrix stay with one XCD
+    // rows of d, the larger operand, stay with one XCD
     const uint32_t plane = (uint32_t)row_tiles * (uint32_t)p.col_tiles;
     split = (int)(at / plane);
     at %= plane;
-    mt = (int)(at % (uint32_t)row_tiles);
-    ct = (int)(at / (uint32_t)row_tiles);
+    mt = (int)(at / (uint32_t)p.col_tiles);
+    ct = (int)(at % (uint32_t)p.col_tiles);
     first = mt * BM;
     rows = (int)(p.M - first < BM ? p.M - first : BM);
   }
@@ -134,8 +134,8 @@ __global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
   struct Fetch {
     float d[kPasses][8], s[NG][8];
     uint32_t w[4];
-  } f;
-  auto fetch = [&](int step) {
+  };
+  auto fetch = [&](Fetch& f, int step) {
     const int64_t n = nb + (int64_t)step * NS + chunk * 8;
     const bool full = n + 8 <= ne;
 #pragma unroll
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
     }
   };
   auto turn_of = [](int row) { return NS == 64 ? (row >> 1) & 7 : (row >> 2) & 3; };
-  auto store = [&](int step) {
+  auto store = [&](const Fetch& f, int step) {
     uint8_t* base = smem + (S == 2 ? (step & 1) * L::kStage : 0);
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
@@ -192,7 +192,8 @@ __global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
         h8 hi, lo;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const float x = settled(__builtin_ldexpf(f.d[i][operand_nibble(e)], de[i]) * s[e]);
+          float x = __builtin_ldexpf(f.d[i][operand_nibble(e)], de[i]) * s[e];
+          if constexpr (P == 2) x = settled(x);
           hi[e] = part_hi(x);
           if constexpr (P == 2) lo[e] = part_lo(x, hi[e]);
         }
@@ -253,29 +254,38 @@ __global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
     }
   };
 
-  if (steps > 0) {
-    fetch(0);
-    if constexpr (S == 2) {
-      store(0);
-      if (steps > 1) fetch(1);
+  if constexpr (S == 2) {
+    // loads two steps ahead of their use: a step's products are shorter than
+    // the way from memory
+    Fetch f0, f1;
+    if (steps > 0) fetch(f0, 0);
+    if (steps > 1) fetch(f1, 1);
+    if (steps > 0) store(f0, 0);
+    if (steps > 2) fetch(f0, 2);
+    lds_barrier();
+    for (int st = 0; st < steps; st += 2) {
+      products(st);
+      if (st + 1 < steps) store(f1, st + 1);
+      if (st + 3 < steps) fetch(f1, st + 3);
       lds_barrier();
-      for (int st = 0; st < steps; ++st) {
-        products(st);
-        if (st + 1 < steps) store(st + 1);
-        if (st + 2 < steps) fetch(st + 2);
+      if (st + 1 < steps) {
+        products(st + 1);
+        if (st + 2 < steps) store(f0, st + 2);
+        if (st + 4 < steps) fetch(f0, st + 4);
         lds_barrier();
-      }
-    } else {
-      for (int st = 0; st < steps; ++st) {
-        lds_barrier();
-        store(st);
-        lds_barrier();
-        if (st + 1 < steps) fetch(st + 1);
-        products(st);
       }
     }
   } else {
+    Fetch f;
+    if (steps > 0) fetch(f, 0);
     lds_barrier();
+    for (int st = 0; st < steps; ++st) {
+      lds_barrier();
+      store(f, st);
+      lds_barrier();
+      if (st + 1 < steps) fetch(f, st + 1);
+      products(st);
+    }
   }
   settle(acc);
 

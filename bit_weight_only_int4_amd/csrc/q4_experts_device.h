@@ -48,11 +48,10 @@ __device__ __forceinline__ uint32_t finite_bits(float x) {
 }
 
 // The two binary16 numbers of a scaled element: x = hi + lo to 22 bits (or hi
-// alone to 11).  Where hi is not finite, lo is 0.
+// alone to 11).  Of an infinity lo is NaN.
 __device__ __forceinline__ _Float16 part_hi(float x) { return (_Float16)x; }
 __device__ __forceinline__ _Float16 part_lo(float x, _Float16 hi) {
-  const float r = x - (float)hi;
-  return (_Float16)(r - r == 0.0f ? r : 0.0f);
+  return (_Float16)__builtin_fmaf(-(float)hi, 1.0f, x);
 }
 
 // A product about to be split, rounded to fp32 here: the compiler may otherwise
