@@ -35,8 +35,9 @@ struct GemmTile {
   static constexpr int kB = kBN * kBK / 2;
   static constexpr int kScale = GM == kOneGroup ? 0 : kGroupsPerStep * kBN * 4;
   static constexpr int kStage = kA + kB + kScale;
-  // two workgroups a CU where three stages allow it
-  static constexpr int kStages = 3 * kStage <= 76 * 1024 ? 3 : 2;
+  // one group: three workgroups a CU of two stages; else two, of three stages
+  // where LDS allows it
+  static constexpr int kStages = GM != kOneGroup && 3 * kStage <= 76 * 1024 ? 3 : 2;
   // vector memory operations a wave issues per step
   static constexpr int kIssue = P * BM / 32 + 1 + (GM == kOneGroup ? 0 : 1);
 };
@@ -87,7 +88,7 @@ typedef Flag<true> Yes;
 typedef Flag<false> No;
 
 template <int P, int BM, int GM, Epilogue EPI>
-__global__ void __launch_bounds__(256, 2) gemm_kernel(const GemmParams p) {
+__global__ void __launch_bounds__(256, GM == kOneGroup && P == 1 ? 3 : 2) gemm_kernel(const GemmParams p) {
   typedef GemmTile<P, BM, GM> L;
   constexpr int RB = BM / 64;  // row blocks of a wave
   constexpr int S = L::kStages;
@@ -286,7 +287,8 @@ __global__ void __launch_bounds__(256, 2) gemm_kernel(const GemmParams p) {
       if constexpr (GM == kGroups32) fold(base, h);
     }
   };
-
+  // a wave without rows (of a tile that is not full) loads for the others
+  const bool idle = wr * (BM / 2) >= rows;
   issue(0);
   if constexpr (S == 3) issue(1);
   auto begin = [&](int step) -> const uint8_t* {
@@ -298,17 +300,20 @@ __global__ void __launch_bounds__(256, 2) gemm_kernel(const GemmParams p) {
   if constexpr (GM == kGroups64) {
     for (int st = 0; st < steps;) {
       const uint8_t* base = begin(st++);
-      products(base, Yes{});
+      if (!idle) products(base, Yes{});
       const int end = st + per_group - 1 < steps ? st + per_group - 1 : steps;
       for (; st < end;) {
         base = begin(st++);
-        products(base, No{});
+        if (!idle) products(base, No{});
       }
       settle(acc);
       fold(base, 0);
     }
   } else {
-    for (int st = 0; st < steps; ++st) products(begin(st), No{});
+    for (int st = 0; st < steps; ++st) {
+      const uint8_t* base = begin(st);
+      if (!idle) products(base, No{});
+    }
     settle(acc);
   }
 
