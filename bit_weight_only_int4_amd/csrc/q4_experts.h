@@ -110,7 +110,9 @@ struct GemmParams {
   const int64_t* targets;
   const float* lse;       // kHeadGrad
   const float* g;         // kHeadGrad
-  float* d;               // kHeadGrad: [M][out_ld]
+  float* d;               // kHeadGrad: [M][out_ld], or with a scale per row
+  _Float16* d_parts;      // [parts][rows of a][out_ld]: times it, scaled as BackParams says
+  const uint32_t* s_bits;
 };
 // rows of a tile the launcher takes for `n` rows over `experts` matrices
 int32_t gemm_tile_rows(int64_t n, int64_t experts);
@@ -159,6 +161,11 @@ struct BackParams {
   int32_t nibble_order, parts;
   const void* d;           // rows of d_dtype
   int64_t ldd;
+  // or, with a scale per row of the matrix: d times it, against the row's and
+  // the scales' largest (times 2^15), as binary16 parts [parts][d_rows][ldd] in
+  // the operands' order, zeros from n_rows to the next multiple of 64
+  const _Float16* d_parts;
+  int64_t d_rows;
   int32_t d_dtype;
   const uint32_t* d_bits;  // [row of d]: bits of a magnitude that none of the row's passes
   const uint32_t* s_bits;  // [experts]: of the largest scale

@@ -605,14 +605,22 @@ q4_status q4_head_cross_entropy_backward(const void* x, int64_t ldx, int32_t dty
       g.targets = targets + m0;
       g.lse = lse + m0;
       g.g = g_loss + m0;
-      g.d = pl.d;
+      if (w.group)
+        g.d = pl.d;
+      else
+        g.d_parts = (_Float16*)pl.d;  // (two of them take the place of a float)
+      g.s_bits = pl.s_bits;
       g.out_ld = pl.piece;
       err = q4::launch_gemm(g, pl.tile_rows, q4::kHeadGrad, s);
       q4::BackParams b{};
       b.w = w;
       b.nibble_order = nibble_order;
       b.parts = pl.parts;
-      b.d = pl.d;
+      if (w.group)
+        b.d = pl.d;
+      else
+        b.d_parts = g.d_parts;
+      b.d_rows = xs.rows;
       b.ldd = pl.piece;
       b.d_dtype = Q4_DTYPE_F32;
       b.d_bits = pl.g_bits;

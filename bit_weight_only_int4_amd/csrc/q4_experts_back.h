@@ -254,6 +254,7 @@ __global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
     }
   };
 
+  const bool idle = wr * (BM / 2) >= rows;  // a wave without rows
   if constexpr (S == 2) {
     // loads two steps ahead of their use: a step's products are shorter than
     // the way from memory
@@ -264,12 +265,12 @@ __global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
     if (steps > 2) fetch(f0, 2);
     lds_barrier();
     for (int st = 0; st < steps; st += 2) {
-      products(st);
+      if (!idle) products(st);
       if (st + 1 < steps) store(f1, st + 1);
       if (st + 3 < steps) fetch(f1, st + 3);
       lds_barrier();
       if (st + 1 < steps) {
-        products(st + 1);
+        if (!idle) products(st + 1);
         if (st + 2 < steps) store(f0, st + 2);
         if (st + 4 < steps) fetch(f0, st + 4);
         lds_barrier();
@@ -284,7 +285,7 @@ __global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
       store(f, st);
       lds_barrier();
       if (st + 1 < steps) fetch(f, st + 1);
-      products(st);
+      if (!idle) products(st);
     }
   }
   settle(acc);
@@ -343,6 +344,181 @@ __global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
       }
     }
   }
+}
+
+// The same with the row operand complete in memory (d_parts): it comes by direct
+// loads, as the forward product's, and only the codes are turned around.
+template <int P, int BM>
+struct DirectTile {
+  static constexpr int kA = P * BM * kBK * 2;
+  static constexpr int kB = 128 * kBK / 2;
+  static constexpr int kLds = 2 * (kA + kB);
+};
+
+template <int P, int BM>
+__global__ void __launch_bounds__(256, 2) back_direct_kernel(const BackParams p) {
+  typedef DirectTile<P, BM> L;
+  constexpr int RB = BM / 64;
+  extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
+  __shared__ int32_t sh_exp[BM];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wr = w >> 1, wc = w & 1, c = lane & 31, q = lane >> 5;
+
+  // rows of d stay with one XCD
+  const uint32_t total = (uint32_t)p.row_tiles * (uint32_t)p.col_tiles * (uint32_t)p.splits;
+  uint32_t at = xcd_swizzle(blockIdx.x, total);
+  const uint32_t plane = (uint32_t)p.row_tiles * (uint32_t)p.col_tiles;
+  const int split = (int)(at / plane);
+  at %= plane;
+  const int mt = (int)(at / (uint32_t)p.col_tiles), ct = (int)(at % (uint32_t)p.col_tiles);
+  const int first = mt * BM, rows = (int)(p.M - first < BM ? p.M - first : BM);
+  const int64_t K = p.w.K, ldq = K >> 1, k0 = (int64_t)ct * 128;
+  const int s_exp = top_exponent(*p.s_bits);
+  const int64_t per = ((p.n_rows + p.splits - 1) / p.splits + kBK - 1) / kBK * kBK;
+  const int64_t nb = per * split < p.n_rows ? per * split : p.n_rows;
+  const int64_t ne = nb + per < p.n_rows ? nb + per : p.n_rows;
+  const int steps = (int)((ne - nb + kBK - 1) / kBK);
+  if (tid < BM) sh_exp[tid] = top_exponent(p.d_bits[first + (tid < rows ? tid : rows - 1)]);
+
+  const _Float16* asrc[BM / 32];
+#pragma unroll
+  for (int i = 0; i < BM / 32; ++i) {
+    const int r = w * (BM / 4) + i * 8 + (lane >> 3);
+    asrc[i] = p.d_parts + (int64_t)(first + (r < rows ? r : rows - 1)) * p.ldd + nb +
+              ((lane & 7) ^ ((r >> 1) & 7)) * 8;
+  }
+  const int64_t piece = p.d_rows * p.ldd;
+  const int kw = tid & 15, u = tid >> 4;
+  const int64_t kword = k0 + kw * 8 < K ? k0 / 8 + kw : 0;
+  const uint8_t* codes = p.w.qw + p.n0 * ldq + kword * 4;
+
+  auto issue = [&](int step) {
+    const int st = step < steps ? step : steps - 1;
+    uint8_t* base = smem + (step & 1) * L::kA;
+#pragma unroll
+    for (int pc = 0; pc < P; ++pc)
+#pragma unroll
+      for (int i = 0; i < BM / 32; ++i)
+        __builtin_amdgcn_global_load_lds(
+            (global_cptr)(asrc[i] + pc * piece + (int64_t)st * kBK),
+            (lds_vptr)(base + pc * BM * 128 + (w * (BM / 4) + i * 8) * 128), 16, 0, 0);
+  };
+  struct Words {
+    uint32_t w[4];
+  };
+  auto fetch = [&](Words& f, int step) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t r = nb + (int64_t)step * kBK + 4 * u + i;
+      // (rows past the end: any codes, the other operand is 0)
+      f.w[i] = *(const uint32_t*)(codes + (r < ne ? r : ne - 1) * ldq);
+    }
+  };
+  const int flip = p.nibble_order == Q4_ORDER_LOW_FIRST ? 0 : 1;
+  auto store = [&](const Words& f, int step) {
+    uint32_t t[4];
+    turn_words(f.w, t);
+    uint8_t* dst = smem + 2 * L::kA + (step & 1) * L::kB + ((kw >> 2) * 32 + (kw & 3)) * 32 + (u >> 1) * 4 + (u & 1) * 2;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      *(uint16_t*)(dst + (i ^ flip) * 4 * 32) = (uint16_t)t[i];
+      *(uint16_t*)(dst + ((i + 4) ^ flip) * 4 * 32) = (uint16_t)(t[i] >> 16);
+    }
+  };
+
+  f32x16 acc[RB][2];
+#pragma unroll
+  for (int r = 0; r < RB; ++r)
+#pragma unroll
+    for (int b = 0; b < 2; ++b) acc[r][b] = f32x16{};
+  const Magic magic = Magic::make();
+  auto products = [&](int step) {
+    const uint8_t *a_base = smem + (step & 1) * L::kA, *b_base = smem + 2 * L::kA + (step & 1) * L::kB;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      uint32_t words[2][2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const u32x2 x = *(const u32x2*)(b_base + (wc * 64 + b * 32 + c) * 32 + h * 16 + q * 8);
+        words[b][0] = x[0];
+        words[b][1] = x[1];
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const h8 bo[2] = {codes_of(words[0][j], magic), codes_of(words[1][j], magic)};
+#pragma unroll
+        for (int r = 0; r < RB; ++r) {
+          const int row = wr * (BM / 2) + r * 32 + c;
+          const int chunk = (h * 4 + q * 2 + j) ^ ((row >> 1) & 7);
+#pragma unroll
+          for (int pc = 0; pc < P; ++pc) {
+            const h8 a = *(const h8*)(a_base + pc * BM * 128 + row * 128 + chunk * 16);
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+              acc[r][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, bo[b], acc[r][b], 0, 0, 0);
+          }
+        }
+      }
+    }
+  };
+
+  // Step st: its rows were asked for a step ago, its codes two; then the next
+  // step's rows, the codes after them, and the next step's codes into LDS.
+  const bool idle = wr * (BM / 2) >= rows;
+  Words f0, f1;
+  if (steps > 0) {
+    fetch(f0, 0);
+    issue(0);
+    fetch(f1, 1);
+    store(f0, 0);
+    auto step = [&](int st, Words& next, Words& after) {
+      wait_loads<4>();  // (the four after them are the next step's codes)
+      lds_barrier();
+      issue(st + 1);
+      fetch(after, st + 2);
+      if (!idle) products(st);
+      store(next, st + 1);
+    };
+    for (int st = 0; st < steps; st += 2) {
+      step(st, f1, f0);
+      if (st + 1 < steps) step(st + 1, f0, f1);
+    }
+  }
+  lds_barrier();
+  wait_loads<0>();
+  settle(acc);
+
+  float* out = p.out + (int64_t)split * p.M * p.out_ld;
+#pragma unroll
+  for (int r = 0; r < RB; ++r) {
+    const int r0 = wr * (BM / 2) + r * 32 + 4 * q;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int64_t k = k0 + wc * 64 + b * 32 + (c & 3) * 8 + (c >> 2);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int row = r0 + 8 * (i >> 2) + (i & 3);
+        if (row >= rows || k >= K) continue;
+        const float z = __builtin_ldexpf(acc[r][b][i], sh_exp[row] + s_exp - 15);
+        float* dst = out + (int64_t)(first + row) * p.out_ld + k;
+        *dst = p.accumulate ? *dst + z : z;
+      }
+    }
+  }
+}
+
+template <int P, int BM>
+hipError_t launch_back_direct(const BackParams& p, hipStream_t s) {
+  constexpr int lds = DirectTile<P, BM>::kLds;
+  if (lds > 64 * 1024) {
+    const hipError_t e = hipFuncSetAttribute((const void*)back_direct_kernel<P, BM>,
+                                             hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (e != hipSuccess) return e;
+  }
+  const dim3 grid((uint32_t)((int64_t)p.row_tiles * p.col_tiles * p.splits));
+  hipLaunchKernelGGL((back_direct_kernel<P, BM>), grid, dim3(256), lds, s, p);
+  return hipGetLastError();
 }
 
 template <int P, typename T, int BM, bool GATE>

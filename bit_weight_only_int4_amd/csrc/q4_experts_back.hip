@@ -13,6 +13,10 @@ Q4_TILES(2, float, true)
 Q4_TILES(1, float, false)
 Q4_TILES(2, float, false)
 #undef Q4_TILES
+extern template hipError_t launch_back_direct<1, 64>(const BackParams&, hipStream_t);
+extern template hipError_t launch_back_direct<1, 128>(const BackParams&, hipStream_t);
+extern template hipError_t launch_back_direct<2, 64>(const BackParams&, hipStream_t);
+extern template hipError_t launch_back_direct<2, 128>(const BackParams&, hipStream_t);
 
 namespace {
 template <int P, typename T, bool GATE>
@@ -23,6 +27,10 @@ hipError_t by_tile(const BackParams& p, int32_t tile_rows, hipStream_t s) {
 
 hipError_t launch_back(const BackParams& in, int32_t tile_rows, bool gate, hipStream_t s) {
   BackParams p = in;
+  if (p.d_parts) {
+    if (tile_rows == 128) return p.parts == 2 ? launch_back_direct<2, 128>(p, s) : launch_back_direct<1, 128>(p, s);
+    return p.parts == 2 ? launch_back_direct<2, 64>(p, s) : launch_back_direct<1, 64>(p, s);
+  }
   const int64_t e = p.d_dtype == Q4_DTYPE_F32 ? 4 : 2;
   p.d_vec = reinterpret_cast<uintptr_t>(p.d) % 16 == 0 && p.ldd * e % 16 == 0;
   if (!gate)

@@ -23,6 +23,11 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 // Nibble at position i of an operand.
 __device__ __forceinline__ constexpr int operand_nibble(int i) { return (i >> 1) + 4 * (i & 1); }
 
+// and the position of a nibble
+__device__ __forceinline__ constexpr int operand_place(int nibble) {
+  return nibble < 4 ? 2 * nibble : 2 * nibble - 7;
+}
+
 __device__ __forceinline__ h8 codes_of(uint32_t w, const Magic& mg) {
   h2 c[4];
   unpack_word(w, mg, c);

@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(256, GM == kOneGroup && P == 1 ? 3 : 2) gemm_k
           st[1] = sum;
         }
       }
-    } else {
+    } else if constexpr (GM != kOneGroup) {
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         const int col = wc * 64 + b * 32 + c;
@@ -410,6 +410,28 @@ __global__ void __launch_bounds__(256, GM == kOneGroup && P == 1 ? 3 : 2) gemm_k
           const float g = sh_g[row];
           const float pr = exp_full(z[b][i] - sh_lse[row]) - (sh_target[row] == col ? 1.0f : 0.0f);
           p.d[(int64_t)slot * p.out_ld + (int64_t)ct * kBN + col] = g != 0.0f ? g * pr : 0.0f;
+        }
+      }
+    } else {
+      // a scale per column: the gradient's operand is complete here, zeros up
+      // to the tile's end
+      const int s_exp = top_exponent(*p.s_bits);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int col = wc * 64 + b * 32 + c;
+        const float s = (int64_t)ct * kBN + col < p.n_cols ? __builtin_ldexpf(scale0[b], 15 - s_exp) : 0.0f;
+        _Float16* to = p.d_parts + (int64_t)ct * kBN + (col & ~7) + operand_place(col & 7);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int row = r0 + 8 * (i >> 2) + (i & 3), slot = sh_slot[row];
+          if (slot < 0) continue;
+          const float g = sh_g[row];
+          const float pr = exp_full(z[b][i] - sh_lse[row]) - (sh_target[row] == col ? 1.0f : 0.0f);
+          const float x = s != 0.0f && g != 0.0f ? settled(__builtin_ldexpf(g, -top_exponent(finite_bits(g))) * pr * s) : 0.0f;
+          _Float16* dst = to + (int64_t)slot * p.out_ld;
+          const _Float16 hi = part_hi(x);
+          *dst = hi;
+          if constexpr (P == 2) dst[p.a.rows * p.out_ld] = part_lo(x, hi);
         }
       }
     }
