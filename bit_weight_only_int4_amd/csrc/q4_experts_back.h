@@ -127,54 +127,69 @@ __global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
   // and of the codes: a word of four rows
   const int kw = tid & 15, u = tid >> 4;
   const bool codes_mine = u < NS / 4;
-  const int64_t kword = k0 + kw * 8 < K ? k0 / 8 + kw : 0;
-  const uint8_t* codes = p.w.qw + expert * p.w.expert_bytes + p.n0 * ldq + kword * 4;
+  // (addresses are a step's base, the same for all lanes, and a lane's 32-bit offset)
+  const uint32_t code_at = (uint32_t)(k0 + kw * 8 < K ? k0 / 8 + kw : 0) * 4u + (uint32_t)(4 * u) * (uint32_t)ldq;
+  const uint8_t* codes = p.w.qw + expert * p.w.expert_bytes + (p.n0 + nb) * ldq;
+  const uint32_t scale_at = (uint32_t)chunk * 8u;
 
   const bool d_vec = p.d_vec != 0;
   struct Fetch {
     float d[kPasses][8], s[NG][8];
     uint32_t w[4];
   };
-  auto fetch = [&](Fetch& f, int step) {
-    const int64_t n = nb + (int64_t)step * NS + chunk * 8;
-    const bool full = n + 8 <= ne;
+  // (past the last step it loads that one again: the waits count on as many
+  // loads whatever the way through the loop)
+  auto fetch = [&](Fetch& f, int at_step) {
+    const int step = at_step < steps ? at_step : steps - 1;
+    const int64_t n0 = nb + (int64_t)step * NS, n = n0 + chunk * 8;
+    const uint8_t* code = codes + (int64_t)step * NS * ldq;
+    if (n0 + NS <= ne) {
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      if (full && d_vec) {
-        constexpr int v = 16 / sizeof(T);
-        typedef T tv __attribute__((ext_vector_type(v)));
+      for (int i = 0; i < kPasses; ++i) {
+        if (d_vec) {
+          constexpr int v = 16 / sizeof(T);
+          typedef T tv __attribute__((ext_vector_type(v)));
 #pragma unroll
-        for (int j = 0; j < 8 / v; ++j) {
-          const tv x = *(const tv*)(dsrc[i] + n + j * v);
+          for (int j = 0; j < 8 / v; ++j) {
+            const tv x = *(const tv*)(dsrc[i] + n + j * v);
 #pragma unroll
-          for (int e = 0; e < v; ++e) f.d[i][j * v + e] = to_f32(x[e]);
+            for (int e = 0; e < v; ++e) f.d[i][j * v + e] = to_f32(x[e]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f.d[i][e] = to_f32(dsrc[i][n + e]);
         }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f.d[i][e] = n + e < ne ? to_f32(dsrc[i][n + e]) : 0.0f;
       }
-    }
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-      const float* s = scales + group_at[g] + n;
-      if (full) {
+      for (int g = 0; g < NG; ++g) {
+        const float* s = scales + (group_at[g] + n0);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const f32x4_a4 x = *(const f32x4_a4*)(s + 4 * j);
+          const f32x4_a4 x = *(const f32x4_a4*)(s + (scale_at + 4 * j));
 #pragma unroll
           for (int e = 0; e < 4; ++e) f.s[g][j * 4 + e] = x[e];
         }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f.s[g][e] = n + e < ne ? s[e] : 0.0f;
       }
-    }
-    if (codes_mine) {
+      if (codes_mine) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t r = nb + (int64_t)step * NS + 4 * u + i;
-        // (rows past the end: any codes, the other operand is 0)
-        f.w[i] = *(const uint32_t*)(codes + (r < ne ? r : ne - 1) * ldq);
+        for (int i = 0; i < 4; ++i) f.w[i] = *(const uint32_t*)(code + i * ldq + code_at);
+      }
+    } else {
+      // the last step: zeros past the end (and any codes)
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f.d[i][e] = n + e < ne ? to_f32(dsrc[i][n + e]) : 0.0f;
+#pragma unroll
+      for (int g = 0; g < NG; ++g)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f.s[g][e] = n + e < ne ? scales[group_at[g] + n + e] : 0.0f;
+      if (codes_mine) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int64_t r = n0 + 4 * u + i;
+          f.w[i] = *(const uint32_t*)(codes + ((r < ne ? r : ne - 1) - nb) * ldq + (code_at - (uint32_t)(4 * u) * (uint32_t)ldq));
+        }
       }
     }
   };
@@ -259,22 +274,24 @@ __global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
     // loads two steps ahead of their use: a step's products are shorter than
     // the way from memory
     Fetch f0, f1;
-    if (steps > 0) fetch(f0, 0);
-    if (steps > 1) fetch(f1, 1);
-    if (steps > 0) store(f0, 0);
-    if (steps > 2) fetch(f0, 2);
-    lds_barrier();
-    for (int st = 0; st < steps; st += 2) {
-      if (!idle) products(st);
-      if (st + 1 < steps) store(f1, st + 1);
-      if (st + 3 < steps) fetch(f1, st + 3);
+    if (steps > 0) {
+      fetch(f0, 0);
+      fetch(f1, 1);
+      store(f0, 0);
+      fetch(f0, 2);
       lds_barrier();
-      if (st + 1 < steps) {
-        if (!idle) products(st + 1);
-        if (st + 2 < steps) store(f0, st + 2);
-        if (st + 4 < steps) fetch(f0, st + 4);
+      for (int st = 0; st < steps; st += 2) {
+        if (!idle) products(st);
+        store(f1, st + 1);
+        fetch(f1, st + 3);
+        lds_barrier();
+        if (st + 1 < steps && !idle) products(st + 1);
+        store(f0, st + 2);
+        fetch(f0, st + 4);
         lds_barrier();
       }
+    } else {
+      lds_barrier();
     }
   } else {
     Fetch f;
@@ -284,7 +301,7 @@ __global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
       lds_barrier();
       store(f, st);
       lds_barrier();
-      if (st + 1 < steps) fetch(f, st + 1);
+      fetch(f, st + 1);
       if (!idle) products(st);
     }
   }
@@ -390,8 +407,9 @@ __global__ void __launch_bounds__(256, 2) back_direct_kernel(const BackParams p)
   }
   const int64_t piece = p.d_rows * p.ldd;
   const int kw = tid & 15, u = tid >> 4;
-  const int64_t kword = k0 + kw * 8 < K ? k0 / 8 + kw : 0;
-  const uint8_t* codes = p.w.qw + p.n0 * ldq + kword * 4;
+  const uint32_t word_at = (uint32_t)(k0 + kw * 8 < K ? k0 / 8 + kw : 0) * 4u;
+  const uint32_t code_at = word_at + (uint32_t)(4 * u) * (uint32_t)ldq;
+  const uint8_t* codes = p.w.qw + (p.n0 + nb) * ldq;
 
   auto issue = [&](int step) {
     const int st = step < steps ? step : steps - 1;
@@ -408,11 +426,17 @@ __global__ void __launch_bounds__(256, 2) back_direct_kernel(const BackParams p)
     uint32_t w[4];
   };
   auto fetch = [&](Words& f, int step) {
+    const int64_t n0 = (int64_t)step * kBK;
+    if (nb + n0 + kBK <= ne) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t r = nb + (int64_t)step * kBK + 4 * u + i;
+      for (int i = 0; i < 4; ++i) f.w[i] = *(const uint32_t*)(codes + (n0 + i) * ldq + code_at);
+    } else {
       // (rows past the end: any codes, the other operand is 0)
-      f.w[i] = *(const uint32_t*)(codes + (r < ne ? r : ne - 1) * ldq);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int64_t r = n0 + 4 * u + i;
+        f.w[i] = *(const uint32_t*)(codes + (nb + r < ne ? r : ne - 1 - nb) * ldq + word_at);
+      }
     }
   };
   const int flip = p.nibble_order == Q4_ORDER_LOW_FIRST ? 0 : 1;
