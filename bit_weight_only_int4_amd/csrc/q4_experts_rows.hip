@@ -47,6 +47,20 @@ __device__ __forceinline__ void load8(const T* row, int64_t k, int64_t K, bool v
 // is that of arrival and changes nothing: a row's result does not depend on its
 // place in a tile.
 constexpr int kListThreads = 1024;
+// The ids of this thread, four loads under way at once.
+template <typename F>
+__device__ __forceinline__ void each_id(const int32_t* __restrict__ ids, int32_t n, F f) {
+  for (int64_t i0 = threadIdx.x; i0 < n; i0 += 4 * kListThreads) {
+    int32_t id[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t i = i0 + j * kListThreads;
+      id[j] = i < n ? ids[i] : -1;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f(id[j], i0 + j * kListThreads);
+  }
+}
 __global__ void __launch_bounds__(kListThreads)
 lists_kernel(const int32_t* __restrict__ ids, int32_t n, int32_t experts, int32_t tile_rows,
              const RowLists r) {
@@ -55,10 +69,9 @@ lists_kernel(const int32_t* __restrict__ ids, int32_t n, int32_t experts, int32_
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
   count[tid] = 0;
   __syncthreads();
-  for (int64_t i = tid; i < n; i += kListThreads) {
-    const int32_t id = ids[i];
+  each_id(ids, n, [&](int32_t id, int64_t) {
     if (id_ok(id, experts)) atomicAdd(&count[id], 1);
-  }
+  });
   __syncthreads();
   // thread e: expert e
   const int32_t c = count[tid], mine = (c + tile_rows - 1) / tile_rows;
@@ -84,52 +97,76 @@ lists_kernel(const int32_t* __restrict__ ids, int32_t n, int32_t experts, int32_
   }
   if (tid == 0) *r.n_tiles = all;
   __syncthreads();
-  for (int64_t i = tid; i < n; i += kListThreads) {
-    const int32_t id = ids[i];
+  each_id(ids, n, [&](int32_t id, int64_t i) {
     if (id_ok(id, experts)) r.slots[atomicAdd(&next[id], 1)] = (int32_t)i;
-  }
+  });
 }
 
 // ---- activations into binary16 parts -----------------------------------------
 
-// A workgroup a row: its largest magnitude, then every word of 8 elements in
-// the order of the codes' operands.
+// A wave a row: its largest magnitude, then every word of 8 elements in the
+// order of the codes' operands.  HOLD: rows of up to 512 HOLD elements stay in
+// registers in between, longer ones (0) are read again.
+typedef float f32x8 __attribute__((ext_vector_type(8)));
 template <typename T>
-__global__ void __launch_bounds__(256)
-split_kernel(const T* __restrict__ x, int64_t ldx, int64_t K, int32_t order,
-             const int32_t* __restrict__ ids, int32_t experts, const SplitRows r, bool vec) {
-  __shared__ uint32_t sh[4];
-  const int tid = threadIdx.x;
-  const int64_t row = blockIdx.x;
-  if (ids && !id_ok(ids[row], experts)) return;
-  const T* src = x + row * ldx;
-  uint32_t m = 0;
-  for (int64_t k = 8 * tid; k < K; k += 8 * 256) {
+__device__ __forceinline__ f32x8 row_word(const T* __restrict__ src, int64_t k, int64_t K, bool vec) {
+  f32x8 r = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (k < K) {
     float v[8];
     load8(src, k, K, vec, v);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = umax(m, finite_bits(v[i]));
+    for (int j = 0; j < 8; ++j) r[j] = v[j];
   }
-  const int e = row_exponent(block_umax(m, sh));
-  if (tid == 0) r.e[row] = e;
-  for (int64_t k = 8 * tid; k < r.Kp; k += 8 * 256) {
-    float v[8];
-    if (k < K) {
-      load8(src, k, K, vec, v);
-    } else {
+  return r;
+}
+__device__ __forceinline__ void store_parts(const SplitRows& r, int64_t row, int64_t k, int e,
+                                            int32_t order, f32x8 y) {
+  h8 hi, lo;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-    }
-    h8 hi, lo;
+  for (int i = 0; i < 8; ++i) {
+    const int nib = operand_nibble(i);
+    const float s = settled(__builtin_ldexpf(order == Q4_ORDER_LOW_FIRST ? y[nib] : y[nib ^ 1], e));
+    hi[i] = part_hi(s);
+    lo[i] = part_lo(s, hi[i]);
+  }
+  *(h8*)(r.a + row * r.Kp + k) = hi;
+  if (r.parts == 2) *(h8*)(r.a + (r.rows + row) * r.Kp + k) = lo;
+}
+template <typename T, int HOLD>
+__global__ void __launch_bounds__(256)
+split_kernel(const T* __restrict__ x, int64_t ldx, int64_t K, int32_t order,
+             const int32_t* __restrict__ ids, int32_t experts, const SplitRows r, bool vec) {
+  const int lane = threadIdx.x & 63;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (row >= r.rows) return;  // whole waves; no barrier follows
+  if (ids && !id_ok(ids[row], experts)) return;
+  const T* src = x + row * ldx;
+  uint32_t m = 0;
+  if constexpr (HOLD > 0) {
+    f32x8 v[HOLD];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int nib = operand_nibble(i);
-      const float s = settled(__builtin_ldexpf(order == Q4_ORDER_LOW_FIRST ? v[nib] : v[nib ^ 1], e));
-      hi[i] = part_hi(s);
-      lo[i] = part_lo(s, hi[i]);
+    for (int i = 0; i < HOLD; ++i) v[i] = row_word(src, 8 * (lane + 64 * i), K, vec);
+#pragma unroll
+    for (int i = 0; i < HOLD; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = umax(m, finite_bits(v[i][j]));
+    const int e = row_exponent(wave_umax(m));
+    if (lane == 0) r.e[row] = e;
+#pragma unroll
+    for (int i = 0; i < HOLD; ++i) {
+      const int64_t k = 8 * (lane + 64 * i);
+      if (k < r.Kp) store_parts(r, row, k, e, order, v[i]);
     }
-    *(h8*)(r.a + row * r.Kp + k) = hi;
-    if (r.parts == 2) *(h8*)(r.a + (r.rows + row) * r.Kp + k) = lo;
+  } else {
+    for (int64_t k = 8 * lane; k < K; k += 512) {
+      const f32x8 v = row_word(src, k, K, vec);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = umax(m, finite_bits(v[j]));
+    }
+    const int e = row_exponent(wave_umax(m));
+    if (lane == 0) r.e[row] = e;
+    for (int64_t k = 8 * lane; k < r.Kp; k += 512)
+      store_parts(r, row, k, e, order, row_word(src, k, K, vec));
   }
 }
 
@@ -183,37 +220,49 @@ __global__ void __launch_bounds__(256) combine_kernel(const CombineParams p, boo
 
 // ---- largest magnitudes ----------------------------------------------------------
 
+// (a wave a row; the waves after the last row clear)
 template <typename T>
 __global__ void __launch_bounds__(256)
 row_bits_kernel(const T* __restrict__ x, int64_t ldx, int64_t rows, int64_t K, uint32_t* bits,
                 uint32_t* zero, int64_t zeros, bool vec) {
-  __shared__ uint32_t sh[4];
-  const int64_t row = blockIdx.x;
+  const int lane = threadIdx.x & 63;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
   if (row >= rows) {
-    const int64_t i = (row - rows) * 256 + threadIdx.x;
+    const int64_t i = (row - rows) * 64 + lane;
     if (i < zeros) zero[i] = 0;
     return;
   }
   uint32_t m = 0;
-  for (int64_t k = 8 * (int64_t)threadIdx.x; k < K; k += 8 * 256) {
+  for (int64_t k = 8 * lane; k < K; k += 512) {
     float v[8];
     load8(x + row * ldx, k, K, vec, v);
 #pragma unroll
     for (int i = 0; i < 8; ++i) m = umax(m, finite_bits(v[i]));
   }
-  m = block_umax(m, sh);
-  if (threadIdx.x == 0) bits[row] = m;
+  m = wave_umax(m);
+  if (lane == 0) bits[row] = m;
 }
 
-constexpr int kScaleRun = 8192;  // scales of a workgroup
+constexpr int kScaleRun = 4096;  // scales of a workgroup
 __global__ void __launch_bounds__(256)
 scale_bits_kernel(const float* __restrict__ s, int64_t n, uint32_t* bits) {
   __shared__ uint32_t sh[4];
   const float* src = s + (int64_t)blockIdx.y * n;
-  const int64_t at = (int64_t)blockIdx.x * kScaleRun;
-  const int64_t end = at + kScaleRun < n ? at + kScaleRun : n;
+  const int64_t at = (int64_t)blockIdx.x * kScaleRun + 4 * threadIdx.x;
   uint32_t m = 0;
-  for (int64_t i = at + threadIdx.x; i < end; i += 256) m = umax(m, finite_bits(src[i]));
+#pragma unroll
+  for (int i = 0; i < kScaleRun / 1024; ++i) {
+    const int64_t k = at + 1024 * i;
+    if (k + 4 <= n) {
+      const f32x4_a4 x = *(const f32x4_a4*)(src + k);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) m = umax(m, finite_bits(x[j]));
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (k + j < n) m = umax(m, finite_bits(src[k + j]));
+    }
+  }
   m = block_umax(m, sh);
   if (threadIdx.x == 0) atomicMax(bits + blockIdx.y, m);
 }
@@ -233,36 +282,50 @@ gate_sums_kernel(const float* __restrict__ part, int32_t parts, const int32_t* _
 
 // ---- the head's last steps -------------------------------------------------------
 
-// A wave a row: parts (maximum, sum of e^(z - maximum)) of the vocabulary's
-// tiles joined, and the loss.
+// A workgroup a row: parts (maximum, sum of e^(z - maximum)) of the vocabulary's
+// tiles joined, and the loss.  A part that is NaN or +inf makes the row NaN.
 __global__ void __launch_bounds__(256) head_finish_kernel(const HeadFinish p) {
-  const int lane = threadIdx.x & 63;
-  const int64_t m = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (m >= p.M) return;
-  const float* st = p.stats + m * p.parts * 2;
+  __shared__ float sh[4];
+  __shared__ uint32_t sh_nan[4];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int64_t m = blockIdx.x;
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  const f32x2* st = (const f32x2*)(p.stats + m * p.parts * 2);
   float top = -__builtin_inff();
   bool nan = false;
-  for (int i = lane; i < p.parts; i += 64) {
-    const float v = st[2 * i];
-    nan |= v != v || st[2 * i + 1] != st[2 * i + 1];
-    top = v > top ? v : top;
+  for (int i = threadIdx.x; i < p.parts; i += 256) {
+    const f32x2 v = st[i];
+    nan |= v[0] != v[0] || v[1] != v[1] || v[0] == __builtin_inff();
+    top = v[0] > top ? v[0] : top;
   }
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) {
     const float o = __shfl_xor(top, d, 64);
     top = o > top ? o : top;
   }
-  nan = __any(nan);
+  if (lane == 0) sh[w] = top;
+  const bool any = __any(nan);
+  if (lane == 0) sh_nan[w] = any;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    top = sh[i] > top ? sh[i] : top;
+    nan |= sh_nan[i] != 0;
+  }
+  __syncthreads();
   float sum = 0.0f;
-  for (int i = lane; i < p.parts; i += 64) {
-    const float y = (st[2 * i] - top) * kLog2e;
-    sum += st[2 * i] == top ? st[2 * i + 1] : exp2_fast(y) * st[2 * i + 1];
+  for (int i = threadIdx.x; i < p.parts; i += 256) {
+    const f32x2 v = st[i];
+    sum += v[0] == top ? v[1] : exp2_fast((v[0] - top) * kLog2e) * v[1];
   }
 #pragma unroll
   for (int d = 32; d >= 1; d >>= 1) sum += __shfl_xor(sum, d, 64);
-  if (lane != 0) return;
+  if (lane == 0) sh[w] = sum;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  sum = (sh[0] + sh[1]) + (sh[2] + sh[3]);
   float lse = top + log2_fast(sum) * kLn2;
-  if (nan || top == __builtin_inff()) lse = bits_f32(0x7fc00000u);
+  if (nan) lse = bits_f32(0x7fc00000u);
   p.lse[m] = lse;
   const int64_t t = p.targets[m];
   p.loss[m] = t < 0 ? 0.0f : t >= p.V ? bits_f32(0x7fc00000u) : lse - p.chosen[m];
@@ -299,16 +362,33 @@ hipError_t launch_lists(const int32_t* ids, int64_t n, int64_t experts, int32_t 
   return hipGetLastError();
 }
 
-hipError_t launch_split(const void* x, int64_t ldx, int32_t dtype, int64_t K,
-                        int32_t nibble_order, const int32_t* ids, int64_t experts,
-                        const SplitRows& r, hipStream_t s) {
-  const dim3 grid((uint32_t)r.rows);
-  if (dtype == Q4_DTYPE_F32)
-    hipLaunchKernelGGL(split_kernel<float>, grid, dim3(256), 0, s, (const float*)x, ldx, K, nibble_order, ids, (int32_t)experts, r, aligned16(x, ldx, 4));
-  else if (dtype == Q4_DTYPE_F16)
-    hipLaunchKernelGGL(split_kernel<_Float16>, grid, dim3(256), 0, s, (const _Float16*)x, ldx, K, nibble_order, ids, (int32_t)experts, r, aligned16(x, ldx, 2));
+template <typename T>
+static void split_of(const void* x, int64_t ldx, int64_t K, int32_t order, const int32_t* ids,
+                     int64_t experts, const SplitRows& r, hipStream_t s) {
+  const dim3 grid((uint32_t)((r.rows + 3) / 4));
+  const bool vec = aligned16(x, ldx, sizeof(T));
+#define Q4_SPLIT(HOLD)                                                                             \
+  hipLaunchKernelGGL((split_kernel<T, HOLD>), grid, dim3(256), 0, s, (const T*)x, ldx, K, order, ids, \
+                     (int32_t)experts, r, vec)
+  if (r.Kp <= 1024)
+    Q4_SPLIT(2);
+  else if (r.Kp <= 2048)
+    Q4_SPLIT(4);
+  else if (r.Kp <= 4096)
+    Q4_SPLIT(8);
   else
-    hipLaunchKernelGGL(split_kernel<bf16>, grid, dim3(256), 0, s, (const bf16*)x, ldx, K, nibble_order, ids, (int32_t)experts, r, aligned16(x, ldx, 2));
+    Q4_SPLIT(0);
+#undef Q4_SPLIT
+}
+
+hipError_t launch_split(const void* x, int64_t ldx, int32_t dtype, int64_t K, int32_t nibble_order,
+                        const int32_t* ids, int64_t experts, const SplitRows& r, hipStream_t s) {
+  if (dtype == Q4_DTYPE_F32)
+    split_of<float>(x, ldx, K, nibble_order, ids, experts, r, s);
+  else if (dtype == Q4_DTYPE_F16)
+    split_of<_Float16>(x, ldx, K, nibble_order, ids, experts, r, s);
+  else
+    split_of<bf16>(x, ldx, K, nibble_order, ids, experts, r, s);
   return hipGetLastError();
 }
 
@@ -325,7 +405,7 @@ hipError_t launch_combine(const CombineParams& p, int32_t dtype, hipStream_t s) 
 
 hipError_t launch_row_bits(const void* x, int64_t ldx, int32_t dtype, int64_t rows, int64_t K,
                            uint32_t* bits, uint32_t* zero, int64_t zeros, hipStream_t s) {
-  const dim3 grid((uint32_t)(rows + (zeros + 255) / 256));
+  const dim3 grid((uint32_t)((rows + (zeros + 63) / 64 + 3) / 4));
   if (dtype == Q4_DTYPE_F32)
     hipLaunchKernelGGL(row_bits_kernel<float>, grid, dim3(256), 0, s, (const float*)x, ldx, rows, K,
                        bits, zero, zeros, aligned16(x, ldx, 4));
@@ -353,7 +433,7 @@ hipError_t launch_gate_sums(const float* part, int32_t parts, const int32_t* ids
 }
 
 hipError_t launch_head_finish(const HeadFinish& p, hipStream_t s) {
-  hipLaunchKernelGGL(head_finish_kernel, dim3((uint32_t)((p.M + 3) / 4)), dim3(256), 0, s, p);
+  hipLaunchKernelGGL(head_finish_kernel, dim3((uint32_t)p.M), dim3(256), 0, s, p);
   return hipGetLastError();
 }
 
