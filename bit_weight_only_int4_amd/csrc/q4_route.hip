@@ -1,7 +1,7 @@
 // q4_route.hip -- the choice of experts and its gradient, for gfx950.
 //
-// A wave owns a token; lane l holds experts l, l + 64, ...  Choosing is top_k
-// rounds of a maximum over the lanes.  Values are ordered as integers: without
+// A wave owns a token; lane l holds EPL experts from EPL l on, so that a lower
+// lane has lower experts.  Choosing is top_k rounds of a maximum over the lanes.  Values are ordered as integers: without
 // a bias the logit's 32 bits (scores have their order), with one the 64 bits of
 // score + bias formed in fp64, so that no rounding of a score decides between
 // two experts (fp32 sums of 8192 tokens over 256 experts differ from the exact
@@ -49,26 +49,45 @@ __device__ __forceinline__ T wave_sum(T x) {
   return x;
 }
 
-// The largest key of the wave and the lowest expert that has it.
+// The largest value of the wave, in every lane.  The lanes' neighbours come
+// through the vector unit's own lane moves (by 1, 2, 4, 8 within 16 lanes, then
+// the rows' last lanes), a few cycles each, and not through LDS.
+__device__ __forceinline__ uint32_t wave_most(uint32_t x) {
+#define Q4_STEP(ctrl, rows) \
+  x = umax(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, ctrl, rows, 0xf, false))
+  Q4_STEP(0x111, 0xf);
+  Q4_STEP(0x112, 0xf);
+  Q4_STEP(0x114, 0xf);
+  Q4_STEP(0x118, 0xf);
+  Q4_STEP(0x142, 0xa);
+  Q4_STEP(0x143, 0xc);
+#undef Q4_STEP
+  return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
+}
+
+// The largest key of the wave and the lowest expert that has it: that of the
+// first lane with this key.
 __device__ __forceinline__ void wave_best(uint32_t& key, int32_t& id) {
-  uint64_t v = ((uint64_t)key << 32) | (uint32_t)~id;
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) {
-    const uint64_t o = __shfl_xor((unsigned long long)v, m, 64);
-    v = o > v ? o : v;
-  }
-  key = (uint32_t)(v >> 32);
-  id = (int32_t)~(uint32_t)v;
+  const uint32_t top = wave_most(key);
+  id = __builtin_amdgcn_readlane(id, (int)__builtin_ctzll(__ballot(key == top)));
+  key = top;
 }
 __device__ __forceinline__ void wave_best(uint64_t& key, int32_t& id) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) {
-    const uint64_t o = __shfl_xor((unsigned long long)key, m, 64);
-    const int32_t oi = __shfl_xor(id, m, 64);
-    const bool take = o > key || (o == key && oi < id);
-    key = take ? o : key;
-    id = take ? oi : id;
+  const uint32_t hi = wave_most((uint32_t)(key >> 32));
+  const bool mine = (uint32_t)(key >> 32) == hi;
+  uint64_t m = __ballot(mine);
+  if (m & (m - 1)) {
+    const uint32_t lo = wave_most(mine ? (uint32_t)key : 0u);  // by all lanes
+    m = __ballot(mine & ((uint32_t)key == lo));
   }
+  const int from = (int)__builtin_ctzll(m);
+  id = __builtin_amdgcn_readlane(id, from);
+  key = ((uint64_t)hi << 32) | (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)key, from);
+}
+
+__device__ __forceinline__ uint32_t shuffle_xor(uint32_t x, int d) { return __shfl_xor(x, d, 64); }
+__device__ __forceinline__ uint64_t shuffle_xor(uint64_t x, int d) {
+  return __shfl_xor((unsigned long long)x, d, 64);
 }
 
 template <bool BIAS>
@@ -98,7 +117,7 @@ __global__ void __launch_bounds__(64 * kWaves) route_kernel(const RouteParams p)
   bool nan = false;
 #pragma unroll
   for (int i = 0; i < EPL; ++i) {
-    const int e = i * 64 + lane;
+    const int e = lane * EPL + i;
     z[i] = e < p.E ? plus_zero(to_f32(row[e])) : -__builtin_inff();
     nan |= z[i] != z[i];
     top = z[i] > top ? z[i] : top;
@@ -125,7 +144,7 @@ __global__ void __launch_bounds__(64 * kWaves) route_kernel(const RouteParams p)
     if (softmax) sum = wave_sum(sum);
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const int e = i * 64 + lane;
+      const int e = lane * EPL + i;
       const bool in = e < p.E && z[i] != -__builtin_inff();
       const double v = (softmax ? s[i] / sum : s[i]) + (e < p.E ? (double)p.bias[e] : 0.0);
       key[i] = !in ? 0 : z[i] != z[i] ? 1 : key64(v + 0.0);
@@ -136,64 +155,102 @@ __global__ void __launch_bounds__(64 * kWaves) route_kernel(const RouteParams p)
   }
 
   if (p.groups > 1) {
-    // lane g < groups collects group g's value; groups <= E <= 64 * EPL, so a
-    // lane may have several
+    // a group's value: its largest key, with a bias the sum of its two largest
     const int per = p.E / p.groups;
-    Key value[EPL];
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) value[i] = 0;
-    for (int g = 0; g < p.groups; ++g) {
-      Key best = 0;
-      int32_t at = 0x7fffffff;
-#pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        const int e = i * 64 + lane;
-        const bool mine = e >= g * per && e < (g + 1) * per && key[i] > best;
-        best = mine ? key[i] : best;
-        at = mine ? e : at;
-      }
-      wave_best(best, at);
+    auto value_of = [](Key best, Key second) {
       if constexpr (BIAS) {
-        uint64_t second = 0;
-        int32_t at2 = 0x7fffffff;
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) {
-          const int e = i * 64 + lane;
-          const bool mine = e >= g * per && e < (g + 1) * per && e != at && key[i] > second;
-          second = mine ? key[i] : second;
-          at2 = mine ? e : at2;
-        }
-        wave_best(second, at2);
         if (second) best = key64(key_value(best) + key_value(second) + 0.0);
       }
-#pragma unroll
-      for (int i = 0; i < EPL; ++i)
-        if (i == (g >> 6) && lane == (g & 63)) value[i] = best;
-    }
-    // the groups that stay, as a bit per group of each lane's slots
-    uint32_t kept[EPL];
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) kept[i] = 0;
-    for (int r = 0; r < p.top_groups; ++r) {
-      Key best = 0;
-      int32_t at = 0x7fffffff;
+      return best;
+    };
+    const int lanes = per / EPL;
+    if (lanes * EPL == per && (lanes & (lanes - 1)) == 0) {
+      // groups of whole lanes, a power of two of them: all groups join their
+      // lanes' two largest keys at once, and every lane has its group's value
+      Key best = 0, second = 0;
 #pragma unroll
       for (int i = 0; i < EPL; ++i) {
-        const bool take = value[i] > best;
-        best = take ? value[i] : best;
-        at = take ? i * 64 + lane : at;
+        const bool up = key[i] > best;
+        const Key less = up ? best : key[i];
+        best = up ? key[i] : best;
+        second = less > second ? less : second;
       }
-      wave_best(best, at);
-      if (best == 0) break;
+      for (int d = 1; d < lanes; d <<= 1) {
+        const Key ob = shuffle_xor(best, d), os = shuffle_xor(second, d);
+        const Key less = ob > best ? best : ob;
+        best = ob > best ? ob : best;
+        second = os > second ? os : second;
+        second = less > second ? less : second;
+      }
+      Key value = value_of(best, second);
+      bool kept = false;
+      for (int r = 0; r < p.top_groups; ++r) {
+        Key top = value;
+        int32_t at = lane / lanes;
+        wave_best(top, at);
+        if (top == 0) break;
+        if (lane / lanes == at) {
+          value = 0;
+          kept = true;
+        }
+      }
 #pragma unroll
-      for (int i = 0; i < EPL; ++i) {
-        if (i * 64 + lane == at) value[i] = 0;
-        const int e = i * 64 + lane;
-        if (e >= at * per && e < (at + 1) * per) kept[i] = 1;
+      for (int i = 0; i < EPL; ++i) key[i] = kept ? key[i] : 0;
+    } else {
+      // one group after the other; lane l collects the values of groups EPL l
+      // and on (groups <= E <= 64 EPL)
+      Key value[EPL];
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) value[i] = 0;
+      for (int g = 0; g < p.groups; ++g) {
+        Key best = 0, second = 0;
+        int32_t at = 0, at2 = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+          const int e = lane * EPL + i;
+          const bool mine = e >= g * per && e < (g + 1) * per && key[i] > best;
+          best = mine ? key[i] : best;
+          at = mine ? e : at;
+        }
+        wave_best(best, at);
+        if constexpr (BIAS) {
+#pragma unroll
+          for (int i = 0; i < EPL; ++i) {
+            const int e = lane * EPL + i;
+            const bool mine = e >= g * per && e < (g + 1) * per && e != at && key[i] > second;
+            second = mine ? key[i] : second;
+          }
+          wave_best(second, at2);
+        }
+        best = value_of(best, second);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i)
+          if (g == lane * EPL + i) value[i] = best;
       }
+      uint32_t kept[EPL];
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) kept[i] = 0;
+      for (int r = 0; r < p.top_groups; ++r) {
+        Key best = 0;
+        int32_t at = 0;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+          const bool take = value[i] > best;
+          best = take ? value[i] : best;
+          at = take ? lane * EPL + i : at;
+        }
+        wave_best(best, at);
+        if (best == 0) break;
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) {
+          const int e = lane * EPL + i;
+          if (e == at) value[i] = 0;
+          if (e >= at * per && e < (at + 1) * per) kept[i] = 1;
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < EPL; ++i) key[i] = kept[i] ? key[i] : 0;
     }
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) key[i] = kept[i] ? key[i] : 0;
   }
 
   // lane j keeps choice j
@@ -201,23 +258,23 @@ __global__ void __launch_bounds__(64 * kWaves) route_kernel(const RouteParams p)
   float chosen = -__builtin_inff();
   for (int j = 0; j < p.top_k; ++j) {
     Key best = 0;
-    int32_t at = 0x7fffffff;
+    int32_t at = 0;
     float zb = 0.0f;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
       const bool take = key[i] > best;
       best = take ? key[i] : best;
-      at = take ? i * 64 + lane : at;
+      at = take ? lane * EPL + i : at;
     }
     wave_best(best, at);
     if (best == 0) break;
 #pragma unroll
     for (int i = 0; i < EPL; ++i) {
-      const bool mine = i * 64 + lane == at;
+      const bool mine = lane * EPL + i == at;
       zb = mine ? z[i] : zb;
       key[i] = mine ? 0 : key[i];
     }
-    zb = __shfl(zb, at & 63, 64);
+    zb = __shfl(zb, at / EPL, 64);
     if (lane == j) {
       id = at;
       chosen = zb;
