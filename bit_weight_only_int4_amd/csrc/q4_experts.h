@@ -114,8 +114,6 @@ struct GemmParams {
   _Float16* d_parts;      // [parts][rows of a][out_ld]: times it, scaled as BackParams says
   const uint32_t* s_bits;
 };
-// rows of a tile the launcher takes for `n` rows over `experts` matrices
-int32_t gemm_tile_rows(int64_t n, int64_t experts);
 hipError_t launch_gemm(const GemmParams& p, int32_t tile_rows, Epilogue epi, hipStream_t s);
 
 // Few rows per expert: up to 16 rows of binary16 operands a tile, weights
@@ -139,7 +137,7 @@ struct FewParams {
   int64_t width;
 };
 constexpr int64_t kFewDepth = 8192;  // of their rows, at most
-constexpr int kFewDirect = 64;  // slots up to which workgroups find their rows themselves
+constexpr int kFewDirect = 48;  // slots up to which workgroups find their rows themselves
 hipError_t launch_few(const FewParams& p, int32_t tile_rows, bool gated, hipStream_t s);
 
 // out[t] = sum_j weights[t, j] y[t * top_k + j]; weights NULL: all 1

@@ -108,19 +108,35 @@ struct ExpertsPlan {
   size_t bytes;
 };
 
+// Tiles of 128 rows unpack a word for twice the rows; tiles of 64 waste less
+// where an expert's rows end.  64 / 128, us: 32 experts of 2048 x 1408 in groups
+// of 128, 128 rows each, fp32 249 / 287, 192 332 / 341, 256 425 / 418, 512
+// 782 / 719; bf16 174 / 183, 234 / 248, 291 / 305, 511 / 519; 8 experts of
+// 4096 x 3584 in groups of 32, 384 rows, 800 / 734 and 541 / 495.
+int32_t gemm_tile_rows(int64_t n, int64_t experts) { return n >= 320 * experts ? 128 : 64; }
+
 ExpertsPlan plan_experts(void* ws, int32_t dtype, int64_t T, int64_t H, int64_t W, int64_t E,
                          int64_t k) {
   ExpertsPlan p{};
   Carve c(ws);
   p.n = T * k;
   const int32_t parts = parts_of(dtype);
-  // up to 16 rows an expert on average the weights' bytes count, not the products
-  p.few = p.n <= 16 * E && H <= q4::kFewDepth && W <= q4::kFewDepth;
-  p.direct = p.few && p.n <= q4::kFewDirect;
+  // While an expert has few rows on average the weights' bytes count, not the
+  // products; a workgroup of the kernel for few rows has 16 rows, and deep ones
+  // are dear to split in each of them.  fp32, few / tiles, us: 64 experts of
+  // 2048 x 1024, 8 rows each 80 / 127, 12 102 / 127, 16 124 / 130, 24 176 / 138
+  // (bf16 63 / 82, 76 / 83, 90 / 84, 119 / 92); 8 experts of 4096 x 3584, 4 rows
+  // 114 / 147, 6 135 / 146, 8 188 / 148 (bf16 105 / 128, 126 / 126, 145 / 129).
+  p.few = p.n <= (H <= 2048 && W <= 2048 ? 12 : 6) * E && H <= q4::kFewDepth && W <= q4::kFewDepth;
+  // Few slots, mostly alone in their experts: each has workgroups, which look
+  // for others of its expert, and the launch that lists the rows falls away.
+  // Direct / listed, us: 64 experts, 8 slots 19.2 / 22.8, 32 37.9 / 40.2, 64
+  // 55.7 / 54.1; 16 experts, 14 slots 40.8 / 42.0, 64 101 / 86.
+  p.direct = p.few && p.n <= q4::kFewDirect && p.n <= E;
   // (a token is in an expert's list once, as a rule: more tiles hold the others;
   // rows of more than 4096 share LDS by eight)
   const int64_t most = (H > 4096 || W > 4096 ? 8 : 16) / parts, few_rows = T < most ? T : most;
-  p.tile_rows = p.few ? (int32_t)few_rows : q4::gemm_tile_rows(p.n, E);
+  p.tile_rows = p.few ? (int32_t)few_rows : gemm_tile_rows(p.n, E);
   p.bound = p.n ? q4::tile_bound(p.n, E, p.tile_rows) : 0;
   p.h = c.take<float>(p.n * W);
   p.y = c.take<float>(p.n * H);
@@ -150,17 +166,29 @@ struct ExpertsBackPlan {
   size_t bytes;
 };
 
+// As above for the gradient, 64 / 128, us.  One scale for a tile's columns: 32
+// experts of 2048 x 1408 in groups of 128, 128 rows each, fp32 340 / 430, 256
+// 536 / 614, 512 940 / 1034, 1024 1791 / 1777; bf16 287 / 366, 460 / 514,
+// 797 / 881, 1508 / 1542 (8 experts of 4096 x 3584, 1024 rows: 2085 / 2021 and
+// 1743 / 1678).  Groups of 32, where the operand is made once a group: 128 rows
+// 630 / 730, 256 1072 / 1024, 512 1876 / 1734; bf16 540 / 465, 913 / 781,
+// 1600 / 1338.
+int32_t back_tile_rows(int64_t n, int64_t experts, int64_t group) {
+  return n >= (group % 128 == 0 ? 1024 : 192) * experts ? 128 : 64;
+}
+
+// (the bytes are those of any group)
 ExpertsBackPlan plan_experts_back(void* ws, int32_t dtype, int64_t T, int64_t H, int64_t W,
-                                  int64_t E, int64_t k) {
+                                  int64_t E, int64_t k, int64_t group) {
   ExpertsBackPlan p{};
   Carve c(ws);
   p.n = T * k;
   p.parts = parts_of(dtype);  // of the second product: dweights is fp32 for every type
-  p.tile_rows = q4::gemm_tile_rows(p.n, E);
+  p.tile_rows = back_tile_rows(p.n, E, group);
   p.bound = q4::tile_bound(p.n, E, p.tile_rows);
   p.width_tiles = (W + 127) / 128;
   p.hidden_tiles = (H + 127) / 128;
-  p.lists = take_lists(c, p.n, E, p.tile_rows);
+  p.lists = take_lists(c, p.n, E, 64);
   p.dout_bits = c.take<uint32_t>(T);
   p.dpre_bits = c.take<uint32_t>(p.n + 2 * E);
   p.s_bits = p.dpre_bits + p.n;
@@ -195,23 +223,35 @@ struct HeadPlan {
   size_t bytes;
 };
 
+// A head's rows end once: tiles of 128 where their last one is not half empty,
+// or where there are many.  64 / 128, loss of 32003 x 2048, fp32, us: 96 rows
+// 44 / 54, 160 59 / 71, 256 90 / 77, 320 96 / 109, 512 143 / 139; bf16 38 / 38,
+// 46 / 47, 58 / 49, 67 / 62, 98 / 88.
+int32_t head_tile_rows(int64_t rows) {
+  return rows > 320 || (rows > 192 && rows <= 256) ? 128 : 64;
+}
+
 HeadPlan plan_head(void* ws, int32_t dtype, int64_t M, int64_t V, int64_t K, bool back) {
   HeadPlan p{};
   Carve c(ws);
   p.rows = M < kHeadRows ? M : kHeadRows;
   p.parts = parts_of(dtype);
-  p.tile_rows = q4::gemm_tile_rows(p.rows, 1);
+  p.tile_rows = head_tile_rows(p.rows);
   p.xs = take_split(c, p.rows, K, p.parts);
   if (!back) {
     p.stats = c.take<float>(p.rows * ((V + 127) / 128) * 4);
     p.chosen = c.take<float>(p.rows);
   } else {
-    // a piece's gradient stays in the last-level cache between its two products
-    const int64_t most = (int64_t)(128 << 20) / 4 / p.rows;
+    // A piece's gradient is to stay in the last-level cache between its two
+    // products.  2048 rows of bf16 over 128257 x 2048: 64 MB a piece 2932 us, 128
+    // 2588, 256 2483, 512 2557; fp32 4597, 4375, 4390, 4469.
+    const int64_t most = (int64_t)(256 << 20) / 4 / p.rows;
     const int64_t pieces = (V + (most > 1024 ? most : 1024) - 1) / (most > 1024 ? most : 1024);
     p.piece = ((V + pieces - 1) / pieces + 127) / 128 * 128;
     const int64_t tiles = (p.rows + p.tile_rows - 1) / p.tile_rows * ((K + 127) / 128);
-    // two workgroups for every CU; each split at least 8 steps deep
+    // Two workgroups for every CU; each split at least 8 steps deep.  333 rows,
+    // 32003 x 2048, bf16: one split 491 us, a workgroup a CU 173, two 153, four
+    // 148 (fp32 785, 282, 241, 249).
     int64_t splits = 512 / tiles;
     if (splits > p.piece / 512) splits = p.piece / 512;
     p.splits = (int32_t)(splits < 1 ? 1 : splits > 16 ? 16 : splits);
@@ -402,7 +442,7 @@ size_t q4_experts_backward_workspace_bytes(int32_t dtype, int64_t T, int64_t hid
   if (!experts_sizes_ok(dtype, T, hidden, width, experts, top_k) || T == 0 ||
       group_status(group_size, hidden) != Q4_OK || group_status(group_size, width) != Q4_OK)
     return 0;
-  return plan_experts_back(nullptr, dtype, T, hidden, width, experts, top_k).bytes;
+  return plan_experts_back(nullptr, dtype, T, hidden, width, experts, top_k, 0).bytes;
 }
 
 q4_status q4_experts_backward(const void* dout, int64_t lddo, int32_t dtype, int64_t T,
@@ -429,7 +469,7 @@ q4_status q4_experts_backward(const void* dout, int64_t lddo, int32_t dtype, int
     return Q4_ERR_INVALID_ARG;
   const Packed gu = q4::packed(gate_up, gate_up_scales, 2 * width, hidden, group_size);
   const Packed dn = q4::packed(down, down_scales, hidden, width, group_size);
-  ExpertsBackPlan pl = plan_experts_back(workspace, dtype, T, hidden, width, experts, top_k);
+  ExpertsBackPlan pl = plan_experts_back(workspace, dtype, T, hidden, width, experts, top_k, group_size);
   const int64_t most = pl.width_tiles > pl.hidden_tiles ? pl.width_tiles : pl.hidden_tiles;
   if ((double)pl.bound * (double)most > (double)q4::kMaxGrid) return Q4_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < pl.bytes || !aligned(workspace, 16)) return Q4_ERR_WORKSPACE;

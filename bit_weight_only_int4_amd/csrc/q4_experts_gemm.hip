@@ -15,8 +15,6 @@ Q4_TILES(kHeadStats)
 Q4_TILES(kHeadGrad)
 #undef Q4_TILES
 
-int32_t gemm_tile_rows(int64_t n, int64_t experts) { return n >= 64 * experts ? 128 : 64; }
-
 namespace {
 template <Epilogue EPI>
 hipError_t by_tile(const GemmParams& p, int32_t tile_rows, hipStream_t s) {
