@@ -166,3 +166,22 @@ def test_no_tokens():
     r = q4.route(torch.empty(0, 8).cuda(), 2)
     assert r.ids.shape == (0, 2)
     assert q4.route_backward(torch.empty(0, 8).cuda(), r.ids, r.weights).shape == (0, 8)
+
+
+@pytest.mark.parametrize("E,groups,top_groups,k", [(64, 64, 10, 8), (128, 64, 5, 7), (256, 16, 3, 10), (160, 8, 3, 6),
+                                                   (96, 8, 4, 8), (512, 32, 6, 32), (1024, 2, 1, 5), (1024, 512, 9, 4), (48, 3, 2, 9)])
+@pytest.mark.parametrize("way", [dict(), dict(bias=True), dict(kind="sigmoid", bias=True)])
+def test_groups_of_any_size(E, groups, top_groups, k, way):
+    """Groups of whole lanes and others, with equal and masked logits among them."""
+    z, zv = logits(33, E, "bf16", E + groups, holes=0.2)
+    z[5] = z[6] = 0.5
+    zv[5] = zv[6] = 0.5
+    bias = np.random.default_rng(1).normal(size=E).astype(np.float32) if way.get("bias") else None
+    if bias is not None:
+        bias[: E // 2] = bias[0]
+    r = q4.route(z.cuda(), k, bias=None if bias is None else torch.from_numpy(bias).cuda(), groups=groups,
+                 top_groups=top_groups, score=way.get("kind", "softmax"))
+    for t in range(33):
+        ids, w = oracle.route(zv[t], k, **{**way, "bias": bias}, groups=groups, top_groups=top_groups)
+        assert r.ids[t].tolist() == ids.tolist()
+        assert (np.abs(r.weights[t].double().cpu().numpy() - w) <= 32 * 2.0 ** -24 * w).all()
