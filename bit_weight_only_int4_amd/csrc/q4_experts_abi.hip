@@ -193,7 +193,7 @@ ExpertsBackPlan plan_experts_back(void* ws, int32_t dtype, int64_t T, int64_t H,
   p.dpre_bits = c.take<uint32_t>(p.n + 2 * E);
   p.s_bits = p.dpre_bits + p.n;
   p.dpre = c.take<float>(p.n * 2 * W);
-  p.dw_part = c.take<float>(p.n * 2 * p.width_tiles);
+  p.dw_part = c.take<float>(p.n * 4 * p.width_tiles);  // a wave's each
   p.dx = c.take<float>(p.n * H);
   p.bytes = c.at;
   return p;
@@ -516,7 +516,7 @@ q4_status q4_experts_backward(const void* dout, int64_t lddo, int32_t dtype, int
   b.dpre_bits = pl.dpre_bits;
   if (err == hipSuccess) err = q4::launch_back(b, pl.tile_rows, true, s);
   if (err == hipSuccess)
-    err = q4::launch_gate_sums(pl.dw_part, (int32_t)(2 * pl.width_tiles), ids, n, experts, dweights, s);
+    err = q4::launch_gate_sums(pl.dw_part, (int32_t)((pl.tile_rows == 64 ? 4 : 2) * pl.width_tiles), ids, n, experts, dweights, s);
   b.w = gu;
   b.d = pl.dpre;
   b.ldd = 2 * width;

@@ -53,7 +53,7 @@ __device__ __forceinline__ void turn_words(const uint32_t (&w)[4], uint32_t (&t)
 template <int P, typename T, int BM, int NG, bool GATE>
 __global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
   typedef BackTile<P, BM, NG> L;
-  constexpr int RB = BM / 64, NS = L::kN, S = L::kStages;
+  constexpr int CB = BM / 64, WC = 4 / CB, NS = L::kN, S = L::kStages;
   constexpr int kChunks = NS / 8;            // 16-byte pieces of a row
   constexpr int kPasses = BM * kChunks / 256;  // rows of a thread
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wr = w >> 1, wc = w & 1, c = lane & 31, q = lane >> 5;
+  const int wr = w / WC, wc = w % WC, c = lane & 31, q = lane >> 5;
 
   const int32_t row_tiles = p.tiles ? *p.n_tiles : p.row_tiles;
   const uint32_t total = (uint32_t)row_tiles * (uint32_t)p.col_tiles * (uint32_t)p.splits;
@@ -231,35 +231,37 @@ __global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
     }
   };
 
-  f32x16 acc[RB][2];
+  f32x16 acc[2][CB];
 #pragma unroll
-  for (int r = 0; r < RB; ++r)
+  for (int r = 0; r < 2; ++r)
 #pragma unroll
-    for (int b = 0; b < 2; ++b) acc[r][b] = f32x16{};
+    for (int b = 0; b < CB; ++b) acc[r][b] = f32x16{};
   const Magic magic = Magic::make();
   auto products = [&](int step) {
     const uint8_t* base = smem + (S == 2 ? (step & 1) * L::kStage : 0);
 #pragma unroll
     for (int h = 0; h < NS / 32; ++h) {
-      uint32_t words[2][2];
+      uint32_t words[CB][2];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const u32x2 x = *(const u32x2*)(base + L::kA + (wc * 64 + b * 32 + c) * (NS / 2) + h * 16 + q * 8);
+      for (int b = 0; b < CB; ++b) {
+        const u32x2 x = *(const u32x2*)(base + L::kA + ((wc * CB + b) * 32 + c) * (NS / 2) + h * 16 + q * 8);
         words[b][0] = x[0];
         words[b][1] = x[1];
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const h8 bo[2] = {codes_of(words[0][j], magic), codes_of(words[1][j], magic)};
+        h8 bo[CB];
 #pragma unroll
-        for (int r = 0; r < RB; ++r) {
-          const int row = wr * (BM / 2) + r * 32 + c;
+        for (int b = 0; b < CB; ++b) bo[b] = codes_of(words[b][j], magic);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int row = wr * 64 + r * 32 + c;
           const int at_ = row * (NS * 2) + (((h * 4 + q * 2 + j) ^ turn_of(row)) * 16);
 #pragma unroll
           for (int pc = 0; pc < P; ++pc) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
-              const int g = NG == 1 ? 0 : wc * 2 + b;
+            for (int b = 0; b < CB; ++b) {
+              const int g = NG == 1 ? 0 : wc * CB + b;
               const h8 a = *(const h8*)(base + (g * P + pc) * L::kPart + at_);
               acc[r][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, bo[b], acc[r][b], 0, 0, 0);
             }
@@ -269,7 +271,7 @@ __global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
     }
   };
 
-  const bool idle = wr * (BM / 2) >= rows;  // a wave without rows
+  const bool idle = wr * 64 >= rows;  // a wave without rows
   if constexpr (S == 2) {
     // loads two steps ahead of their use: a step's products are shorter than
     // the way from memory
@@ -309,15 +311,15 @@ __global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
 
   // ---- results -------------------------------------------------------------
 #pragma unroll
-  for (int r = 0; r < RB; ++r) {
-    const int r0 = wr * (BM / 2) + r * 32 + 4 * q;
+  for (int r = 0; r < 2; ++r) {
+    const int r0 = wr * 64 + r * 32 + 4 * q;
     if constexpr (GATE) {
       float dot[16], top[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) dot[i] = top[i] = 0.0f;
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int64_t k = k0 + wc * 64 + b * 32 + (c & 3) * 8 + (c >> 2);
+      for (int b = 0; b < CB; ++b) {
+        const int64_t k = k0 + (wc * CB + b) * 32 + (c & 3) * 8 + (c >> 2);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int row = r0 + 8 * (i >> 2) + (i & 3), slot = sh_slot[row];
@@ -341,15 +343,15 @@ __global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
       if ((lane & 16) == 0) {
         const int i = lane & 15, row = r0 + 8 * (i >> 2) + (i & 3), slot = sh_slot[row];
         if (slot >= 0) {
-          p.dw_part[((int64_t)slot * p.col_tiles + ct) * 2 + wc] = sum;
+          p.dw_part[((int64_t)slot * p.col_tiles + ct) * WC + wc] = sum;
           atomicMax(p.dpre_bits + slot, f32_bits(most));
         }
       }
     } else {
       float* out = p.out + (int64_t)split * p.M * p.out_ld;
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int64_t k = k0 + wc * 64 + b * 32 + (c & 3) * 8 + (c >> 2);
+      for (int b = 0; b < CB; ++b) {
+        const int64_t k = k0 + (wc * CB + b) * 32 + (c & 3) * 8 + (c >> 2);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int row = r0 + 8 * (i >> 2) + (i & 3), slot = sh_slot[row];

@@ -89,6 +89,10 @@ __device__ __forceinline__ void settle(V (&a)[2][2]) {
                : "+v"(a[0][0]), "+v"(a[0][1]), "+v"(a[1][0]), "+v"(a[1][1]));
 }
 template <typename V>
+__device__ __forceinline__ void settle(V (&a)[2][1]) {
+  asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" : "+v"(a[0][0]), "+v"(a[1][0]));
+}
+template <typename V>
 __device__ __forceinline__ void settle(V (&a)[1][2]) {
   asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 7" : "+v"(a[0][0]), "+v"(a[0][1]));
 }
