@@ -105,7 +105,7 @@ struct GemmParams {
   int64_t out_ld;
   float* pre;             // kGatedRows, optional: [slot][2 width]
   int64_t width;
-  float* stats;           // kHeadStats: [M][col_tiles][2]
+  float* stats;           // kHeadStats: [M][col_tiles][waves side by side][2]
   float* chosen;          // kHeadStats: [M] logit of the target
   const int64_t* targets;
   const float* lse;       // kHeadGrad

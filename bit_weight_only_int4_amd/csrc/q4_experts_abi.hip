@@ -239,7 +239,7 @@ HeadPlan plan_head(void* ws, int32_t dtype, int64_t M, int64_t V, int64_t K, boo
   p.tile_rows = head_tile_rows(p.rows);
   p.xs = take_split(c, p.rows, K, p.parts);
   if (!back) {
-    p.stats = c.take<float>(p.rows * ((V + 127) / 128) * 4);
+    p.stats = c.take<float>(p.rows * ((V + 127) / 128) * 2 * (p.tile_rows == 64 ? 4 : 2));
     p.chosen = c.take<float>(p.rows);
   } else {
     // A piece's gradient is to stay in the last-level cache between its two
@@ -580,7 +580,7 @@ q4_status q4_head_cross_entropy(const void* x, int64_t ldx, int32_t dtype, int64
     g.chosen = pl.chosen;
     g.targets = targets + m0;
     if (err == hipSuccess) err = q4::launch_gemm(g, pl.tile_rows, q4::kHeadStats, s);
-    q4::HeadFinish f{pl.stats, 2 * g.col_tiles, pl.chosen, targets + m0, xs.rows, vocab, loss + m0,
+    q4::HeadFinish f{pl.stats, (pl.tile_rows == 64 ? 4 : 2) * g.col_tiles, pl.chosen, targets + m0, xs.rows, vocab, loss + m0,
                      lse + m0};
     if (err == hipSuccess) err = q4::launch_head_finish(f, s);
   }

@@ -4,7 +4,7 @@
 //   z[r, n] = sum_g s[g, n] * sum_{k in g} a[r, k] c[n, k]
 //
 // with the rows of an expert (or of the head) in tiles of BM and 128 columns,
-// four waves of BM/2 x 64 as 32x32x16 products.  A step is 64 k: rows of a and
+// four waves of 64 rows and BM/2 columns as 32x32x16 products.  A step is 64 k: rows of a and
 // packed words come by direct loads into LDS (chunks of 16 bytes of a turned by
 // row so that the reads meet no bank twice) in a ring of S stages, a barrier
 // each.  A wave unpacks the words it needs itself, two
@@ -90,7 +90,8 @@ typedef Flag<false> No;
 template <int P, int BM, int GM, Epilogue EPI>
 __global__ void __launch_bounds__(256, GM == kOneGroup && P == 1 ? 3 : 2) gemm_kernel(const GemmParams p) {
   typedef GemmTile<P, BM, GM> L;
-  constexpr int RB = BM / 64;  // row blocks of a wave
+  constexpr int CB = BM / 64;  // column blocks of a wave (and two of rows)
+  constexpr int WC = 4 / CB;   // waves side by side
   constexpr int S = L::kStages;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   __shared__ int32_t sh_slot[BM], sh_exp[BM];
@@ -100,7 +101,7 @@ __global__ void __launch_bounds__(256, GM == kOneGroup && P == 1 ? 3 : 2) gemm_k
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wr = w >> 1, wc = w & 1, c = lane & 31, q = lane >> 5;
+  const int wr = w / WC, wc = w % WC, c = lane & 31, q = lane >> 5;
 
   // which tile
   const int32_t row_tiles = p.tiles ? *p.n_tiles : p.row_tiles;
@@ -156,9 +157,10 @@ __global__ void __launch_bounds__(256, GM == kOneGroup && P == 1 ? 3 : 2) gemm_k
   // packed row of a local column
   auto packed_row = [&](int n) -> int64_t {
     if constexpr (EPI == kGatedRows) {
-      const int64_t h = (int64_t)ct * 64 + (n >> 6) * 32 + (n & 31);
+      constexpr int side = CB * 16;  // columns of a wave's gate, up's beside them
+      const int64_t h = (int64_t)ct * 64 + n / (2 * side) * side + n % side;
       const int64_t hc = h < p.width ? h : p.width - 1;
-      return (n & 32) ? p.width + hc : hc;
+      return (n & side) ? p.width + hc : hc;
     } else {
       const int64_t col = (int64_t)ct * kBN + n;
       return p.n0 + (col < p.n_cols ? col : p.n_cols - 1);
@@ -219,33 +221,33 @@ __global__ void __launch_bounds__(256, GM == kOneGroup && P == 1 ? 3 : 2) gemm_k
     }
   };
 
-  f32x16 out[RB][2], acc[RB][2];
+  f32x16 out[2][CB], acc[2][CB];
 #pragma unroll
-  for (int r = 0; r < RB; ++r)
+  for (int r = 0; r < 2; ++r)
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < CB; ++b) {
       out[r][b] = f32x16{};
       acc[r][b] = f32x16{};
     }
 
   // where this lane reads
-  int a_at[RB], a_turn[RB];
+  int a_at[2], a_turn[2];
 #pragma unroll
-  for (int r = 0; r < RB; ++r) {
-    const int row = wr * (BM / 2) + r * 32 + c;
+  for (int r = 0; r < 2; ++r) {
+    const int row = wr * 64 + r * 32 + c;
     a_at[r] = row * 128;
     a_turn[r] = (row >> 1) & 7;
   }
-  const int b_at = (wc * 64 + c) * 32 + q * 8;
+  const int b_at = (wc * CB * 32 + c) * 32 + q * 8;
 
   const Magic magic = Magic::make();
   auto fold = [&](const uint8_t* base, int g) {
-    const float* s = (const float*)(base + L::kA + L::kB) + g * kBN + wc * 64 + c;
+    const float* s = (const float*)(base + L::kA + L::kB) + g * kBN + wc * CB * 32 + c;
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
+    for (int b = 0; b < CB; ++b) {
       const float sc = s[b * 32];
 #pragma unroll
-      for (int r = 0; r < RB; ++r)
+      for (int r = 0; r < 2; ++r)
 #pragma unroll
         for (int i = 0; i < 16; ++i) out[r][b][i] = __builtin_fmaf(acc[r][b][i], sc, out[r][b][i]);
     }
@@ -255,32 +257,29 @@ __global__ void __launch_bounds__(256, GM == kOneGroup && P == 1 ? 3 : 2) gemm_k
     constexpr bool FIRST = decltype(first_step)::value;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint32_t words[2][2];
+      uint32_t words[CB][2];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
+      for (int b = 0; b < CB; ++b) {
         const u32x2 x = *(const u32x2*)(base + L::kA + b_at + b * 32 * 32 + h * 16);
         words[b][0] = x[0];
         words[b][1] = x[1];
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const h8 b0 = codes_of(words[0][j], magic), b1 = codes_of(words[1][j], magic);
+        h8 bo[CB];
 #pragma unroll
-        for (int r = 0; r < RB; ++r) {
+        for (int b = 0; b < CB; ++b) bo[b] = codes_of(words[b][j], magic);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
 #pragma unroll
           for (int pc = 0; pc < P; ++pc) {
             const int chunk = (h * 4 + q * 2 + j) ^ a_turn[r];
             const h8 a = *(const h8*)(base + pc * BM * 128 + a_at[r] + chunk * 16);
             const bool start = GM == kGroups32 ? j == 0 && pc == 0
                                                : GM == kGroups64 && FIRST && h == 0 && j == 0 && pc == 0;
-            if (start) {
-              const f32x16 o = {};
-              acc[r][0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b0, o, 0, 0, 0);
-              acc[r][1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b1, o, 0, 0, 0);
-            } else {
-              acc[r][0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b0, acc[r][0], 0, 0, 0);
-              acc[r][1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b1, acc[r][1], 0, 0, 0);
-            }
+#pragma unroll
+            for (int b = 0; b < CB; ++b)
+              acc[r][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, bo[b], start ? f32x16{} : acc[r][b], 0, 0, 0);
           }
         }
       }
@@ -288,7 +287,7 @@ __global__ void __launch_bounds__(256, GM == kOneGroup && P == 1 ? 3 : 2) gemm_k
     }
   };
   // a wave without rows (of a tile that is not full) loads for the others
-  const bool idle = wr * (BM / 2) >= rows;
+  const bool idle = wr * 64 >= rows;
   issue(0);
   if constexpr (S == 3) issue(1);
   auto begin = [&](int step) -> const uint8_t* {
@@ -322,19 +321,19 @@ __global__ void __launch_bounds__(256, GM == kOneGroup && P == 1 ? 3 : 2) gemm_k
   float scale0[2] = {1.0f, 1.0f};
   if constexpr (GM == kOneGroup) {
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
-      scale0[b] = p.w.scales[expert * p.w.expert_scales + packed_row(wc * 64 + b * 32 + c)];
+    for (int b = 0; b < CB; ++b)
+      scale0[b] = p.w.scales[expert * p.w.expert_scales + packed_row((wc * CB + b) * 32 + c)];
   }
 #pragma unroll
-  for (int r = 0; r < RB; ++r) {
-    const int r0 = wr * (BM / 2) + r * 32 + 4 * q;
-    float z[2][16];
+  for (int r = 0; r < 2; ++r) {
+    const int r0 = wr * 64 + r * 32 + 4 * q;
+    float z[CB][16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
       const int row = r0 + 8 * (i >> 2) + (i & 3);
       const int e = sh_exp[row];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
+      for (int b = 0; b < CB; ++b) {
         if constexpr (GM == kOneGroup)
           z[b][i] = __builtin_ldexpf(acc[r][b][i] * scale0[b], -e);
         else
@@ -342,23 +341,33 @@ __global__ void __launch_bounds__(256, GM == kOneGroup && P == 1 ? 3 : 2) gemm_k
       }
     }
     if constexpr (EPI == kGatedRows) {
-      const int64_t h = (int64_t)ct * 64 + wc * 32 + c;
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
+      auto put = [&](int i, float g, float u, int64_t h) {
         const int slot = sh_slot[r0 + 8 * (i >> 2) + (i & 3)];
-        if (slot < 0 || h >= p.width) continue;
-        const float g = z[0][i], u = z[1][i];
+        if (slot < 0 || h >= p.width) return;
         p.out[(int64_t)slot * p.out_ld + h] = g * sigmoid(g) * u;
         if (p.pre) {
           float* pre = p.pre + (int64_t)slot * 2 * p.width + h;
           pre[0] = g;
           pre[p.width] = u;
         }
+      };
+      if constexpr (CB == 2) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) put(i, z[0][i], z[1][i], (int64_t)ct * 64 + wc * 32 + c);
+      } else {
+        // lanes of the gate and of up change halves of their rows
+        const bool up = c & 16;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float other = __shfl_xor(up ? z[0][i] : z[0][i + 8], 16, 64);
+          const float mine = up ? z[0][i + 8] : z[0][i];
+          put(up ? i + 8 : i, up ? other : mine, up ? mine : other, (int64_t)ct * 64 + wc * 16 + (c & 15));
+        }
       }
     } else if constexpr (EPI == kPlainRows) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int64_t col = (int64_t)ct * kBN + wc * 64 + b * 32 + c;
+      for (int b = 0; b < CB; ++b) {
+        const int64_t col = (int64_t)ct * kBN + (wc * CB + b) * 32 + c;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int slot = sh_slot[r0 + 8 * (i >> 2) + (i & 3)];
@@ -366,19 +375,18 @@ __global__ void __launch_bounds__(256, GM == kOneGroup && P == 1 ? 3 : 2) gemm_k
         }
       }
     } else if constexpr (EPI == kHeadStats) {
-      const int col = wc * 64 + c;
-      const bool in0 = (int64_t)ct * kBN + col < p.n_cols, in1 = (int64_t)ct * kBN + col + 32 < p.n_cols;
       float m[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const int row = r0 + 8 * (i >> 2) + (i & 3), slot = sh_slot[row], t = sh_target[row];
-        if (slot >= 0) {
-          if (t == col) p.chosen[slot] = z[0][i];
-          if (t == col + 32) p.chosen[slot] = z[1][i];
+        m[i] = -__builtin_inff();
+#pragma unroll
+        for (int b = 0; b < CB; ++b) {
+          const int col = (wc * CB + b) * 32 + c;
+          if (slot >= 0 && t == col) p.chosen[slot] = z[b][i];
+          if ((int64_t)ct * kBN + col >= p.n_cols) z[b][i] = -__builtin_inff();
+          m[i] = b == 0 || z[b][i] > m[i] ? z[b][i] : m[i];
         }
-        if (!in0) z[0][i] = -__builtin_inff();
-        if (!in1) z[1][i] = -__builtin_inff();
-        m[i] = z[0][i] > z[1][i] ? z[0][i] : z[1][i];
       }
       // lane l of a half ends with row value l & 15's maximum, and hands it back
       const float mine = reduce16(m, lane, [](float x, float y) { return x > y ? x : y; });
@@ -387,21 +395,23 @@ __global__ void __launch_bounds__(256, GM == kOneGroup && P == 1 ? 3 : 2) gemm_k
       for (int i = 0; i < 16; ++i) {
         const float top = __shfl(mine, (lane & 48) | i, 64);
         const float base = top > -__builtin_inff() ? top : 0.0f;
-        s[i] = exp2_fast((z[0][i] - base) * kLog2e) + exp2_fast((z[1][i] - base) * kLog2e);
+        s[i] = 0.0f;
+#pragma unroll
+        for (int b = 0; b < CB; ++b) s[i] += exp2_fast((z[b][i] - base) * kLog2e);
       }
       const float sum = reduce16(s, lane, [](float x, float y) { return x + y; });
       if ((lane & 16) == 0) {
         const int i = lane & 15, row = r0 + 8 * (i >> 2) + (i & 3), slot = sh_slot[row];
         if (slot >= 0) {
-          float* st = p.stats + ((int64_t)slot * p.col_tiles + ct) * 4 + wc * 2;
+          float* st = p.stats + (((int64_t)slot * p.col_tiles + ct) * WC + wc) * 2;
           st[0] = mine;
           st[1] = sum;
         }
       }
     } else if constexpr (GM != kOneGroup) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int col = wc * 64 + b * 32 + c;
+      for (int b = 0; b < CB; ++b) {
+        const int col = (wc * CB + b) * 32 + c;
         if ((int64_t)ct * kBN + col >= p.n_cols) continue;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
@@ -417,8 +427,8 @@ __global__ void __launch_bounds__(256, GM == kOneGroup && P == 1 ? 3 : 2) gemm_k
       // to the tile's end
       const int s_exp = top_exponent(*p.s_bits);
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int col = wc * 64 + b * 32 + c;
+      for (int b = 0; b < CB; ++b) {
+        const int col = (wc * CB + b) * 32 + c;
         const float s = (int64_t)ct * kBN + col < p.n_cols ? __builtin_ldexpf(scale0[b], 15 - s_exp) : 0.0f;
         _Float16* to = p.d_parts + (int64_t)ct * kBN + (col & ~7) + operand_place(col & 7);
 #pragma unroll
