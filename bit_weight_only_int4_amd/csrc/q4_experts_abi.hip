@@ -110,10 +110,13 @@ struct ExpertsPlan {
 
 // Tiles of 128 rows unpack a word for twice the rows; tiles of 64 waste less
 // where an expert's rows end.  64 / 128, us: 32 experts of 2048 x 1408 in groups
-// of 128, 128 rows each, fp32 249 / 287, 192 332 / 341, 256 425 / 418, 512
-// 782 / 719; bf16 174 / 183, 234 / 248, 291 / 305, 511 / 519; 8 experts of
-// 4096 x 3584 in groups of 32, 384 rows, 800 / 734 and 541 / 495.
-int32_t gemm_tile_rows(int64_t n, int64_t experts) { return n >= 320 * experts ? 128 : 64; }
+// of 128, fp32, 128 rows each 249 / 287, 192 332 / 341, 256 425 / 418, 512
+// 782 / 719; one part, bf16, 256 283 / 308, 512 497 / 517, 1024 920 / 908; 8
+// experts of 4096 x 3584 in groups of 32, fp32, 384 rows 800 / 734; bf16 506 /
+// 550, 750 rows 893 / 877.
+int32_t gemm_tile_rows(int64_t n, int64_t experts, int32_t parts) {
+  return n >= (parts == 2 ? 320 : 640) * experts ? 128 : 64;
+}
 
 ExpertsPlan plan_experts(void* ws, int32_t dtype, int64_t T, int64_t H, int64_t W, int64_t E,
                          int64_t k) {
@@ -124,10 +127,10 @@ ExpertsPlan plan_experts(void* ws, int32_t dtype, int64_t T, int64_t H, int64_t 
   // While an expert has few rows on average the weights' bytes count, not the
   // products; a workgroup of the kernel for few rows has 16 rows, and deep ones
   // are dear to split in each of them.  fp32, few / tiles, us: 64 experts of
-  // 2048 x 1024, 8 rows each 80 / 127, 12 102 / 127, 16 124 / 130, 24 176 / 138
-  // (bf16 63 / 82, 76 / 83, 90 / 84, 119 / 92); 8 experts of 4096 x 3584, 4 rows
-  // 114 / 147, 6 135 / 146, 8 188 / 148 (bf16 105 / 128, 126 / 126, 145 / 129).
-  p.few = p.n <= (H <= 2048 && W <= 2048 ? 12 : 6) * E && H <= q4::kFewDepth && W <= q4::kFewDepth;
+  // 2048 x 1024, 8 rows each 82 / 140, 14 115 / 138, 16 124 / 130, 24 176 / 138
+  // (bf16 63 / 92, 78 / 94, 90 / 84, 119 / 92); 8 experts of 4096 x 3584, 4 rows
+  // 101 / 142, 8 157 / 152, 16 198 / 152 (bf16 93 / 117, 112 / 120, 185 / 130).
+  p.few = p.n <= (H <= 2048 && W <= 2048 ? 14 : 8) * E && H <= q4::kFewDepth && W <= q4::kFewDepth;
   // Few slots, mostly alone in their experts: each has workgroups, which look
   // for others of its expert, and the launch that lists the rows falls away.
   // Direct / listed, us: 64 experts, 8 slots 19.2 / 22.8, 32 37.9 / 40.2, 64
@@ -136,7 +139,7 @@ ExpertsPlan plan_experts(void* ws, int32_t dtype, int64_t T, int64_t H, int64_t 
   // (a token is in an expert's list once, as a rule: more tiles hold the others;
   // rows of more than 4096 share LDS by eight)
   const int64_t most = (H > 4096 || W > 4096 ? 8 : 16) / parts, few_rows = T < most ? T : most;
-  p.tile_rows = p.few ? (int32_t)few_rows : gemm_tile_rows(p.n, E);
+  p.tile_rows = p.few ? (int32_t)few_rows : gemm_tile_rows(p.n, E, parts);
   p.bound = p.n ? q4::tile_bound(p.n, E, p.tile_rows) : 0;
   p.h = c.take<float>(p.n * W);
   p.y = c.take<float>(p.n * H);
@@ -214,7 +217,8 @@ struct HeadPlan {
   int64_t rows;  // at a time
   int32_t tile_rows, parts;
   SplitRows xs;
-  float *stats, *chosen;  // forward
+  int32_t stat_parts;  // forward
+  float *stats, *chosen;
   // backward
   int64_t piece;  // of the vocabulary
   int32_t splits;
@@ -239,7 +243,8 @@ HeadPlan plan_head(void* ws, int32_t dtype, int64_t M, int64_t V, int64_t K, boo
   p.tile_rows = head_tile_rows(p.rows);
   p.xs = take_split(c, p.rows, K, p.parts);
   if (!back) {
-    p.stats = c.take<float>(p.rows * ((V + 127) / 128) * 2 * (p.tile_rows == 64 ? 4 : 2));
+    p.stat_parts = (int32_t)((V + 127) / 128) * (p.tile_rows == 64 && p.parts == 1 ? 4 : 2);  // a wave's each
+    p.stats = c.take<float>(p.rows * p.stat_parts * 2);
     p.chosen = c.take<float>(p.rows);
   } else {
     // A piece's gradient is to stay in the last-level cache between its two
@@ -580,7 +585,7 @@ q4_status q4_head_cross_entropy(const void* x, int64_t ldx, int32_t dtype, int64
     g.chosen = pl.chosen;
     g.targets = targets + m0;
     if (err == hipSuccess) err = q4::launch_gemm(g, pl.tile_rows, q4::kHeadStats, s);
-    q4::HeadFinish f{pl.stats, (pl.tile_rows == 64 ? 4 : 2) * g.col_tiles, pl.chosen, targets + m0, xs.rows, vocab, loss + m0,
+    q4::HeadFinish f{pl.stats, pl.stat_parts, pl.chosen, targets + m0, xs.rows, vocab, loss + m0,
                      lse + m0};
     if (err == hipSuccess) err = q4::launch_head_finish(f, s);
   }

@@ -4,7 +4,7 @@
 //   z[r, n] = sum_g s[g, n] * sum_{k in g} a[r, k] c[n, k]
 //
 // with the rows of an expert (or of the head) in tiles of BM and 128 columns,
-// four waves of 64 rows and BM/2 columns as 32x32x16 products.  A step is 64 k: rows of a and
+// four waves (WaveGrid) as 32x32x16 products.  A step is 64 k: rows of a and
 // packed words come by direct loads into LDS (chunks of 16 bytes of a turned by
 // row so that the reads meet no bank twice) in a ring of S stages, a barrier
 // each.  A wave unpacks the words it needs itself, two
@@ -40,6 +40,17 @@ struct GemmTile {
   static constexpr int kStages = GM != kOneGroup && 3 * kStage <= 76 * 1024 ? 3 : 2;
   // vector memory operations a wave issues per step
   static constexpr int kIssue = P * BM / 32 + 1 + (GM == kOneGroup ? 0 : 1);
+};
+
+// The four waves of a tile.  Of 64 rows in one part, each has all rows of 32
+// columns: a word is unpacked once, at the price of reading the rows from LDS by
+// four waves and not two.  With two parts LDS would bound it (32003 x 2048, 96
+// rows of fp32: 52 us so, 44 with waves of 32 rows by 64 columns).
+template <int P, int BM>
+struct WaveGrid {
+  static constexpr int WC = BM == 64 && P == 1 ? 4 : 2;  // waves side by side
+  static constexpr int CB = 4 / WC;                      // column blocks of 32 of a wave
+  static constexpr int RB = BM * WC / 128;               // and of rows
 };
 
 template <int N>
@@ -90,8 +101,8 @@ typedef Flag<false> No;
 template <int P, int BM, int GM, Epilogue EPI>
 __global__ void __launch_bounds__(256, GM == kOneGroup && P == 1 ? 3 : 2) gemm_kernel(const GemmParams p) {
   typedef GemmTile<P, BM, GM> L;
-  constexpr int CB = BM / 64;  // column blocks of a wave (and two of rows)
-  constexpr int WC = 4 / CB;   // waves side by side
+  typedef WaveGrid<P, BM> G;
+  constexpr int WC = G::WC, CB = G::CB, RB = G::RB;
   constexpr int S = L::kStages;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   __shared__ int32_t sh_slot[BM], sh_exp[BM];
@@ -221,9 +232,9 @@ __global__ void __launch_bounds__(256, GM == kOneGroup && P == 1 ? 3 : 2) gemm_k
     }
   };
 
-  f32x16 out[2][CB], acc[2][CB];
+  f32x16 out[RB][CB], acc[RB][CB];
 #pragma unroll
-  for (int r = 0; r < 2; ++r)
+  for (int r = 0; r < RB; ++r)
 #pragma unroll
     for (int b = 0; b < CB; ++b) {
       out[r][b] = f32x16{};
@@ -231,10 +242,10 @@ __global__ void __launch_bounds__(256, GM == kOneGroup && P == 1 ? 3 : 2) gemm_k
     }
 
   // where this lane reads
-  int a_at[2], a_turn[2];
+  int a_at[RB], a_turn[RB];
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int row = wr * 64 + r * 32 + c;
+  for (int r = 0; r < RB; ++r) {
+    const int row = (wr * RB + r) * 32 + c;
     a_at[r] = row * 128;
     a_turn[r] = (row >> 1) & 7;
   }
@@ -247,7 +258,7 @@ __global__ void __launch_bounds__(256, GM == kOneGroup && P == 1 ? 3 : 2) gemm_k
     for (int b = 0; b < CB; ++b) {
       const float sc = s[b * 32];
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
+      for (int r = 0; r < RB; ++r)
 #pragma unroll
         for (int i = 0; i < 16; ++i) out[r][b][i] = __builtin_fmaf(acc[r][b][i], sc, out[r][b][i]);
     }
@@ -270,7 +281,7 @@ __global__ void __launch_bounds__(256, GM == kOneGroup && P == 1 ? 3 : 2) gemm_k
 #pragma unroll
         for (int b = 0; b < CB; ++b) bo[b] = codes_of(words[b][j], magic);
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+        for (int r = 0; r < RB; ++r) {
 #pragma unroll
           for (int pc = 0; pc < P; ++pc) {
             const int chunk = (h * 4 + q * 2 + j) ^ a_turn[r];
@@ -287,7 +298,7 @@ __global__ void __launch_bounds__(256, GM == kOneGroup && P == 1 ? 3 : 2) gemm_k
     }
   };
   // a wave without rows (of a tile that is not full) loads for the others
-  const bool idle = wr * 64 >= rows;
+  const bool idle = wr * RB * 32 >= rows;
   issue(0);
   if constexpr (S == 3) issue(1);
   auto begin = [&](int step) -> const uint8_t* {
@@ -325,8 +336,8 @@ __global__ void __launch_bounds__(256, GM == kOneGroup && P == 1 ? 3 : 2) gemm_k
       scale0[b] = p.w.scales[expert * p.w.expert_scales + packed_row((wc * CB + b) * 32 + c)];
   }
 #pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int r0 = wr * 64 + r * 32 + 4 * q;
+  for (int r = 0; r < RB; ++r) {
+    const int r0 = (wr * RB + r) * 32 + 4 * q;
     float z[CB][16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
