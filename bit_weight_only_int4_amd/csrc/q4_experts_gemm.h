@@ -7,12 +7,16 @@
 // four waves (WaveGrid) as 32x32x16 products.  A step is 64 k: rows of a and
 // packed words come by direct loads into LDS (chunks of 16 bytes of a turned by
 // row so that the reads meet no bank twice) in a ring of S stages, a barrier
-// each.  A wave unpacks the words it needs itself, two
-// products' worth of columns per word read.  A group's products are summed by
-// MFMA and added to the result in fp32 times the column's scale; with a scale per row of the matrix there is
-// one group and one multiplication.
+// each.  A wave unpacks the words it needs itself.  A group's products are summed
+// by MFMA and added to the result in fp32 times the column's scale; with a scale
+// per row of the matrix there is one group and one multiplication.
 //
-// Bound: MFMA against the vector unit's unpacking (9 operations a word) and group sums (64 a group); see the table of measurements at launch_gemm.
+// Bound: MFMA against the vector unit's unpacking (9 operations a word) and group
+// sums (64 a group and wave).  Head of 128257 x 2048, a scale per row: 2048 rows
+// of bf16 1.08 ms, 1000 TFLOP/s; 512 of fp32 0.51 ms, twice 530 (a library
+// product of binary16, 8192^3, reaches 1324).  4099 tokens by 8 over 64 experts
+// of 2048 x 1024 in groups of 128, bf16: gate and up 350 us, 785 TFLOP/s, down
+// 215, 640, where an eighth of the tiles' rows are empty.
 #pragma once
 
 #include "q4_experts.h"

@@ -7,8 +7,9 @@
 // two experts (fp32 sums of 8192 tokens over 256 experts differ from the exact
 // order in a few places).  An integer of 0 is an expert that is not eligible.
 //
-// Bound by latency: 6 cross-lane steps a maximum, top_k of them one after the
-// other; tokens are independent, so many waves share a SIMD.
+// Bound by the vector unit's issue: top_k maxima of 6 cross-lane steps one after
+// the other, and with a bias exponentials in fp64.  8192 tokens, 8 of 256 experts
+// in 8 groups with a bias, 19 us; 32 tokens, 8 of 64, 4.3 (an empty launch 1.7).
 #include <hip/hip_runtime.h>
 
 #include "q4_experts.h"

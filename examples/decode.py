@@ -5,12 +5,14 @@ input.
 
     python examples/decode.py                # Llama-3.2-1B layer shapes, 4 layers
     python examples/decode.py --layers 16 --steps 64
+    python examples/decode.py --experts 32   # feed-forward parts of 32 experts, 4 for each token
 
 Weights are random (seeded); there is no tokenizer.  Per layer: a root-mean-
 square norm, the fused q/k/v projection (q4 linear), ``kv_append`` (keys and
 values into the paged cache, queries and keys turned on the way, the queries in
 place in the projection's rows), ``attention``, the output projection, and a
-gated feed-forward part; then the output head and ``token_logprobs``.
+gated feed-forward part, one for all tokens or ``route`` and ``experts``; then the
+output head and ``token_logprobs``, or its ``head_cross_entropy`` without logits.
 """
 import argparse
 import os
@@ -37,6 +39,9 @@ class Shape:
     group: int = 32
     page: int = 64
     rope_base: float = 500000.0
+    experts: int = 0  # 0: one feed-forward part for all tokens
+    top_k: int = 4
+    expert_ffn: int = 1024
 
 
 class Linear:
@@ -56,6 +61,30 @@ class Linear:
         return q4.linear_backward(dout, self.qw, self.scales, K=self.K, group_size=self.group)
 
 
+class Experts:
+    """A router and its experts' packed weights, matrix after matrix."""
+
+    def __init__(self, experts, top_k, hidden, ffn, group, gen, device):
+        self.top_k, self.group = top_k, group
+        self.router = (torch.randn((hidden, experts), generator=gen) / hidden ** 0.5).to(device)
+        up = [Linear(2 * ffn, hidden, group, gen, device) for _ in range(experts)]
+        down = [Linear(hidden, ffn, group, gen, device) for _ in range(experts)]
+        self.mats = [torch.stack([getattr(m, n) for m in of]) for of in (up, down) for n in ("qw", "scales")]
+
+    def __call__(self, x, trace=None):
+        logits = x @ self.router
+        r = q4.route(logits, self.top_k)
+        out, pre = q4.experts(x, r.ids, r.weights, *self.mats, group_size=self.group, keep=True)
+        if trace is not None:
+            trace.update(x=x, logits=logits, ids=r.ids, weights=r.weights, pre=pre, out=out)
+        return out
+
+    def backward(self, dout, logits, ids, weights, pre):
+        """The gradient of the rows (through the products and the router) from what the pass left."""
+        dx, dw = q4.experts_backward(dout, ids, weights, pre, *self.mats, group_size=self.group)
+        return dx + q4.route_backward(logits, ids, dw) @ self.router.t()
+
+
 def norm(x):
     return x * torch.rsqrt(x.square().mean(-1, keepdim=True) + 1e-5)
 
@@ -67,8 +96,9 @@ class Decoder:
         make = lambda n, k: Linear(n, k, s.group, gen, device)  # noqa: E731
         self.embed = torch.randn((s.vocab, s.hidden), generator=gen).to(device)
         self.layers = [dict(qkv=make((s.heads + 2 * s.kv_heads) * s.head_dim, s.hidden),
-                            out=make(s.hidden, s.heads * s.head_dim), up=make(2 * s.ffn, s.hidden),
-                            down=make(s.hidden, s.ffn),
+                            out=make(s.hidden, s.heads * s.head_dim),
+                            **(dict(experts=Experts(s.experts, s.top_k, s.hidden, s.expert_ffn, s.group, gen, device))
+                               if s.experts else dict(up=make(2 * s.ffn, s.hidden), down=make(s.hidden, s.ffn))),
                             cache=q4.new_cache(pages, s.kv_heads, s.head_dim, s.page, device))
                        for _ in range(s.layers)]
         self.head = Linear(s.vocab, s.hidden, 0, gen, device)
@@ -104,9 +134,14 @@ class Decoder:
             if trace is not None:
                 trace[-1].update(q=q.clone(), out=o, after=[c.clone() for c in layer["cache"]])
             x = x + layer["out"](o.view(len(tokens), -1))
-            gate, up = layer["up"](norm(x)).chunk(2, 1)
-            x = x + layer["down"](torch.nn.functional.silu(gate) * up)
+            x = x + self.feed(layer, norm(x))
         return norm(x)
+
+    def feed(self, layer, x):
+        if self.shape.experts:
+            return layer["experts"](x)
+        gate, up = layer["up"](x).chunk(2, 1)
+        return layer["down"](torch.nn.functional.silu(gate) * up)
 
     def logits(self, hidden):
         return self.head(hidden.contiguous())
@@ -143,13 +178,24 @@ def score(model, hidden, targets, entropy_weight=0.01):
     return r, model.head.backward(dlogits)
 
 
+def loss(model, hidden, targets):
+    """Mean cross entropy of the targets after their hidden states, and its
+    gradient, without the logits."""
+    head = (model.head.qw, model.head.scales, targets)
+    kw = dict(group_size=model.head.group)
+    r = q4.head_cross_entropy(hidden, *head, **kw)
+    g = torch.full_like(r.loss, 1.0 / len(targets))
+    return r.loss.mean(), q4.head_cross_entropy_backward(hidden, *head, r.lse, g, **kw)
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--layers", type=int, default=4)
     ap.add_argument("--steps", type=int, default=16)
     ap.add_argument("--prompts", type=int, nargs="+", default=[17, 300, 64, 129])
+    ap.add_argument("--experts", type=int, default=0)
     a = ap.parse_args()
-    shape = Shape(layers=a.layers)
+    shape = Shape(layers=a.layers, experts=a.experts)
     per = -(-(max(a.prompts) + a.steps + 1) // shape.page)
     model = Decoder(shape, pages=per * len(a.prompts), batch=len(a.prompts), max_pages=per)
     gen = torch.Generator().manual_seed(1)
@@ -167,6 +213,8 @@ def main():
     r, dx = score(model2, hidden, prompts[1][1:])
     print(f"prompt 1 scored: mean log probability {r.logprob.mean():.3f}, mean entropy {r.entropy.mean():.3f}, "
           f"gradient norm {dx.norm():.3e}")
+    mean, dh = loss(model2, hidden, prompts[1][1:])
+    print(f"the same without logits: mean loss {mean:.3f}, gradient norm {dh.norm():.3e}")
 
 
 if __name__ == "__main__":

@@ -11,8 +11,8 @@
  * Packed weights are those of q4_linear, contiguous, one matrix after the
  * other for experts: codes uint8 [E, N, K / 2] (4-byte aligned) and scales
  * float [E, ceil(K / group_size), N], or [E, N] when group_size is 0 (a scale
- * per row).  K is a multiple of 8; group_size is 0, 32 or a multiple of 64
- * (others: Q4_ERR_UNSUPPORTED).  A group_size >= K is one group.  Weights are
+ * per row).  K (hidden, width) is a multiple of 8 up to 32768; group_size is
+ * 0, 32 or a multiple of 64 (others: Q4_ERR_UNSUPPORTED).  A group_size >= K is one group.  Weights are
  * constants: gradients are those of the activations.
  *
  * Arithmetic: binary16 operands on MFMA with fp32 sums.  A weight's code is
@@ -21,7 +21,9 @@
  * magnitude overflows, and held as one binary16 number (16-bit types: bf16
  * and fp16 values are exact, values computed on the way are rounded to 11
  * bits) or as two (fp32: 22 bits), no finer than 2^-39 of its row's largest.
- * Infinities and NaN of a row reach no other row.
+ * Infinities and NaN of a row reach no other row; an infinite element makes
+ * its row's results infinite or NaN.  A workspace may serve any number of
+ * calls one after the other, from captured graphs too, but no two at once.
  */
 #ifndef Q4EXPERTS_H
 #define Q4EXPERTS_H
@@ -101,7 +103,8 @@ q4_status q4_route_backward(const void *logits, int64_t ld, int32_t dtype,
  *            left as they are)
  *   workspace  q4_experts_workspace_bytes(...) bytes, 16-byte aligned
  * The sum over slots is in slot order.  experts <= 1024, top_k <= 32,
- * T * top_k < 2^24.
+ * T * top_k < 2^24; a call of more than 2^23 tiles (64 rows by 128 columns of
+ * hidden or 2 * width) is refused.
  */
 q4_status q4_experts(const void *x, int64_t ldx, int32_t dtype, int64_t T,
                      int64_t hidden, int64_t width, int64_t experts,

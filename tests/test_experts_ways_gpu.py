@@ -8,6 +8,8 @@ import torch
 import bit_weight_only_int4_amd as q4
 from oracle import experts_oracle as oracle
 from tests.experts_util import HALF_STEP, TORCH, assert_within, expert_bounds, expert_grad_bounds, packed, rounded
+from tests.test_experts_gpu import Layer
+from tests.test_experts_gpu import check as check_layer
 
 pytestmark = pytest.mark.gpu
 
@@ -185,3 +187,38 @@ def test_steps_at_once_and_captured(M):
         torch.cuda.synchronize()
         for got, w in zip(held, want):
             assert all(torch.equal(a, b) for a, b in zip(got, w))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,k", [(1, 1), (1, 6), (3, 2), (11, 4)])
+def test_few_slots_of_many_experts(T, k, dtype):
+    """Slots that look for their expert's other rows themselves: spread, all of
+    one expert, one expert several times in a token, empty ones."""
+    layer = Layer(48, 264, 72, 32)
+    ids = np.random.default_rng(T).integers(0, 48, (T, k)).astype(np.int32)
+    check_layer(layer, T, k, dtype, ids=ids)
+    check_layer(layer, T, k, dtype, ids=np.full((T, k), 47, dtype=np.int32))
+    check_layer(layer, T, k, dtype, ids=(ids % 2).astype(np.int32))
+    check_layer(layer, T, k, dtype, empty=0.6)
+    check_layer(layer, T, k, dtype, ids=np.full((T, k), -1, dtype=np.int32), layout="wide")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_few_slots_with_bad_ids_and_rows(dtype):
+    layer = Layer(40, 264, 72, 64)
+    ids, w = layer.slots(6, 3, 0)
+    x = torch.randn(6, 264).to(TORCH[dtype]).cuda()
+    it, wt = torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda()
+    it[3] = it[0]
+    good, pre = q4.experts(x, it, wt, *layer.dev, **layer.kw, keep=True)
+    order = torch.tensor([4, 0, 5, 2, 1, 3]).cuda()
+    again, pre2 = q4.experts(x[order], it[order], wt[order], *layer.dev, **layer.kw, keep=True)
+    assert torch.equal(again, good[order]) and torch.equal(pre2, pre[order])
+    rest = torch.arange(6) != 1
+    it2, x2 = it.clone(), x.clone()
+    it2[1, 2] = 40
+    assert torch.equal(q4.experts(x, it2, wt, *layer.dev, **layer.kw)[rest], good[rest])
+    assert q4.experts(x, it2, wt, *layer.dev, **layer.kw)[1].isnan().all()
+    x2[1, 100] = float("inf")
+    bad = q4.experts(x2, it, wt, *layer.dev, **layer.kw)
+    assert torch.equal(bad[rest], good[rest]) and not torch.isfinite(bad[1]).any()
