@@ -396,9 +396,15 @@ hipError_t few_blocks(const FewParams& p, int32_t tile_rows, hipStream_t s) {
   const int64_t tiles = p.tiles ? p.row_tiles : p.n;
   const int64_t busy = p.tiles ? tiles : (p.n < p.experts ? p.n : p.experts);
   const int nw = p.w.K <= 4 * kHold * kChunk ? 4 : p.w.K <= 8 * kHold * kChunk ? 8 : 16;
-  // four column blocks of a workgroup where that leaves four workgroups for every CU
+  // Four column blocks share a workgroup's rows, which pays where there are
+  // many workgroups, or several rows to split.  One / four blocks, us (fp32; bf16
+  // alike): 64 experts of 2048 x 1024, 4 tokens by 8 35.6 / 31.4, 16 81 / 57, 48
+  // 128 / 70, 96 215 / 104; 16 of 2048 x 1408, 4 tokens by 2 17.8 / 19.8, 32
+  // 46 / 33; 8 of 4096 x 3584, 4 tokens by 2 38 / 52, 16 104 / 71; 4 of 2144 x
+  // 384, 12 tokens by 2 21.6 / 26.3.
   const bool even = p.w.K % 32 == 0;
-  const int cg = even && nw < 16 && cols * busy >= 4 * 4 * 256 ? 4 : 1;
+  const int64_t enough = p.n >= 2 * p.experts ? 1024 : 2048;
+  const int cg = even && nw < 16 && cols * busy >= enough ? 4 : 1;
   FewShape f;
   f.col_groups = (int32_t)((cols + cg - 1) / cg);
   f.xcd_groups = (f.col_groups + 7) / 8;
