@@ -61,6 +61,8 @@ q4_status group_status(int64_t gs, int64_t K) {
   return gs == 0 || gs >= K || gs == 32 || gs % 64 == 0 ? Q4_OK : Q4_ERR_UNSUPPORTED;
 }
 
+bool one_group(int64_t gs, int64_t K) { return gs == 0 || gs >= K; }
+
 // Pieces of a workspace, each 256-byte aligned within it.
 struct Carve {
   uint8_t* base;
@@ -235,7 +237,8 @@ int32_t head_tile_rows(int64_t rows) {
   return rows > 320 || (rows > 192 && rows <= 256) ? 128 : 64;
 }
 
-HeadPlan plan_head(void* ws, int32_t dtype, int64_t M, int64_t V, int64_t K, bool back) {
+HeadPlan plan_head(void* ws, int32_t dtype, int64_t M, int64_t V, int64_t K, bool one_scale,
+                   bool back) {
   HeadPlan p{};
   Carve c(ws);
   p.rows = M < kHeadRows ? M : kHeadRows;
@@ -254,12 +257,21 @@ HeadPlan plan_head(void* ws, int32_t dtype, int64_t M, int64_t V, int64_t K, boo
     const int64_t pieces = (V + (most > 1024 ? most : 1024) - 1) / (most > 1024 ? most : 1024);
     p.piece = ((V + pieces - 1) / pieces + 127) / 128 * 128;
     const int64_t tiles = (p.rows + p.tile_rows - 1) / p.tile_rows * ((K + 127) / 128);
-    // Two workgroups for every CU; each split at least 8 steps deep.  333 rows,
-    // 32003 x 2048, bf16: one split 491 us, a workgroup a CU 173, two 153, four
-    // 148 (fp32 785, 282, 241, 249).
-    int64_t splits = 512 / tiles;
-    if (splits > p.piece / 512) splits = p.piece / 512;
-    p.splits = (int32_t)(splits < 1 ? 1 : splits > 16 ? 16 : splits);
+    // Splits of a piece, at least 8 steps deep, so that rounds of the workgroups
+    // that fit the card (three a CU in one part with a scale per row, else two)
+    // come out even, at a hundredth each for their sums.  Backward of 32003 x 4096
+    // and 700 rows, 192 tiles, fp32, 2, 4, 5, 8, 10 splits 830, 788, 772, 764, 803
+    // us; 128257 x 2048, 2048 rows, 256 tiles, bf16, 1, 2, 3, 4, 6, 8 splits 2967,
+    // 2515, 2464, 2551, 2575, 2683.
+    const int64_t fit = 256 * (one_scale && p.parts == 1 ? 3 : 2);
+    double least = 0.0;
+    for (int64_t n = 1; n <= 16 && (n == 1 || n <= p.piece / 512); ++n) {
+      const double cost = (double)((tiles * n + fit - 1) / fit) / (double)n * (1.0 + 0.01 * (double)n);
+      if (n == 1 || cost < least) {
+        p.splits = (int32_t)n;
+        least = cost;
+      }
+    }
     p.d = c.take<float>(p.rows * p.piece);
     p.acc = c.take<float>(p.splits * p.rows * K);
     p.g_bits = c.take<uint32_t>(p.rows);
@@ -542,7 +554,7 @@ q4_status q4_experts_backward(const void* dout, int64_t lddo, int32_t dtype, int
 size_t q4_head_cross_entropy_workspace_bytes(int32_t dtype, int64_t M, int64_t vocab, int64_t K,
                                              int64_t group_size) {
   if (!head_sizes_ok(dtype, M, vocab, K) || M == 0 || group_status(group_size, K) != Q4_OK) return 0;
-  return plan_head(nullptr, dtype, M, vocab, K, false).bytes;
+  return plan_head(nullptr, dtype, M, vocab, K, one_group(group_size, K), false).bytes;
 }
 
 q4_status q4_head_cross_entropy(const void* x, int64_t ldx, int32_t dtype, int64_t M,
@@ -560,7 +572,7 @@ q4_status q4_head_cross_entropy(const void* x, int64_t ldx, int32_t dtype, int64
       !aligned(scales, 4) || !aligned(targets, 8) || !aligned(loss, 4) || !aligned(lse, 4))
     return Q4_ERR_INVALID_ARG;
   const Packed w = q4::packed(qw, scales, vocab, K, group_size);
-  const HeadPlan pl = plan_head(workspace, dtype, M, vocab, K, false);
+  const HeadPlan pl = plan_head(workspace, dtype, M, vocab, K, one_group(group_size, K), false);
   if (!workspace || workspace_bytes < pl.bytes || !aligned(workspace, 16)) return Q4_ERR_WORKSPACE;
   const Range outs[] = {flat(loss, M, 4), flat(lse, M, 4), flat(workspace, (int64_t)pl.bytes, 1)};
   const Range ins[] = {span(x, M, ldx, K, e), flat(qw, w.expert_bytes, 1),
@@ -595,7 +607,7 @@ q4_status q4_head_cross_entropy(const void* x, int64_t ldx, int32_t dtype, int64
 size_t q4_head_cross_entropy_backward_workspace_bytes(int32_t dtype, int64_t M, int64_t vocab,
                                                       int64_t K, int64_t group_size) {
   if (!head_sizes_ok(dtype, M, vocab, K) || M == 0 || group_status(group_size, K) != Q4_OK) return 0;
-  return plan_head(nullptr, dtype, M, vocab, K, true).bytes;
+  return plan_head(nullptr, dtype, M, vocab, K, one_group(group_size, K), true).bytes;
 }
 
 q4_status q4_head_cross_entropy_backward(const void* x, int64_t ldx, int32_t dtype, int64_t M,
@@ -617,7 +629,7 @@ q4_status q4_head_cross_entropy_backward(const void* x, int64_t ldx, int32_t dty
       !aligned(lse, 4) || !aligned(g_loss, 4))
     return Q4_ERR_INVALID_ARG;
   const Packed w = q4::packed(qw, scales, vocab, K, group_size);
-  const HeadPlan pl = plan_head(workspace, dtype, M, vocab, K, true);
+  const HeadPlan pl = plan_head(workspace, dtype, M, vocab, K, one_group(group_size, K), true);
   if (!workspace || workspace_bytes < pl.bytes || !aligned(workspace, 16)) return Q4_ERR_WORKSPACE;
   const Range outs[] = {span(dx, M, lddx, K, e), flat(workspace, (int64_t)pl.bytes, 1)};
   const Range ins[] = {span(x, M, ldx, K, e), flat(qw, w.expert_bytes, 1),
