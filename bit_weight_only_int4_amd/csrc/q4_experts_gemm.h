@@ -59,7 +59,8 @@ struct WaveGrid {
 
 template <int N>
 __device__ __forceinline__ void wait_loads() {
-  // vmcnt(N), other counters left free
+  // vmcnt(N), other counters left free; no load moves past it
+  asm volatile("" ::: "memory");
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
 
