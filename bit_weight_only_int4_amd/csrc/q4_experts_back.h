@@ -22,7 +22,7 @@
 // Bound: the vector unit, which forms the row operand anew for every tile of
 // columns (6 operations an element in two parts, 4 in one) beside the codes'.
 // 2048 tokens by 4 over 32 experts of 2048 x 1408 in groups of 128, bf16:
-// through down 235 us (two parts), through gate and up 210 (one), 200 and 450
+// through down 235 us (two parts), through gate and up 206 (one), 200 and 460
 // TFLOP/s.
 #pragma once
 

@@ -13,10 +13,10 @@
 //
 // Bound: MFMA against the vector unit's unpacking (9 operations a word) and group
 // sums (64 a group and wave).  Head of 128257 x 2048, a scale per row: 2048 rows
-// of bf16 1.08 ms, 1000 TFLOP/s; 512 of fp32 0.51 ms, twice 530 (a library
+// of bf16 1.07 ms, 1000 TFLOP/s; 512 of fp32 0.51 ms, twice 530 (a library
 // product of binary16, 8192^3, reaches 1324).  4099 tokens by 8 over 64 experts
-// of 2048 x 1024 in groups of 128, bf16: gate and up 350 us, 785 TFLOP/s, down
-// 215, 640, where an eighth of the tiles' rows are empty.
+// of 2048 x 1024 in groups of 128, bf16: gate and up 374 us, 735 TFLOP/s, down
+// 230, 600, where an eighth of the tiles' rows are empty.
 #pragma once
 
 #include "q4_experts.h"
