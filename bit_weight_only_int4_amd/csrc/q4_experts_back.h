@@ -14,7 +14,8 @@
 // of four rows n, turns its 4 x 8 nibbles around in registers (12 operations)
 // and writes 16 bits for each k, so LDS holds the tile packed along n and a
 // wave unpacks it as the forward product does.  Within each 32 columns the order
-// is (k % 4 word, k in word) so that the writes spread over the banks.
+// is (k in word, word % 4), and pieces of 8 bytes are turned, so that writes and
+// reads spread over the banks.
 //
 // Tiles of BM rows by 128 columns, four waves of 64 rows by BM/2 columns; the
 // next two steps' loads are in registers while a step's products run.
@@ -54,6 +55,33 @@ __device__ __forceinline__ void turn_words(const uint32_t (&w)[4], uint32_t (&t)
   t[1] = __builtin_amdgcn_perm(o23, o01, 0x06020400u);  // 1, 5
   t[2] = __builtin_amdgcn_perm(e23, e01, 0x07030501u);  // 2, 6
   t[3] = __builtin_amdgcn_perm(o23, o01, 0x07030501u);  // 3, 7
+}
+
+// Where 8 bytes of a column's codes lie (of NS / 16 such pieces): turned by the
+// column's eighth of 32 and by its 32, so that reads of 16 lanes and writes of 64
+// meet no bank twice.
+template <int NS>
+__device__ __forceinline__ int turned(int piece, int eighth, int block) {
+  return piece ^ ((eighth ^ block) & (NS / 16 - 1));
+}
+// A word (8 k) of rows n .. n + 3 into LDS: word kw of 16, rows' place u of NS /
+// 4.  Element i is column (kw / 4) * 32 + kw % 4 + 4 i, in the eighth i / 2 (the
+// words' low element second if flip).
+template <int NS>
+__device__ __forceinline__ void store_turned(uint8_t* b, const uint32_t (&w)[4], int kw, int u, bool flip) {
+  uint32_t t[4];
+  turn_words(w, t);
+  const uint32_t e[4] = {flip ? t[1] : t[0], flip ? t[0] : t[1], flip ? t[3] : t[2], flip ? t[2] : t[3]};
+  const int at = ((kw >> 2) * 32 + (kw & 3)) * (NS / 2) + turned<NS>(u >> 2, 0, kw >> 2) * 8 + (u & 3) * 2;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    uint8_t *lo = b + (at ^ turned<NS>(0, j, 0) * 8), *hi = b + (at ^ turned<NS>(0, j + 2, 0) * 8);
+#pragma unroll
+    for (int i = 2 * j; i < 2 * j + 2; ++i) {
+      *(uint16_t*)(lo + i * 4 * (NS / 2)) = (uint16_t)e[i];
+      *(uint16_t*)(hi + (i + 4) * 4 * (NS / 2)) = (uint16_t)(e[i] >> 16);
+    }
+  }
 }
 
 template <int P, typename T, int BM, int NG, bool GATE>
@@ -223,18 +251,7 @@ __global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
         if constexpr (P == 2) *(h8*)(dst + L::kPart) = lo;
       }
     }
-    if (codes_mine) {
-      uint32_t t[4];
-      turn_words(f.w, t);
-      // n word u / 2, half u % 2, of column (kw, k in word)
-      uint8_t* dst = base + L::kA + ((kw >> 2) * 32 + (kw & 3)) * (NS / 2) + (u >> 1) * 4 + (u & 1) * 2;
-      const int flip = p.nibble_order == Q4_ORDER_LOW_FIRST ? 0 : 1;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        *(uint16_t*)(dst + (i ^ flip) * 4 * (NS / 2)) = (uint16_t)t[i];
-        *(uint16_t*)(dst + ((i + 4) ^ flip) * 4 * (NS / 2)) = (uint16_t)(t[i] >> 16);
-      }
-    }
+    if (codes_mine) store_turned<NS>(base + L::kA, f.w, kw, u, p.nibble_order != Q4_ORDER_LOW_FIRST);
   };
 
   f32x16 acc[2][CB];
@@ -250,7 +267,7 @@ __global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
       uint32_t words[CB][2];
 #pragma unroll
       for (int b = 0; b < CB; ++b) {
-        const u32x2 x = *(const u32x2*)(base + L::kA + ((wc * CB + b) * 32 + c) * (NS / 2) + h * 16 + q * 8);
+        const u32x2 x = *(const u32x2*)(base + L::kA + ((wc * CB + b) * 32 + c) * (NS / 2) + turned<NS>(h * 2 + q, c >> 3, wc * CB + b) * 8);
         words[b][0] = x[0];
         words[b][1] = x[1];
       }
@@ -447,16 +464,8 @@ __global__ void __launch_bounds__(256, 2) back_direct_kernel(const BackParams p)
       }
     }
   };
-  const int flip = p.nibble_order == Q4_ORDER_LOW_FIRST ? 0 : 1;
   auto store = [&](const Words& f, int step) {
-    uint32_t t[4];
-    turn_words(f.w, t);
-    uint8_t* dst = smem + 2 * L::kA + (step & 1) * L::kB + ((kw >> 2) * 32 + (kw & 3)) * 32 + (u >> 1) * 4 + (u & 1) * 2;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      *(uint16_t*)(dst + (i ^ flip) * 4 * 32) = (uint16_t)t[i];
-      *(uint16_t*)(dst + ((i + 4) ^ flip) * 4 * 32) = (uint16_t)(t[i] >> 16);
-    }
+    store_turned<kBK>(smem + 2 * L::kA + (step & 1) * L::kB, f.w, kw, u, p.nibble_order != Q4_ORDER_LOW_FIRST);
   };
 
   f32x16 acc[RB][2];
@@ -472,7 +481,7 @@ __global__ void __launch_bounds__(256, 2) back_direct_kernel(const BackParams p)
       uint32_t words[2][2];
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
-        const u32x2 x = *(const u32x2*)(b_base + (wc * 64 + b * 32 + c) * 32 + h * 16 + q * 8);
+        const u32x2 x = *(const u32x2*)(b_base + (wc * 64 + b * 32 + c) * 32 + turned<kBK>(h * 2 + q, c >> 3, wc * 2 + b) * 8);
         words[b][0] = x[0];
         words[b][1] = x[1];
       }
