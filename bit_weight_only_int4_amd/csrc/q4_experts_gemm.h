@@ -191,7 +191,9 @@ __global__ void __launch_bounds__(256, GM == kOneGroup && P == 1 ? 3 : 2) gemm_k
 #pragma unroll
   for (int i = 0; i < 4; ++i)
     bsrc[i] = bbase + packed_row(wide ? tid >> 1 : w * 32 + i * 8 + (lane >> 3)) * ldq;
-  const int b_byte = wide ? (tid & 1) * 16 : (lane & 7) * 4;  // within a step of a row
+  // (within a step of a row; its halves change places by the row's eighth, so that
+  // the reads of 16 lanes meet no bank twice)
+  const int b_byte = wide ? ((tid ^ (tid >> 4)) & 1) * 16 : (lane & 7) * 4;
   // scales of a step's groups, 4 bytes a lane
   const float* ssrc = nullptr;
   int sslot = 0, sgroup = 0;
@@ -224,15 +226,17 @@ __global__ void __launch_bounds__(256, GM == kOneGroup && P == 1 ? 3 : 2) gemm_k
                                        (lds_vptr)(base + L::kA + L::kB + sslot * 4), 4, 0, 0);
     }
     // words past K are other rows' (here the row's first): activations are 0 there
-    const int64_t byte = (int64_t)st * (kBK / 2) + b_byte;
-    const int64_t from = byte < ldq ? byte : 0;
+    auto from = [&](int at) {
+      const int64_t byte = (int64_t)st * (kBK / 2) + at;
+      return byte < ldq ? byte : 0;
+    };
     if (wide) {
-      __builtin_amdgcn_global_load_lds((global_cptr)(bsrc[0] + from),
+      __builtin_amdgcn_global_load_lds((global_cptr)(bsrc[0] + from(b_byte)),
                                        (lds_vptr)(base + L::kA + w * 1024), 16, 0, 0);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        __builtin_amdgcn_global_load_lds((global_cptr)(bsrc[i] + from),
+        __builtin_amdgcn_global_load_lds((global_cptr)(bsrc[i] + from(b_byte ^ (i & 1) * 16)),
                                          (lds_vptr)(base + L::kA + w * 1024 + i * 256), 4, 0, 0);
     }
   };
@@ -254,7 +258,7 @@ __global__ void __launch_bounds__(256, GM == kOneGroup && P == 1 ? 3 : 2) gemm_k
     a_at[r] = row * 128;
     a_turn[r] = (row >> 1) & 7;
   }
-  const int b_at = (wc * CB * 32 + c) * 32 + q * 8;
+  const int b_at = (wc * CB * 32 + c) * 32 + (c >> 3 & 1) * 16 + q * 8;
 
   const Magic magic = Magic::make();
   auto fold = [&](const uint8_t* base, int g) {
@@ -276,7 +280,7 @@ __global__ void __launch_bounds__(256, GM == kOneGroup && P == 1 ? 3 : 2) gemm_k
       uint32_t words[CB][2];
 #pragma unroll
       for (int b = 0; b < CB; ++b) {
-        const u32x2 x = *(const u32x2*)(base + L::kA + b_at + b * 32 * 32 + h * 16);
+        const u32x2 x = *(const u32x2*)(base + L::kA + (b_at ^ h * 16) + b * 32 * 32);
         words[b][0] = x[0];
         words[b][1] = x[1];
       }
