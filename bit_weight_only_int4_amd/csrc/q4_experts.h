@@ -116,13 +116,13 @@ struct GemmParams {
 };
 hipError_t launch_gemm(const GemmParams& p, int32_t tile_rows, Epilogue epi, hipStream_t s);
 
-// Few rows per expert: up to 16 rows of binary16 operands a tile, weights
-// straight from memory into the matrix operands.
+// Few rows per expert: up to 8 a tile, weights straight from memory into the
+// matrix operands.
 struct FewParams {
   Packed w;
   const void* x;          // rows of dtype
   int64_t ldx;
-  int32_t dtype, parts;
+  int32_t dtype;
   int32_t nibble_order;
   const int32_t* ids;     // direct: tiles are found from the n ids by each workgroup
   int32_t n, experts;

@@ -113,12 +113,10 @@ struct ExpertsPlan {
 // Tiles of 128 rows unpack a word for twice the rows; tiles of 64 waste less
 // where an expert's rows end.  64 / 128, us: 32 experts of 2048 x 1408 in groups
 // of 128, fp32, 128 rows each 249 / 287, 192 332 / 341, 256 425 / 418, 512
-// 782 / 719; one part, bf16, 256 283 / 308, 512 497 / 517, 1024 920 / 908; 8
-// experts of 4096 x 3584 in groups of 32, fp32, 384 rows 800 / 734; bf16 506 /
-// 550, 750 rows 893 / 877.
-int32_t gemm_tile_rows(int64_t n, int64_t experts, int32_t parts) {
-  return n >= (parts == 2 ? 320 : 640) * experts ? 128 : 64;
-}
+// 782 / 719; bf16, 128 212 / 226, 256 342 / 325, 512 608 / 558, 1024 1123 /
+// 1017; 8 experts of 4096 x 3584 in groups of 32, fp32, 384 rows 800 / 734;
+// bf16, 200 371 / 343, 400 623 / 591.
+int32_t gemm_tile_rows(int64_t n, int64_t experts) { return n >= 256 * experts ? 128 : 64; }
 
 ExpertsPlan plan_experts(void* ws, int32_t dtype, int64_t T, int64_t H, int64_t W, int64_t E,
                          int64_t k) {
@@ -127,28 +125,30 @@ ExpertsPlan plan_experts(void* ws, int32_t dtype, int64_t T, int64_t H, int64_t 
   p.n = T * k;
   const int32_t parts = parts_of(dtype);
   // While an expert has few rows on average the weights' bytes count, not the
-  // products; a workgroup of the kernel for few rows has 16 rows, and deep ones
-  // are dear to split in each of them.  fp32, few / tiles, us: 64 experts of
-  // 2048 x 1024, 8 rows each 82 / 140, 14 115 / 138, 16 124 / 130, 24 176 / 138
-  // (bf16 63 / 92, 78 / 94, 90 / 84, 119 / 92); 8 experts of 4096 x 3584, 4 rows
-  // 101 / 142, 8 157 / 152, 16 198 / 152 (bf16 93 / 117, 112 / 120, 185 / 130).
+  // products; a workgroup of the kernel for few rows has 8 rows, and deep ones
+  // are dear to split in each of them.  Few / tiles, us: 64 experts of 2048 x
+  // 1024, fp32, 8 rows each 81 / 126, 14 116 / 128, 16 128 / 129, 24 175 / 136;
+  // bf16 82 / 105, 109 / 105, 120 / 105, 166 / 108; 8 experts of 4096 x 3584,
+  // fp32, 4 rows 73 / 147, 8 110 / 146, 16 166 / 147; bf16 61 / 127, 91 / 128,
+  // 132 / 129.
   p.few = p.n <= (H <= 2048 && W <= 2048 ? 14 : 8) * E && H <= q4::kFewDepth && W <= q4::kFewDepth;
   // Few slots, mostly alone in their experts: each has workgroups, which look
   // for others of its expert, and the launch that lists the rows falls away.
   // Direct / listed, us: 64 experts, 8 slots 19.2 / 22.8, 32 37.9 / 40.2, 64
   // 55.7 / 54.1; 16 experts, 14 slots 40.8 / 42.0, 64 101 / 86.
   p.direct = p.few && p.n <= q4::kFewDirect && p.n <= E;
-  // (a token is in an expert's list once, as a rule: more tiles hold the others;
-  // rows of more than 4096 share LDS by eight)
-  const int64_t most = (H > 4096 || W > 4096 ? 8 : 16) / parts, few_rows = T < most ? T : most;
-  p.tile_rows = p.few ? (int32_t)few_rows : gemm_tile_rows(p.n, E, parts);
+  // 8 rows in two parts fill the second product's operands, and rows of more than
+  // 4096 share LDS by four (a token is in an expert's list once, as a rule: more
+  // tiles hold the others)
+  const int64_t most = H > 4096 || W > 4096 ? 4 : 8, few_rows = T < most ? T : most;
+  p.tile_rows = p.few ? (int32_t)few_rows : gemm_tile_rows(p.n, E);
   p.bound = p.n ? q4::tile_bound(p.n, E, p.tile_rows) : 0;
   p.h = c.take<float>(p.n * W);
   p.y = c.take<float>(p.n * H);
   if (!p.direct) p.lists = take_lists(c, p.n, E, p.tile_rows);
   if (!p.few) {
     p.xs = take_split(c, T, H, parts);
-    p.hs = take_split(c, p.n, W, parts);
+    p.hs = take_split(c, p.n, W, 2);  // of fp32 values
   }
   p.bytes = c.at;
   return p;
@@ -388,7 +388,6 @@ q4_status q4_experts(const void* x, int64_t ldx, int32_t dtype, int64_t T, int64
   if (pl.few) {
     q4::FewParams f{};
     f.nibble_order = nibble_order;
-    f.parts = parts_of(dtype);
     f.n = (int32_t)n;
     f.experts = (int32_t)experts;
     if (pl.direct) {

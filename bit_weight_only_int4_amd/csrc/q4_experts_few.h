@@ -3,9 +3,9 @@
 //
 //   z[r, n] = sum_g s[g, n] * sum_{k in g} x[r, k] c[n, k]
 //
-// A workgroup owns an expert's next rows, up to 16 rows of binary16 operands
-// (16 of a 16-bit type; 8 of fp32, whose second parts are rows 8 .. 15 of the
-// same products), and CG blocks of 32 of its columns: for the gated half 16
+// A workgroup owns an expert's next rows, up to 8 (of fp32, in two binary16
+// parts, the second parts are rows 8 .. 15 of the same products; the second half
+// reads fp32 whatever the type, so both halves take 8), and CG blocks of 32 of its columns: for the gated half 16
 // columns of the gate and the 16 of up beside them.  The depth is divided
 // between NW waves (4, 8 or 16), up to four chunks of 128 k for each: a wave
 // splits the rows' elements there into binary16 parts, in LDS, scaled by what

@@ -9,7 +9,6 @@ Q4_FEW(2, float, true)
 Q4_FEW(1, _Float16, true)
 Q4_FEW(1, bf16, true)
 Q4_FEW(2, float, false)
-Q4_FEW(1, float, false)
 #undef Q4_FEW
 
 hipError_t launch_few(const FewParams& p, int32_t tile_rows, bool gated, hipStream_t s) {
@@ -21,8 +20,7 @@ hipError_t launch_few(const FewParams& p, int32_t tile_rows, bool gated, hipStre
     }
   }
   // the gated rows are fp32
-  return p.parts == 2 ? few_scales<2, float, false>(p, tile_rows, s)
-                      : few_scales<1, float, false>(p, tile_rows, s);
+  return few_scales<2, float, false>(p, tile_rows, s);
 }
 
 }  // namespace q4

@@ -4,6 +4,4 @@
 namespace q4 {
 template hipError_t launch_gemm_tile<1, 64, kGatedRows>(const GemmParams&, hipStream_t);
 template hipError_t launch_gemm_tile<1, 128, kGatedRows>(const GemmParams&, hipStream_t);
-template hipError_t launch_gemm_tile<1, 64, kPlainRows>(const GemmParams&, hipStream_t);
-template hipError_t launch_gemm_tile<1, 128, kPlainRows>(const GemmParams&, hipStream_t);
 }  // namespace q4
