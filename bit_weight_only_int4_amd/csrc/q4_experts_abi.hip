@@ -163,7 +163,7 @@ bool experts_grid_ok(const ExpertsPlan& p, int64_t H, int64_t W) {
 // ---- and backward -----------------------------------------------------------------
 
 struct ExpertsBackPlan {
-  int32_t tile_rows, parts;
+  int32_t tile_rows;
   int64_t n, bound, width_tiles, hidden_tiles;
   RowLists lists;
   uint32_t *dout_bits, *dpre_bits, *s_bits;
@@ -171,24 +171,22 @@ struct ExpertsBackPlan {
   size_t bytes;
 };
 
-// As above for the gradient, 64 / 128, us.  One scale for a tile's columns: 32
-// experts of 2048 x 1408 in groups of 128, 128 rows each, fp32 340 / 430, 256
-// 536 / 614, 512 940 / 1034, 1024 1791 / 1777; bf16 287 / 366, 460 / 514,
-// 797 / 881, 1508 / 1542 (8 experts of 4096 x 3584, 1024 rows: 2085 / 2021 and
-// 1743 / 1678).  Groups of 32, where the operand is made once a group: 128 rows
-// 630 / 730, 256 1072 / 1024, 512 1876 / 1734; bf16 540 / 465, 913 / 781,
-// 1600 / 1338.
+// As above for the gradient, 64 / 128, us, fp32; 16-bit types alike, in two parts
+// too.  One scale for a tile's columns: 32 experts of 2048 x 1408 in groups of
+// 128, 128 rows each 340 / 430, 256 536 / 614, 512 940 / 1034, 1024 1791 / 1777
+// (bf16 1774 / 1752); 8 experts of 4096 x 3584, 1024 rows 2085 / 2021.  Groups of
+// 32, where the operand is made once a group: 128 rows 630 / 730, 192 850 / 795,
+// 256 1072 / 1024, 512 1876 / 1734.
 int32_t back_tile_rows(int64_t n, int64_t experts, int64_t group) {
   return n >= (group % 128 == 0 ? 1024 : 192) * experts ? 128 : 64;
 }
 
 // (the bytes are those of any group)
-ExpertsBackPlan plan_experts_back(void* ws, int32_t dtype, int64_t T, int64_t H, int64_t W,
-                                  int64_t E, int64_t k, int64_t group) {
+ExpertsBackPlan plan_experts_back(void* ws, int64_t T, int64_t H, int64_t W, int64_t E, int64_t k,
+                                  int64_t group) {
   ExpertsBackPlan p{};
   Carve c(ws);
   p.n = T * k;
-  p.parts = parts_of(dtype);  // of the second product: dweights is fp32 for every type
   p.tile_rows = back_tile_rows(p.n, E, group);
   p.bound = q4::tile_bound(p.n, E, p.tile_rows);
   p.width_tiles = (W + 127) / 128;
@@ -458,7 +456,7 @@ size_t q4_experts_backward_workspace_bytes(int32_t dtype, int64_t T, int64_t hid
   if (!experts_sizes_ok(dtype, T, hidden, width, experts, top_k) || T == 0 ||
       group_status(group_size, hidden) != Q4_OK || group_status(group_size, width) != Q4_OK)
     return 0;
-  return plan_experts_back(nullptr, dtype, T, hidden, width, experts, top_k, 0).bytes;
+  return plan_experts_back(nullptr, T, hidden, width, experts, top_k, 0).bytes;
 }
 
 q4_status q4_experts_backward(const void* dout, int64_t lddo, int32_t dtype, int64_t T,
@@ -485,7 +483,7 @@ q4_status q4_experts_backward(const void* dout, int64_t lddo, int32_t dtype, int
     return Q4_ERR_INVALID_ARG;
   const Packed gu = q4::packed(gate_up, gate_up_scales, 2 * width, hidden, group_size);
   const Packed dn = q4::packed(down, down_scales, hidden, width, group_size);
-  ExpertsBackPlan pl = plan_experts_back(workspace, dtype, T, hidden, width, experts, top_k, group_size);
+  ExpertsBackPlan pl = plan_experts_back(workspace, T, hidden, width, experts, top_k, group_size);
   const int64_t most = pl.width_tiles > pl.hidden_tiles ? pl.width_tiles : pl.hidden_tiles;
   if ((double)pl.bound * (double)most > (double)q4::kMaxGrid) return Q4_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < pl.bytes || !aligned(workspace, 16)) return Q4_ERR_WORKSPACE;
@@ -510,7 +508,7 @@ q4_status q4_experts_backward(const void* dout, int64_t lddo, int32_t dtype, int
     err = q4::launch_scale_bits(gate_up_scales, gu.expert_scales, experts, pl.s_bits + experts, s);
   q4::BackParams b{};
   b.nibble_order = nibble_order;
-  b.parts = pl.parts;
+  b.parts = 2;
   b.slots = pl.lists.slots;
   b.tiles = pl.lists.tiles;
   b.n_tiles = pl.lists.n_tiles;

@@ -35,7 +35,7 @@ hipError_t launch_back(const BackParams& in, int32_t tile_rows, bool gate, hipSt
   p.d_vec = reinterpret_cast<uintptr_t>(p.d) % 16 == 0 && p.ldd * e % 16 == 0;
   if (!gate)
     return p.parts == 2 ? by_tile<2, float, false>(p, tile_rows, s) : by_tile<1, float, false>(p, tile_rows, s);
-  // two parts whatever the type: the gradient of the weights is fp32
+  // two parts whatever the type, as the gradients of gate and up
   switch (p.d_dtype) {
     case Q4_DTYPE_F32: return by_tile<2, float, true>(p, tile_rows, s);
     case Q4_DTYPE_F16: return by_tile<2, _Float16, true>(p, tile_rows, s);

@@ -1,5 +1,5 @@
 """16-bit types lose nothing between the products: what is computed on the way
-(the gated rows) is held to 22 bits whatever the
+(the gated rows, gradients of gate and up) is held to 22 bits whatever the
 activations' type, so only the output's own rounding is the type's.
 
 Bounds are those of experts_util.py with 2^-22 for the kept values of every
@@ -42,3 +42,18 @@ def test_gated_rows(T, E, k, group, dtype):
     want = oracle.experts(xv, ids[pick], w[pick].astype(np.float64), layer.gate_up, layer.down)
     e = u.expert_bounds(xv, ids[pick], w[pick], layer.gate_up, layer.down, dtype, oracle.sigmoid)[2]
     assert_within(got[torch.from_numpy(pick).cuda()], want, e + HALF_STEP[dtype] * (np.abs(want) + e) + 2.0 ** -25, "out")
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("group", [0, 32, 128])
+@pytest.mark.parametrize("T,E,k", WAYS)
+def test_gradients_of_gate_and_up(T, E, k, group, dtype):
+    layer = Layer(E, 128, 32, group)
+    d, dv, ids, w, pick = inputs(layer, T, k, dtype)
+    pre = np.random.default_rng(2).normal(size=(T, k, 64)).astype(np.float32)
+    dx, _ = q4.experts_backward(d, torch.from_numpy(ids).cuda(), torch.from_numpy(w).cuda(),
+                                torch.from_numpy(pre).cuda(), *layer.dev, **layer.kw)
+    args = (dv, ids[pick], w[pick].astype(np.float64), pre[pick].astype(np.float64), layer.gate_up, layer.down)
+    want = oracle.experts_grad(*args)[0]
+    e = u.expert_grad_bounds(*args, dtype, oracle.sigmoid)[0]
+    assert_within(dx[torch.from_numpy(pick).cuda()], want, e + HALF_STEP[dtype] * (np.abs(want) + e) + 2.0 ** -25, "dx")
