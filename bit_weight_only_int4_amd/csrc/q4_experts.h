@@ -111,7 +111,7 @@ struct GemmParams {
   const float* lse;       // kHeadGrad
   const float* g;         // kHeadGrad
   float* d;               // kHeadGrad: [M][out_ld], or with a scale per row
-  _Float16* d_parts;      // [parts][rows of a][out_ld]: times it, scaled as BackParams says
+  _Float16* d_parts;      // [2][rows of a][out_ld]: times it, scaled as BackParams says
   const uint32_t* s_bits;
 };
 hipError_t launch_gemm(const GemmParams& p, int32_t tile_rows, Epilogue epi, hipStream_t s);
@@ -156,11 +156,11 @@ hipError_t launch_combine(const CombineParams& p, int32_t dtype, hipStream_t s);
 // contracted over N.
 struct BackParams {
   Packed w;
-  int32_t nibble_order, parts;
+  int32_t nibble_order;
   const void* d;           // rows of d_dtype
   int64_t ldd;
   // or, with a scale per row of the matrix: d times it, against the row's and
-  // the scales' largest (times 2^15), as binary16 parts [parts][d_rows][ldd] in
+  // the scales' largest (times 2^15), as two binary16 parts [2][d_rows][ldd] in
   // the operands' order, zeros from n_rows to the next multiple of 64
   const _Float16* d_parts;
   int64_t d_rows;

@@ -61,8 +61,6 @@ q4_status group_status(int64_t gs, int64_t K) {
   return gs == 0 || gs >= K || gs == 32 || gs % 64 == 0 ? Q4_OK : Q4_ERR_UNSUPPORTED;
 }
 
-bool one_group(int64_t gs, int64_t K) { return gs == 0 || gs >= K; }
-
 // Pieces of a workspace, each 256-byte aligned within it.
 struct Carve {
   uint8_t* base;
@@ -215,7 +213,7 @@ bool head_sizes_ok(int32_t dtype, int64_t M, int64_t V, int64_t K) {
 
 struct HeadPlan {
   int64_t rows;  // at a time
-  int32_t tile_rows, parts;
+  int32_t tile_rows;
   SplitRows xs;
   int32_t stat_parts;  // forward
   float *stats, *chosen;
@@ -235,33 +233,31 @@ int32_t head_tile_rows(int64_t rows) {
   return rows > 320 || (rows > 192 && rows <= 256) ? 128 : 64;
 }
 
-HeadPlan plan_head(void* ws, int32_t dtype, int64_t M, int64_t V, int64_t K, bool one_scale,
-                   bool back) {
+HeadPlan plan_head(void* ws, int32_t dtype, int64_t M, int64_t V, int64_t K, bool back) {
   HeadPlan p{};
   Carve c(ws);
   p.rows = M < kHeadRows ? M : kHeadRows;
-  p.parts = parts_of(dtype);
+  const int32_t parts = parts_of(dtype);
   p.tile_rows = head_tile_rows(p.rows);
-  p.xs = take_split(c, p.rows, K, p.parts);
+  p.xs = take_split(c, p.rows, K, parts);
   if (!back) {
-    p.stat_parts = (int32_t)((V + 127) / 128) * (p.tile_rows == 64 && p.parts == 1 ? 4 : 2);  // a wave's each
+    p.stat_parts = (int32_t)((V + 127) / 128) * (p.tile_rows == 64 && parts == 1 ? 4 : 2);  // a wave's each
     p.stats = c.take<float>(p.rows * p.stat_parts * 2);
     p.chosen = c.take<float>(p.rows);
   } else {
     // A piece's gradient is to stay in the last-level cache between its two
-    // products.  2048 rows of bf16 over 128257 x 2048: 64 MB a piece 2932 us, 128
-    // 2588, 256 2483, 512 2557; fp32 4597, 4375, 4390, 4469.
+    // products.  2048 rows of bf16 over 128257 x 2048: 64 MB a piece 3647 us, 128
+    // 3343, 256 3352, 512 3417; fp32 4501, 4205, 4276, 4339.
     const int64_t most = (int64_t)(256 << 20) / 4 / p.rows;
     const int64_t pieces = (V + (most > 1024 ? most : 1024) - 1) / (most > 1024 ? most : 1024);
     p.piece = ((V + pieces - 1) / pieces + 127) / 128 * 128;
     const int64_t tiles = (p.rows + p.tile_rows - 1) / p.tile_rows * ((K + 127) / 128);
     // Splits of a piece, at least 8 steps deep, so that rounds of the workgroups
-    // that fit the card (three a CU in one part with a scale per row, else two)
-    // come out even, at a hundredth each for their sums.  Backward of 32003 x 4096
-    // and 700 rows, 192 tiles, fp32, 2, 4, 5, 8, 10 splits 830, 788, 772, 764, 803
-    // us; 128257 x 2048, 2048 rows, 256 tiles, bf16, 1, 2, 3, 4, 6, 8 splits 2967,
-    // 2515, 2464, 2551, 2575, 2683.
-    const int64_t fit = 256 * (one_scale && p.parts == 1 ? 3 : 2);
+    // that fit the card (two a CU) come out even, at a hundredth each for their
+    // sums.  Backward of 32003 x 4096 and 700 rows, 192 tiles, fp32, 2, 4, 5, 8, 10
+    // splits 791, 759, 748, 746, 774 us; 128257 x 2048, 2048 rows, 256 tiles, bf16,
+    // 1, 2, 3, 4, 6, 8 splits 4164, 3370, 3622, 3465, 3546, 3646.
+    const int64_t fit = 512;
     double least = 0.0;
     for (int64_t n = 1; n <= 16 && (n == 1 || n <= p.piece / 512); ++n) {
       const double cost = (double)((tiles * n + fit - 1) / fit) / (double)n * (1.0 + 0.01 * (double)n);
@@ -508,7 +504,6 @@ q4_status q4_experts_backward(const void* dout, int64_t lddo, int32_t dtype, int
     err = q4::launch_scale_bits(gate_up_scales, gu.expert_scales, experts, pl.s_bits + experts, s);
   q4::BackParams b{};
   b.nibble_order = nibble_order;
-  b.parts = 2;
   b.slots = pl.lists.slots;
   b.tiles = pl.lists.tiles;
   b.n_tiles = pl.lists.n_tiles;
@@ -551,7 +546,7 @@ q4_status q4_experts_backward(const void* dout, int64_t lddo, int32_t dtype, int
 size_t q4_head_cross_entropy_workspace_bytes(int32_t dtype, int64_t M, int64_t vocab, int64_t K,
                                              int64_t group_size) {
   if (!head_sizes_ok(dtype, M, vocab, K) || M == 0 || group_status(group_size, K) != Q4_OK) return 0;
-  return plan_head(nullptr, dtype, M, vocab, K, one_group(group_size, K), false).bytes;
+  return plan_head(nullptr, dtype, M, vocab, K, false).bytes;
 }
 
 q4_status q4_head_cross_entropy(const void* x, int64_t ldx, int32_t dtype, int64_t M,
@@ -569,7 +564,7 @@ q4_status q4_head_cross_entropy(const void* x, int64_t ldx, int32_t dtype, int64
       !aligned(scales, 4) || !aligned(targets, 8) || !aligned(loss, 4) || !aligned(lse, 4))
     return Q4_ERR_INVALID_ARG;
   const Packed w = q4::packed(qw, scales, vocab, K, group_size);
-  const HeadPlan pl = plan_head(workspace, dtype, M, vocab, K, one_group(group_size, K), false);
+  const HeadPlan pl = plan_head(workspace, dtype, M, vocab, K, false);
   if (!workspace || workspace_bytes < pl.bytes || !aligned(workspace, 16)) return Q4_ERR_WORKSPACE;
   const Range outs[] = {flat(loss, M, 4), flat(lse, M, 4), flat(workspace, (int64_t)pl.bytes, 1)};
   const Range ins[] = {span(x, M, ldx, K, e), flat(qw, w.expert_bytes, 1),
@@ -604,7 +599,7 @@ q4_status q4_head_cross_entropy(const void* x, int64_t ldx, int32_t dtype, int64
 size_t q4_head_cross_entropy_backward_workspace_bytes(int32_t dtype, int64_t M, int64_t vocab,
                                                       int64_t K, int64_t group_size) {
   if (!head_sizes_ok(dtype, M, vocab, K) || M == 0 || group_status(group_size, K) != Q4_OK) return 0;
-  return plan_head(nullptr, dtype, M, vocab, K, one_group(group_size, K), true).bytes;
+  return plan_head(nullptr, dtype, M, vocab, K, true).bytes;
 }
 
 q4_status q4_head_cross_entropy_backward(const void* x, int64_t ldx, int32_t dtype, int64_t M,
@@ -626,7 +621,7 @@ q4_status q4_head_cross_entropy_backward(const void* x, int64_t ldx, int32_t dty
       !aligned(lse, 4) || !aligned(g_loss, 4))
     return Q4_ERR_INVALID_ARG;
   const Packed w = q4::packed(qw, scales, vocab, K, group_size);
-  const HeadPlan pl = plan_head(workspace, dtype, M, vocab, K, one_group(group_size, K), true);
+  const HeadPlan pl = plan_head(workspace, dtype, M, vocab, K, true);
   if (!workspace || workspace_bytes < pl.bytes || !aligned(workspace, 16)) return Q4_ERR_WORKSPACE;
   const Range outs[] = {span(dx, M, lddx, K, e), flat(workspace, (int64_t)pl.bytes, 1)};
   const Range ins[] = {span(x, M, ldx, K, e), flat(qw, w.expert_bytes, 1),
@@ -669,7 +664,6 @@ q4_status q4_head_cross_entropy_backward(const void* x, int64_t ldx, int32_t dty
       q4::BackParams b{};
       b.w = w;
       b.nibble_order = nibble_order;
-      b.parts = pl.parts;
       if (w.group)
         b.d = pl.d;
       else

@@ -33,11 +33,15 @@
 
 namespace q4 {
 
-template <int P, int BM, int NG>
+// The row operand is a value computed on the way: two binary16 parts (22 bits)
+// whatever the activations' type.
+constexpr int kParts = 2;
+
+template <int BM, int NG>
 struct BackTile {
   static constexpr int kN = NG == 1 ? 64 : 32;  // n of a step
   static constexpr int kPart = BM * kN * 2;     // bytes of one part of one operand
-  static constexpr int kA = NG * P * kPart;
+  static constexpr int kA = NG * kParts * kPart;
   static constexpr int kB = 128 * kN / 2;
   static constexpr int kStage = kA + kB;
   static constexpr int kStages = 2 * kStage <= 76 * 1024 ? 2 : 1;
@@ -84,9 +88,9 @@ __device__ __forceinline__ void store_turned(uint8_t* b, const uint32_t (&w)[4],
   }
 }
 
-template <int P, typename T, int BM, int NG, bool GATE>
+template <typename T, int BM, int NG, bool GATE>
 __global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
-  typedef BackTile<P, BM, NG> L;
+  typedef BackTile<BM, NG> L;
   constexpr int CB = BM / 64, WC = 4 / CB, NS = L::kN, S = L::kStages;
   constexpr int kChunks = NS / 8;            // 16-byte pieces of a row
   constexpr int kPasses = BM * kChunks / 256;  // rows of a thread
@@ -241,14 +245,13 @@ __global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
         h8 hi, lo;
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          float x = __builtin_ldexpf(f.d[i][operand_nibble(e)], de[i]) * s[e];
-          if constexpr (P == 2) x = settled(x);
+          const float x = settled(__builtin_ldexpf(f.d[i][operand_nibble(e)], de[i]) * s[e]);
           hi[e] = part_hi(x);
-          if constexpr (P == 2) lo[e] = part_lo(x, hi[e]);
+          lo[e] = part_lo(x, hi[e]);
         }
-        uint8_t* dst = base + g * P * L::kPart + row * (NS * 2) + ((chunk ^ turn_of(row)) * 16);
+        uint8_t* dst = base + g * kParts * L::kPart + row * (NS * 2) + ((chunk ^ turn_of(row)) * 16);
         *(h8*)dst = hi;
-        if constexpr (P == 2) *(h8*)(dst + L::kPart) = lo;
+        *(h8*)(dst + L::kPart) = lo;
       }
     }
     if (codes_mine) store_turned<NS>(base + L::kA, f.w, kw, u, p.nibble_order != Q4_ORDER_LOW_FIRST);
@@ -281,11 +284,11 @@ __global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
           const int row = wr * 64 + r * 32 + c;
           const int at_ = row * (NS * 2) + (((h * 4 + q * 2 + j) ^ turn_of(row)) * 16);
 #pragma unroll
-          for (int pc = 0; pc < P; ++pc) {
+          for (int pc = 0; pc < kParts; ++pc) {
 #pragma unroll
             for (int b = 0; b < CB; ++b) {
               const int g = NG == 1 ? 0 : wc * CB + b;
-              const h8 a = *(const h8*)(base + (g * P + pc) * L::kPart + at_);
+              const h8 a = *(const h8*)(base + (g * kParts + pc) * L::kPart + at_);
               acc[r][b] = __builtin_amdgcn_mfma_f32_32x32x16_f16(a, bo[b], acc[r][b], 0, 0, 0);
             }
           }
@@ -390,16 +393,16 @@ __global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
 
 // The same with the row operand complete in memory (d_parts): it comes by direct
 // loads, as the forward product's, and only the codes are turned around.
-template <int P, int BM>
+template <int BM>
 struct DirectTile {
-  static constexpr int kA = P * BM * kBK * 2;
+  static constexpr int kA = kParts * BM * kBK * 2;
   static constexpr int kB = 128 * kBK / 2;
   static constexpr int kLds = 2 * (kA + kB);
 };
 
-template <int P, int BM>
+template <int BM>
 __global__ void __launch_bounds__(256, 2) back_direct_kernel(const BackParams p) {
-  typedef DirectTile<P, BM> L;
+  typedef DirectTile<BM> L;
   constexpr int RB = BM / 64;
   extern __shared__ __attribute__((aligned(16))) uint8_t smem[];
   __shared__ int32_t sh_exp[BM];
@@ -440,7 +443,7 @@ __global__ void __launch_bounds__(256, 2) back_direct_kernel(const BackParams p)
     const int st = step < steps ? step : steps - 1;
     uint8_t* base = smem + (step & 1) * L::kA;
 #pragma unroll
-    for (int pc = 0; pc < P; ++pc)
+    for (int pc = 0; pc < kParts; ++pc)
 #pragma unroll
       for (int i = 0; i < BM / 32; ++i)
         __builtin_amdgcn_global_load_lds(
@@ -493,7 +496,7 @@ __global__ void __launch_bounds__(256, 2) back_direct_kernel(const BackParams p)
           const int row = wr * (BM / 2) + r * 32 + c;
           const int chunk = (h * 4 + q * 2 + j) ^ ((row >> 1) & 7);
 #pragma unroll
-          for (int pc = 0; pc < P; ++pc) {
+          for (int pc = 0; pc < kParts; ++pc) {
             const h8 a = *(const h8*)(a_base + pc * BM * 128 + row * 128 + chunk * 16);
 #pragma unroll
             for (int b = 0; b < 2; ++b)
@@ -549,32 +552,32 @@ __global__ void __launch_bounds__(256, 2) back_direct_kernel(const BackParams p)
   }
 }
 
-template <int P, int BM>
+template <int BM>
 hipError_t launch_back_direct(const BackParams& p, hipStream_t s) {
-  constexpr int lds = DirectTile<P, BM>::kLds;
+  constexpr int lds = DirectTile<BM>::kLds;
   if (lds > 64 * 1024) {
-    const hipError_t e = hipFuncSetAttribute((const void*)back_direct_kernel<P, BM>,
+    const hipError_t e = hipFuncSetAttribute((const void*)back_direct_kernel<BM>,
                                              hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (e != hipSuccess) return e;
   }
   const dim3 grid((uint32_t)((int64_t)p.row_tiles * p.col_tiles * p.splits));
-  hipLaunchKernelGGL((back_direct_kernel<P, BM>), grid, dim3(256), lds, s, p);
+  hipLaunchKernelGGL((back_direct_kernel<BM>), grid, dim3(256), lds, s, p);
   return hipGetLastError();
 }
 
-template <int P, typename T, int BM, bool GATE>
+template <typename T, int BM, bool GATE>
 hipError_t launch_back_tile(const BackParams& p, hipStream_t s) {
   const dim3 grid((uint32_t)((int64_t)p.row_tiles * p.col_tiles * p.splits));
 #define Q4_BACK(NG)                                                                          \
   do {                                                                                       \
-    typedef BackTile<P, BM, NG> L;                                                           \
+    typedef BackTile<BM, NG> L;                                                              \
     constexpr int lds = L::kStages * L::kStage;                                              \
     if (lds > 64 * 1024) {                                                                   \
-      const hipError_t e = hipFuncSetAttribute((const void*)back_kernel<P, T, BM, NG, GATE>,  \
+      const hipError_t e = hipFuncSetAttribute((const void*)back_kernel<T, BM, NG, GATE>,  \
                                                hipFuncAttributeMaxDynamicSharedMemorySize, lds); \
       if (e != hipSuccess) return e;                                                         \
     }                                                                                        \
-    hipLaunchKernelGGL((back_kernel<P, T, BM, NG, GATE>), grid, dim3(256), lds, s, p);       \
+    hipLaunchKernelGGL((back_kernel<T, BM, NG, GATE>), grid, dim3(256), lds, s, p);       \
   } while (0)
   if (p.w.group % 128 == 0)
     Q4_BACK(1);

@@ -2,8 +2,6 @@
 #include "q4_experts_back.h"
 
 namespace q4 {
-template hipError_t launch_back_direct<1, 64>(const BackParams&, hipStream_t);
-template hipError_t launch_back_direct<1, 128>(const BackParams&, hipStream_t);
-template hipError_t launch_back_direct<2, 64>(const BackParams&, hipStream_t);
-template hipError_t launch_back_direct<2, 128>(const BackParams&, hipStream_t);
+template hipError_t launch_back_direct<64>(const BackParams&, hipStream_t);
+template hipError_t launch_back_direct<128>(const BackParams&, hipStream_t);
 }  // namespace q4

@@ -2,6 +2,6 @@
 #include "q4_experts_back.h"
 
 namespace q4 {
-template hipError_t launch_back_tile<2, bf16, 64, true>(const BackParams&, hipStream_t);
-template hipError_t launch_back_tile<2, bf16, 128, true>(const BackParams&, hipStream_t);
+template hipError_t launch_back_tile<bf16, 64, true>(const BackParams&, hipStream_t);
+template hipError_t launch_back_tile<bf16, 128, true>(const BackParams&, hipStream_t);
 }  // namespace q4

@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(256, GM == kOneGroup && P == 1 ? 3 : 2) gemm_k
           _Float16* dst = to + (int64_t)slot * p.out_ld;
           const _Float16 hi = part_hi(x);
           *dst = hi;
-          if constexpr (P == 2) dst[p.a.rows * p.out_ld] = part_lo(x, hi);
+          dst[p.a.rows * p.out_ld] = part_lo(x, hi);
         }
       }
     }

@@ -19,9 +19,8 @@
  * exact in binary16 and its scale multiplies fp32 sums.  A row of activations
  * is scaled by a power of two to the top of binary16's range, so that no
  * magnitude overflows, and held as one binary16 number (16-bit types: bf16
- * and fp16 values are exact, the head's gradients of its logits are rounded to
- * 11 bits) or as two (fp32 and what the experts compute on the way: 22 bits),
- * no finer than 2^-39 of its row's largest.
+ * and fp16 values are exact) or as two (fp32, and for every type what is
+ * computed on the way: 22 bits), no finer than 2^-39 of its row's largest.
  * Infinities and NaN of a row reach no other row; an infinite element makes
  * its row's results infinite or NaN.  A workspace may serve any number of
  * calls one after the other, from captured graphs too, but no two at once.

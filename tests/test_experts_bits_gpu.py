@@ -1,5 +1,5 @@
 """16-bit types lose nothing between the products: what is computed on the way
-(the gated rows, gradients of gate and up) is held to 22 bits whatever the
+(the gated rows, gradients, probabilities) is held to 22 bits whatever the
 activations' type, so only the output's own rounding is the type's.
 
 Bounds are those of experts_util.py with 2^-22 for the kept values of every
@@ -14,6 +14,7 @@ from oracle import experts_oracle as oracle
 from tests import experts_util as u
 from tests.experts_util import HALF_STEP, assert_within, rounded
 from tests.test_experts_gpu import Layer
+from tests.test_head_loss_gpu import check as check_head
 
 pytestmark = pytest.mark.gpu
 WAYS = [(1, 8, 2), (9, 8, 2), (40, 8, 2), (130, 8, 2), (1400, 2, 1)]  # T, experts, top_k
@@ -57,3 +58,10 @@ def test_gradients_of_gate_and_up(T, E, k, group, dtype):
     want = oracle.experts_grad(*args)[0]
     e = u.expert_grad_bounds(*args, dtype, oracle.sigmoid)[0]
     assert_within(dx[torch.from_numpy(pick).cuda()], want, e + HALF_STEP[dtype] * (np.abs(want) + e) + 2.0 ** -25, "dx")
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("group", [0, 32, 128])
+@pytest.mark.parametrize("M,V", [(3, 129), (70, 200), (400, 136)])
+def test_heads_gradient(M, V, group, dtype):
+    check_head(M, V, 72, group, dtype)
