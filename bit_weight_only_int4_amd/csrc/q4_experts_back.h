@@ -508,18 +508,23 @@ __global__ void __launch_bounds__(256, 2) back_direct_kernel(const BackParams p)
   };
 
   // Step st: its rows were asked for a step ago, its codes two; then the next
-  // step's rows, the codes after them, and the next step's codes into LDS.
+  // step's rows, the codes after them (in this order: the wait counts on it), and
+  // the next step's codes into LDS.  The compiler waits for all loads before it
+  // takes a step's codes, as their addresses depend on a branch.
   const bool idle = wr * (BM / 2) >= rows;
   Words f0, f1;
   if (steps > 0) {
     fetch(f0, 0);
+    keep_order();
     issue(0);
+    keep_order();
     fetch(f1, 1);
     store(f0, 0);
     auto step = [&](int st, Words& next, Words& after) {
       wait_loads<4>();  // (the four after them are the next step's codes)
       lds_barrier();
       issue(st + 1);
+      keep_order();
       fetch(after, st + 2);
       if (!idle) products(st);
       store(next, st + 1);

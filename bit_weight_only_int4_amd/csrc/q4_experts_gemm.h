@@ -64,6 +64,13 @@ __device__ __forceinline__ void wait_loads() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (7 << 4) | (15 << 8));
 }
 
+// Loads before it are issued before those after it: a wait that counts the newest
+// loads relies on their order, which the compiler is otherwise free to change.
+__device__ __forceinline__ void keep_order() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 // Maximum or sum over the 32 lanes of a half for 16 values: each step halves
 // the values a lane holds, so 16 exchanges do where 80 would.  Lane l ends with
 // value (l & 15) for lanes 0..15 of its half (and again for 16..31).
@@ -309,7 +316,10 @@ __global__ void __launch_bounds__(256, GM == kOneGroup && P == 1 ? 3 : 2) gemm_k
   // a wave without rows (of a tile that is not full) loads for the others
   const bool idle = wr * RB * 32 >= rows;
   issue(0);
-  if constexpr (S == 3) issue(1);
+  if constexpr (S == 3) {
+    keep_order();
+    issue(1);
+  }
   auto begin = [&](int step) -> const uint8_t* {
     wait_loads<(S - 2) * L::kIssue>();
     lds_barrier();
