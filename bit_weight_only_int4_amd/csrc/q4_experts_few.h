@@ -240,6 +240,13 @@ few_kernel(const FewParams pa, const FewShape fa) {
   };
 #pragma unroll
   for (int i = 0; i < kHold; ++i) load_codes(cg0 + cs, i);
+  float row_scale[kMine][2];
+  if constexpr (FS == kRowScale) {
+#pragma unroll
+    for (int g = 0; g < kMine; ++g)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) row_scale[g][b] = scales[packed_row(cg0 + g * CS + cs, b)];
+  }
 
   // the rows' elements among this wave's k, split: rows of binary16 operands,
   // first parts, then second parts
@@ -358,6 +365,8 @@ few_kernel(const FewParams pa, const FewShape fa) {
       for (int b = 0; b < 2; ++b) {
         float x = out[g][b][v];
         if constexpr (P == 2) x += __shfl_xor(x, 32, 64);
+        // (before the exponent: a sum of codes times large rows may pass fp32's range)
+        if constexpr (FS == kRowScale) x *= row_scale[g][b];
         if (P == 1 || q < 2)
           red[(w * kRows + r) * kRedPitch + (g * CS + cs) * 32 + b * 16 + n16] = __builtin_ldexpf(x, -e);
       }
@@ -367,17 +376,16 @@ few_kernel(const FewParams pa, const FewShape fa) {
     const int r = t / (CG * kBlock), c = t % (CG * kBlock);
     const int g = c / kBlock, cc = c % kBlock;
     const int to = sh_slot[r];
-    auto value = [&](int col, int row) {
+    auto value = [&](int col) {
       float x = 0.0f;
 #pragma unroll
       for (int i = 0; i < NW; ++i) x += red[(i * kRows + r) * kRedPitch + g * 32 + col];
-      if constexpr (FS == kRowScale) x *= scales[row];
       return x;
     };
     const int col = (cg0 + g) * kBlock + cc;
     if (col >= width) continue;
     if constexpr (GATED) {
-      const float gate = value(cc, col), up = value(16 + cc, width + col);
+      const float gate = value(cc), up = value(16 + cc);
       p.out[(int64_t)to * p.out_ld + col] = gate * sigmoid(gate) * up;
       if (p.pre) {
         float* pre = p.pre + (int64_t)to * 2 * width + col;
@@ -385,7 +393,7 @@ few_kernel(const FewParams pa, const FewShape fa) {
         pre[width] = up;
       }
     } else {
-      p.out[(int64_t)to * p.out_ld + col] = value(cc, col);
+      p.out[(int64_t)to * p.out_ld + col] = value(cc);
     }
   }
 }
