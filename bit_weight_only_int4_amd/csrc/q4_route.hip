@@ -91,6 +91,14 @@ __device__ __forceinline__ uint64_t shuffle_xor(uint64_t x, int d) {
   return __shfl_xor((unsigned long long)x, d, 64);
 }
 
+// Sigmoid of a chosen logit for the share among the chosen, of which `base` is
+// the largest: times e^-base where base < 0, so that scores too small for fp32
+// keep their shares (the largest is then 1/2 at least).
+__device__ __forceinline__ float small_sigmoid(float z, float base) {
+  if (!(base < 0.0f)) return sigmoid(z);
+  return exp_full(z - base) / (1.0f + exp_full(z));
+}
+
 template <bool BIAS>
 struct KeyOf {
   typedef uint32_t type;
@@ -298,10 +306,11 @@ __global__ void __launch_bounds__(64 * kWaves) route_kernel(const RouteParams p)
     }
     w = id >= 0 ? s / sum : 0.0f;
   } else {
-    w = id >= 0 ? sigmoid(chosen) : 0.0f;
+    const float base = p.renormalize ? wave_max(chosen) : 0.0f;
+    w = id >= 0 ? small_sigmoid(chosen, base) : 0.0f;
     if (p.renormalize) {
       const float sum = wave_sum(w);
-      w = sum > 0.0f ? w / sum : 0.0f;
+      w = id >= 0 ? w / sum : 0.0f;
     }
   }
   w = id >= 0 ? w * p.scale : 0.0f;
@@ -349,12 +358,12 @@ __global__ void __launch_bounds__(64 * kWaves) route_backward_kernel(const Route
   float dz = 0.0f, share_sum = 0.0f, denom = 1.0f;
   if (p.renormalize) {
     float s, rest;
+    const float base = wave_max(zc);
     if (softmax) {
-      const float base = wave_max(zc);
       s = zc > -__builtin_inff() ? exp_full(zc - base) : 0.0f;
       rest = 1.0f;
     } else {
-      s = id >= 0 ? sigmoid(zc) : 0.0f;
+      s = id >= 0 ? small_sigmoid(zc, base) : 0.0f;
       rest = id >= 0 ? sigmoid(-zc) : 0.0f;  // 1 - s without its cancellation
     }
     const float sum = wave_sum(s);

@@ -57,7 +57,7 @@ extern "C" {
  * go to the lowest index.
  *   ids      int32 [T, top_k]; -1 where fewer are eligible
  *   weights  float [T, top_k]: scale * s, divided by the sum of the chosen s
- *            if renormalize (0 where that sum is); 0 where the id is -1
+ *            if renormalize (however small they are); 0 where the id is -1
  * A NaN in a row, or a +inf under softmax, makes the row's weights NaN.
  * experts <= 1024, top_k <= 32, top_k <= experts / groups * top_groups.
  */
