@@ -47,10 +47,13 @@ struct Packed {
   int64_t expert_bytes; // N * K / 2
   int64_t expert_scales;
 };
+inline int64_t groups_of(int64_t K, int64_t group) {
+  return group == 0 || group >= K ? 1 : (K + group - 1) / group;
+}
 inline Packed packed(const uint8_t* qw, const float* scales, int64_t N, int64_t K, int64_t group) {
   const int64_t gs = group >= K ? 0 : group;
   // a group of the whole depth indexes like a scale per row
-  const int64_t G = gs == 0 ? 1 : (K + gs - 1) / gs;
+  const int64_t G = groups_of(K, group);
   return Packed{qw, scales, N, K, (int32_t)gs, (int32_t)G, N * (K / 2), G * N};
 }
 
@@ -166,7 +169,7 @@ struct BackParams {
   int64_t d_rows;
   int32_t d_dtype;
   const uint32_t* d_bits;  // [row of d]: bits of a magnitude that none of the row's passes
-  const uint32_t* s_bits;  // [experts]: of the largest scale
+  const uint32_t* s_bits;  // [experts][groups]: of the group's largest scale
   const int32_t* slots;
   const Tile* tiles;
   const int32_t* n_tiles;
@@ -192,8 +195,8 @@ hipError_t launch_back(const BackParams& p, int32_t tile_rows, bool gate, hipStr
 // Bits of rows' largest finite magnitudes; `zero` words beside them become 0.
 hipError_t launch_row_bits(const void* x, int64_t ldx, int32_t dtype, int64_t rows, int64_t K,
                            uint32_t* bits, uint32_t* zero, int64_t zeros, hipStream_t s);
-// and of each expert's scales, as maxima over what is there
-hipError_t launch_scale_bits(const float* s, int64_t per_expert, int64_t experts, uint32_t* bits,
+// and of n scales each of so many groups, as maxima over what is there
+hipError_t launch_scale_bits(const float* s, int64_t n, int64_t groups, uint32_t* bits,
                              hipStream_t st);
 // dweights from its parts
 hipError_t launch_gate_sums(const float* part, int32_t parts, const int32_t* ids, int64_t n,

@@ -162,7 +162,7 @@ bool experts_grid_ok(const ExpertsPlan& p, int64_t H, int64_t W) {
 
 struct ExpertsBackPlan {
   int32_t tile_rows;
-  int64_t n, bound, width_tiles, hidden_tiles;
+  int64_t n, bound, width_tiles, hidden_tiles, s_words;
   RowLists lists;
   uint32_t *dout_bits, *dpre_bits, *s_bits;
   float *dpre, *dw_part, *dx;
@@ -179,7 +179,6 @@ int32_t back_tile_rows(int64_t n, int64_t experts, int64_t group) {
   return n >= (group % 128 == 0 ? 1024 : 192) * experts ? 128 : 64;
 }
 
-// (the bytes are those of any group)
 ExpertsBackPlan plan_experts_back(void* ws, int64_t T, int64_t H, int64_t W, int64_t E, int64_t k,
                                   int64_t group) {
   ExpertsBackPlan p{};
@@ -191,7 +190,8 @@ ExpertsBackPlan plan_experts_back(void* ws, int64_t T, int64_t H, int64_t W, int
   p.hidden_tiles = (H + 127) / 128;
   p.lists = take_lists(c, p.n, E, 64);
   p.dout_bits = c.take<uint32_t>(T);
-  p.dpre_bits = c.take<uint32_t>(p.n + 2 * E);
+  p.s_words = E * (q4::groups_of(W, group) + q4::groups_of(H, group));
+  p.dpre_bits = c.take<uint32_t>(p.n + p.s_words);
   p.s_bits = p.dpre_bits + p.n;
   p.dpre = c.take<float>(p.n * 2 * W);
   p.dw_part = c.take<float>(p.n * 4 * p.width_tiles);  // a wave's each
@@ -233,7 +233,7 @@ int32_t head_tile_rows(int64_t rows) {
   return rows > 320 || (rows > 192 && rows <= 256) ? 128 : 64;
 }
 
-HeadPlan plan_head(void* ws, int32_t dtype, int64_t M, int64_t V, int64_t K, bool back) {
+HeadPlan plan_head(void* ws, int32_t dtype, int64_t M, int64_t V, int64_t K, int64_t group, bool back) {
   HeadPlan p{};
   Carve c(ws);
   p.rows = M < kHeadRows ? M : kHeadRows;
@@ -269,7 +269,7 @@ HeadPlan plan_head(void* ws, int32_t dtype, int64_t M, int64_t V, int64_t K, boo
     p.d = c.take<float>(p.rows * p.piece);
     p.acc = c.take<float>(p.splits * p.rows * K);
     p.g_bits = c.take<uint32_t>(p.rows);
-    p.s_bits = c.take<uint32_t>(1);
+    p.s_bits = c.take<uint32_t>(q4::groups_of(K, group));
   }
   p.bytes = c.at;
   return p;
@@ -452,7 +452,7 @@ size_t q4_experts_backward_workspace_bytes(int32_t dtype, int64_t T, int64_t hid
   if (!experts_sizes_ok(dtype, T, hidden, width, experts, top_k) || T == 0 ||
       group_status(group_size, hidden) != Q4_OK || group_status(group_size, width) != Q4_OK)
     return 0;
-  return plan_experts_back(nullptr, T, hidden, width, experts, top_k, 0).bytes;
+  return plan_experts_back(nullptr, T, hidden, width, experts, top_k, group_size).bytes;
 }
 
 q4_status q4_experts_backward(const void* dout, int64_t lddo, int32_t dtype, int64_t T,
@@ -497,11 +497,10 @@ q4_status q4_experts_backward(const void* dout, int64_t lddo, int32_t dtype, int
   hipError_t err = q4::launch_lists(ids, n, experts, pl.tile_rows, pl.lists, s);
   if (err == hipSuccess)
     err = q4::launch_row_bits(dout, lddo, dtype, T, hidden, pl.dout_bits, pl.dpre_bits,
-                              n + 2 * experts, s);
-  if (err == hipSuccess)
-    err = q4::launch_scale_bits(down_scales, dn.expert_scales, experts, pl.s_bits, s);
-  if (err == hipSuccess)
-    err = q4::launch_scale_bits(gate_up_scales, gu.expert_scales, experts, pl.s_bits + experts, s);
+                              n + pl.s_words, s);
+  uint32_t* gu_bits = pl.s_bits + experts * dn.G;
+  if (err == hipSuccess) err = q4::launch_scale_bits(down_scales, dn.N, experts * dn.G, pl.s_bits, s);
+  if (err == hipSuccess) err = q4::launch_scale_bits(gate_up_scales, gu.N, experts * gu.G, gu_bits, s);
   q4::BackParams b{};
   b.nibble_order = nibble_order;
   b.slots = pl.lists.slots;
@@ -531,7 +530,7 @@ q4_status q4_experts_backward(const void* dout, int64_t lddo, int32_t dtype, int
   b.ldd = 2 * width;
   b.d_dtype = Q4_DTYPE_F32;
   b.d_bits = pl.dpre_bits;
-  b.s_bits = pl.s_bits + experts;
+  b.s_bits = gu_bits;
   b.slots_per_row = 1;
   b.n_rows = 2 * width;
   b.col_tiles = (int32_t)pl.hidden_tiles;
@@ -546,7 +545,7 @@ q4_status q4_experts_backward(const void* dout, int64_t lddo, int32_t dtype, int
 size_t q4_head_cross_entropy_workspace_bytes(int32_t dtype, int64_t M, int64_t vocab, int64_t K,
                                              int64_t group_size) {
   if (!head_sizes_ok(dtype, M, vocab, K) || M == 0 || group_status(group_size, K) != Q4_OK) return 0;
-  return plan_head(nullptr, dtype, M, vocab, K, false).bytes;
+  return plan_head(nullptr, dtype, M, vocab, K, group_size, false).bytes;
 }
 
 q4_status q4_head_cross_entropy(const void* x, int64_t ldx, int32_t dtype, int64_t M,
@@ -564,7 +563,7 @@ q4_status q4_head_cross_entropy(const void* x, int64_t ldx, int32_t dtype, int64
       !aligned(scales, 4) || !aligned(targets, 8) || !aligned(loss, 4) || !aligned(lse, 4))
     return Q4_ERR_INVALID_ARG;
   const Packed w = q4::packed(qw, scales, vocab, K, group_size);
-  const HeadPlan pl = plan_head(workspace, dtype, M, vocab, K, false);
+  const HeadPlan pl = plan_head(workspace, dtype, M, vocab, K, group_size, false);
   if (!workspace || workspace_bytes < pl.bytes || !aligned(workspace, 16)) return Q4_ERR_WORKSPACE;
   const Range outs[] = {flat(loss, M, 4), flat(lse, M, 4), flat(workspace, (int64_t)pl.bytes, 1)};
   const Range ins[] = {span(x, M, ldx, K, e), flat(qw, w.expert_bytes, 1),
@@ -599,7 +598,7 @@ q4_status q4_head_cross_entropy(const void* x, int64_t ldx, int32_t dtype, int64
 size_t q4_head_cross_entropy_backward_workspace_bytes(int32_t dtype, int64_t M, int64_t vocab,
                                                       int64_t K, int64_t group_size) {
   if (!head_sizes_ok(dtype, M, vocab, K) || M == 0 || group_status(group_size, K) != Q4_OK) return 0;
-  return plan_head(nullptr, dtype, M, vocab, K, true).bytes;
+  return plan_head(nullptr, dtype, M, vocab, K, group_size, true).bytes;
 }
 
 q4_status q4_head_cross_entropy_backward(const void* x, int64_t ldx, int32_t dtype, int64_t M,
@@ -621,7 +620,7 @@ q4_status q4_head_cross_entropy_backward(const void* x, int64_t ldx, int32_t dty
       !aligned(lse, 4) || !aligned(g_loss, 4))
     return Q4_ERR_INVALID_ARG;
   const Packed w = q4::packed(qw, scales, vocab, K, group_size);
-  const HeadPlan pl = plan_head(workspace, dtype, M, vocab, K, true);
+  const HeadPlan pl = plan_head(workspace, dtype, M, vocab, K, group_size, true);
   if (!workspace || workspace_bytes < pl.bytes || !aligned(workspace, 16)) return Q4_ERR_WORKSPACE;
   const Range outs[] = {span(dx, M, lddx, K, e), flat(workspace, (int64_t)pl.bytes, 1)};
   const Range ins[] = {span(x, M, ldx, K, e), flat(qw, w.expert_bytes, 1),
@@ -638,8 +637,8 @@ q4_status q4_head_cross_entropy_backward(const void* x, int64_t ldx, int32_t dty
                            nullptr, 0, xs, s);
     // no element of a row passes its g_loss: |p - 1[target]| <= 1
     if (err == hipSuccess)
-      err = q4::launch_row_bits(g_loss + m0, 1, Q4_DTYPE_F32, xs.rows, 1, pl.g_bits, pl.s_bits, 1, s);
-    if (err == hipSuccess) err = q4::launch_scale_bits(scales, w.expert_scales, 1, pl.s_bits, s);
+      err = q4::launch_row_bits(g_loss + m0, 1, Q4_DTYPE_F32, xs.rows, 1, pl.g_bits, pl.s_bits, w.G, s);
+    if (err == hipSuccess) err = q4::launch_scale_bits(scales, vocab, w.G, pl.s_bits, s);
     const int32_t row_tiles = (int32_t)((xs.rows + pl.tile_rows - 1) / pl.tile_rows);
     for (int64_t v0 = 0; v0 < vocab && err == hipSuccess; v0 += pl.piece) {
       const int64_t cols = vocab - v0 < pl.piece ? vocab - v0 : pl.piece;

@@ -7,7 +7,7 @@
 // group belongs to the row operand here: d times the scales of the tile's
 // group is formed in fp32 on the way into LDS and split into binary16 parts
 // there (d against its row's largest magnitude, the scales against their
-// matrix's), so codes stay exact integers.  128 columns of one group need one
+// group's), so codes stay exact integers.  128 columns of one group need one
 // such operand; with groups of 32 or 64 each 32 columns have their own (NG = 4).
 //
 // Codes lie along k, the contraction runs along n: a thread takes a word (8 k)
@@ -126,7 +126,6 @@ __global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
   }
   const int64_t K = p.w.K, N = p.w.N, ldq = K >> 1;
   const int64_t k0 = (int64_t)ct * 128;
-  const int s_exp = top_exponent(p.s_bits[expert]);
   // this split's rows of the matrix
   const int64_t per = ((p.n_rows + p.splits - 1) / p.splits + NS - 1) / NS * NS;
   const int64_t nb = per * split < p.n_rows ? per * split : p.n_rows;
@@ -156,11 +155,18 @@ __global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
     de[i] = -top_exponent(p.d_bits[dr]);
   }
   const float* scales = p.w.scales + expert * p.w.expert_scales + p.n0;
+  // (a group's scales against its largest: a group far below the others keeps its bits)
+  const uint32_t* s_bits = p.s_bits + (int64_t)expert * p.w.G;
+  auto group_of = [&](int64_t k) {
+    const int64_t g = p.w.group ? k / p.w.group : 0;
+    return g < p.w.G ? g : p.w.G - 1;
+  };
   int64_t group_at[NG];
+  int s_exp[NG];
 #pragma unroll
   for (int g = 0; g < NG; ++g) {
-    const int64_t gr = p.w.group ? (k0 + g * 32) / p.w.group : 0;
-    group_at[g] = (gr < p.w.G ? gr : p.w.G - 1) * N;
+    group_at[g] = group_of(k0 + g * 32) * N;
+    s_exp[g] = top_exponent(s_bits[group_of(k0 + g * 32)]);
   }
   // and of the codes: a word of four rows
   const int kw = tid & 15, u = tid >> 4;
@@ -238,7 +244,7 @@ __global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
     for (int g = 0; g < NG; ++g) {
       float s[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[e] = __builtin_ldexpf(f.s[g][operand_nibble(e)], 15 - s_exp);
+      for (int e = 0; e < 8; ++e) s[e] = __builtin_ldexpf(f.s[g][operand_nibble(e)], 15 - s_exp[g]);
 #pragma unroll
       for (int i = 0; i < kPasses; ++i) {
         const int row = arow + i * (256 / kChunks);
@@ -336,6 +342,10 @@ __global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
   settle(acc);
 
   // ---- results -------------------------------------------------------------
+  int b_exp[CB];  // of the wave's blocks of columns
+#pragma unroll
+  for (int b = 0; b < CB; ++b)
+    b_exp[b] = (NG == 1 ? s_exp[0] : top_exponent(s_bits[group_of(k0 + (wc * CB + b) * 32)])) - 15;
 #pragma unroll
   for (int r = 0; r < 2; ++r) {
     const int r0 = wr * 64 + r * 32 + 4 * q;
@@ -350,7 +360,7 @@ __global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
         for (int i = 0; i < 16; ++i) {
           const int row = r0 + 8 * (i >> 2) + (i & 3), slot = sh_slot[row];
           if (slot < 0 || k >= K) continue;
-          const float z = __builtin_ldexpf(acc[r][b][i], sh_exp[row] + s_exp - 15);
+          const float z = __builtin_ldexpf(acc[r][b][i], sh_exp[row] + b_exp[b]);
           const float* pre = p.pre + (int64_t)slot * 2 * K + k;
           const float g = pre[0], up = pre[K];
           const float sig = sigmoid(g), silu = g * sig;
@@ -382,7 +392,7 @@ __global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
         for (int i = 0; i < 16; ++i) {
           const int row = r0 + 8 * (i >> 2) + (i & 3), slot = sh_slot[row];
           if (slot < 0 || k >= K) continue;
-          const float z = __builtin_ldexpf(acc[r][b][i], sh_exp[row] + s_exp - 15);
+          const float z = __builtin_ldexpf(acc[r][b][i], sh_exp[row] + b_exp[b]);
           float* dst = out + (int64_t)slot * p.out_ld + k;
           *dst = p.accumulate ? *dst + z : z;
         }

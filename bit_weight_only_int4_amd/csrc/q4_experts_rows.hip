@@ -245,12 +245,13 @@ row_bits_kernel(const T* __restrict__ x, int64_t ldx, int64_t rows, int64_t K, u
   if (lane == 0) bits[row] = m;
 }
 
-constexpr int kScaleRun = 4096;  // scales of a workgroup
+constexpr int kScaleRun = 4096;  // scales of a workgroup, `runs` of them a group
 __global__ void __launch_bounds__(256)
-scale_bits_kernel(const float* __restrict__ s, int64_t n, uint32_t* bits) {
+scale_bits_kernel(const float* __restrict__ s, int64_t n, uint32_t runs, uint32_t* bits) {
   __shared__ uint32_t sh[4];
-  const float* src = s + (int64_t)blockIdx.y * n;
-  const int64_t at = (int64_t)blockIdx.x * kScaleRun + 4 * threadIdx.x;
+  const uint32_t group = blockIdx.x / runs;
+  const float* src = s + (int64_t)group * n;
+  const int64_t at = (int64_t)(blockIdx.x % runs) * kScaleRun + 4 * threadIdx.x;
   uint32_t m = 0;
 #pragma unroll
   for (int i = 0; i < kScaleRun / 1024; ++i) {
@@ -266,7 +267,7 @@ scale_bits_kernel(const float* __restrict__ s, int64_t n, uint32_t* bits) {
     }
   }
   m = block_umax(m, sh);
-  if (threadIdx.x == 0) atomicMax(bits + blockIdx.y, m);
+  if (threadIdx.x == 0) atomicMax(bits + group, m);
 }
 
 __global__ void __launch_bounds__(256)
@@ -420,10 +421,10 @@ hipError_t launch_row_bits(const void* x, int64_t ldx, int32_t dtype, int64_t ro
   return hipGetLastError();
 }
 
-hipError_t launch_scale_bits(const float* sc, int64_t per_expert, int64_t experts, uint32_t* bits,
+hipError_t launch_scale_bits(const float* sc, int64_t n, int64_t groups, uint32_t* bits,
                              hipStream_t s) {
-  const dim3 grid((uint32_t)((per_expert + kScaleRun - 1) / kScaleRun), (uint32_t)experts);
-  hipLaunchKernelGGL(scale_bits_kernel, grid, dim3(256), 0, s, sc, per_expert, bits);
+  const uint32_t runs = (uint32_t)((n + kScaleRun - 1) / kScaleRun);
+  hipLaunchKernelGGL(scale_bits_kernel, dim3((uint32_t)groups * runs), dim3(256), 0, s, sc, n, runs, bits);
   return hipGetLastError();
 }
 

@@ -16,11 +16,14 @@
  * constants: gradients are those of the activations.
  *
  * Arithmetic: binary16 operands on MFMA with fp32 sums.  A weight's code is
- * exact in binary16 and its scale multiplies fp32 sums.  A row of activations
- * is scaled by a power of two to the top of binary16's range, so that no
- * magnitude overflows, and held as one binary16 number (16-bit types: bf16
- * and fp16 values are exact) or as two (fp32, and for every type what is
- * computed on the way: 22 bits), no finer than 2^-39 of its row's largest.
+ * exact in binary16.  A row of activations is scaled by a power of two to the
+ * top of binary16's range, so that no magnitude overflows, and held as one
+ * binary16 number (16-bit types: bf16 and fp16 values are exact) or as two
+ * (fp32, and for every type what is computed on the way: 22 bits), no finer
+ * than 2^-39 of its row's largest.  Forward, a scale multiplies fp32 sums.
+ * Backward, a row's gradient times the scale (formed in fp32) is held as two, no
+ * finer than 2^-39 of its row's largest (for the head |g_loss|) times the
+ * largest scale of its group.
  * Infinities and NaN of a row reach no other row; an infinite element makes
  * its row's results infinite or NaN.  A workspace may serve any number of
  * calls one after the other, from captured graphs too, but no two at once.
