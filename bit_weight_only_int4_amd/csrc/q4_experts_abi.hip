@@ -205,12 +205,6 @@ ExpertsBackPlan plan_experts_back(void* ws, int64_t T, int64_t H, int64_t W, int
 // Rows are taken so many at a time, which bounds the workspace.
 constexpr int64_t kHeadRows = 8192;
 
-bool head_sizes_ok(int32_t dtype, int64_t M, int64_t V, int64_t K) {
-  return dtype_ok(dtype) && M >= 0 && M < kMaxRows && V >= 1 && V <= kMaxVocab && depth_ok(K) &&
-         // the workgroups of a launch
-         (double)((V + 127) / 128) * (kHeadRows / 64) <= (double)q4::kMaxGrid;
-}
-
 struct HeadPlan {
   int64_t rows;  // at a time
   int32_t tile_rows;
@@ -231,6 +225,13 @@ struct HeadPlan {
 // 46 / 47, 58 / 49, 67 / 62, 98 / 88.
 int32_t head_tile_rows(int64_t rows) {
   return rows > 320 || (rows > 192 && rows <= 256) ? 128 : 64;
+}
+
+bool head_sizes_ok(int32_t dtype, int64_t M, int64_t V, int64_t K) {
+  if (!dtype_ok(dtype) || M < 0 || M >= kMaxRows || V < 1 || V > kMaxVocab || !depth_ok(K)) return false;
+  // the workgroups of a launch
+  const int64_t rows = M < kHeadRows ? M : kHeadRows, tile = head_tile_rows(rows);
+  return (double)((V + 127) / 128) * (double)((rows + tile - 1) / tile) <= (double)q4::kMaxGrid;
 }
 
 HeadPlan plan_head(void* ws, int32_t dtype, int64_t M, int64_t V, int64_t K, int64_t group, bool back) {
