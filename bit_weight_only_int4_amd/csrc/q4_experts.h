@@ -187,7 +187,7 @@ struct BackParams {
   const float* pre;
   const float* weights;
   float* dpre;
-  float* dw_part;          // [slot][2 col_tiles]
+  float* dw_part;          // [slot][col_tiles][waves side by side: 4 of 64 rows, 2 of 128]
   uint32_t* dpre_bits;     // [slot]: the largest magnitude, by maximum
 };
 hipError_t launch_back(const BackParams& p, int32_t tile_rows, bool gate, hipStream_t s);

@@ -18,13 +18,13 @@
 // reads spread over the banks.
 //
 // Tiles of BM rows by 128 columns, four waves of 64 rows by BM/2 columns; the
-// next two steps' loads are in registers while a step's products run.
+// next two steps' loads are in registers while a step's products run (the next
+// step's where LDS holds one stage: 128 rows, NG = 4).
 //
 // Bound: the vector unit, which forms the row operand anew for every tile of
-// columns (6 operations an element in two parts, 4 in one) beside the codes'.
-// 2048 tokens by 4 over 32 experts of 2048 x 1408 in groups of 128, bf16:
-// through down 235 us (two parts), through gate and up 206 (one), 200 and 460
-// TFLOP/s.
+// columns (6 operations an element) beside the codes'.  2048 tokens by 4 over 32
+// experts of 2048 x 1408 in groups of 128, bf16: through down 230 us, through gate
+// and up 275, 205 and 345 TFLOP/s (twice that in its two parts).
 #pragma once
 
 #include "q4_experts.h"

@@ -13,10 +13,10 @@
 //
 // Bound: MFMA against the vector unit's unpacking (9 operations a word) and group
 // sums (64 a group and wave).  Head of 128257 x 2048, a scale per row: 2048 rows
-// of bf16 1.07 ms, 1000 TFLOP/s; 512 of fp32 0.51 ms, twice 530 (a library
+// of bf16 1.07 ms, 1000 TFLOP/s; 512 of fp32 0.49 ms, twice 550 (a library
 // product of binary16, 8192^3, reaches 1324).  4099 tokens by 8 over 64 experts
-// of 2048 x 1024 in groups of 128, bf16: gate and up 374 us, 735 TFLOP/s, down
-// 230, 600, where an eighth of the tiles' rows are empty.
+// of 2048 x 1024 in groups of 128, bf16: gate and up 402 us, 685 TFLOP/s, down (two
+// parts) 335, twice 410, where a ninth of the tiles' rows are empty.
 #pragma once
 
 #include "q4_experts.h"
@@ -39,8 +39,8 @@ struct GemmTile {
   static constexpr int kB = kBN * kBK / 2;
   static constexpr int kScale = GM == kOneGroup ? 0 : kGroupsPerStep * kBN * 4;
   static constexpr int kStage = kA + kB + kScale;
-  // one group: three workgroups a CU of two stages; else two, of three stages
-  // where LDS allows it
+  // one group: two stages (three workgroups a CU, or two of 128 rows in two
+  // parts); else two workgroups, of three stages where LDS allows it
   static constexpr int kStages = GM != kOneGroup && 3 * kStage <= 76 * 1024 ? 3 : 2;
   // vector memory operations a wave issues per step
   static constexpr int kIssue = P * BM / 32 + 1 + (GM == kOneGroup ? 0 : 1);

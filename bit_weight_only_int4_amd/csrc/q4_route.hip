@@ -1,11 +1,11 @@
 // q4_route.hip -- the choice of experts and its gradient, for gfx950.
 //
 // A wave owns a token; lane l holds EPL experts from EPL l on, so that a lower
-// lane has lower experts.  Choosing is top_k rounds of a maximum over the lanes.  Values are ordered as integers: without
-// a bias the logit's 32 bits (scores have their order), with one the 64 bits of
-// score + bias formed in fp64, so that no rounding of a score decides between
-// two experts (fp32 sums of 8192 tokens over 256 experts differ from the exact
-// order in a few places).  An integer of 0 is an expert that is not eligible.
+// lane has lower experts.  Choosing is top_k rounds of a maximum over the lanes.
+// Values are ordered as integers: without a bias the logit's 32 bits (scores have
+// their order), with one the 64 bits of score + bias formed in fp64, so that no
+// rounding of a score decides between two experts (fp32 sums of 8192 tokens over
+// 256 experts differ from the exact order in a few places).  An integer of 0 is an expert that is not eligible.
 //
 // Bound by the vector unit's issue: top_k maxima of 6 cross-lane steps one after
 // the other, and with a bias exponentials in fp64.  8192 tokens, 8 of 256 experts

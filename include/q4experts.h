@@ -12,8 +12,8 @@
  * other for experts: codes uint8 [E, N, K / 2] (4-byte aligned) and scales
  * float [E, ceil(K / group_size), N], or [E, N] when group_size is 0 (a scale
  * per row).  K (hidden, width) is a multiple of 8 up to 32768; group_size is
- * 0, 32 or a multiple of 64 (others: Q4_ERR_UNSUPPORTED).  A group_size >= K is one group.  Weights are
- * constants: gradients are those of the activations.
+ * 0, 32 or a multiple of 64 (others: Q4_ERR_UNSUPPORTED).  A group_size >= K is
+ * one group.  Weights are constants: gradients are those of the activations.
  *
  * Arithmetic: binary16 operands on MFMA with fp32 sums.  A weight's code is
  * exact in binary16.  A row of activations is scaled by a power of two to the
@@ -53,9 +53,9 @@ extern "C" {
  * With s = softmax or sigmoid of the logits, an expert's value is s (without
  * a bias: its logit, which has the same order) or s + bias, formed in 64 bits
  * so that rounding decides no choice.  An expert whose logit or value is -inf
- * is not eligible; NaN ranks below every number.  With groups > 1 the top_groups groups
- * of the largest group value stay: the value of a group's best expert, with a
- * bias the sum of its two best.  Of the experts left, the top_k of the
+ * is not eligible; NaN ranks below every number.  With groups > 1 the
+ * top_groups groups of the largest group value stay: the value of a group's best
+ * expert, with a bias the sum of its two best.  Of the experts left, the top_k of the
  * largest values are chosen, in descending order; ties, also between groups,
  * go to the lowest index.
  *   ids      int32 [T, top_k]; -1 where fewer are eligible
@@ -185,7 +185,8 @@ size_t q4_head_cross_entropy_workspace_bytes(int32_t dtype, int64_t M,
  *   lse      as q4_head_cross_entropy gave it
  *   g_loss   float [M]
  *   dx       [M, K] of `dtype`, row pitch lddx; a row with a negative target
- *            becomes 0, one with a target >= vocab NaN
+ *            becomes 0, one with a target >= vocab NaN, any other with a g_loss
+ *            of 0 becomes 0 whatever its lse
  */
 q4_status q4_head_cross_entropy_backward(
     const void *x, int64_t ldx, int32_t dtype, int64_t M, int64_t vocab,
