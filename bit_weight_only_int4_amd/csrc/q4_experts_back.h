@@ -366,7 +366,8 @@ __global__ void __launch_bounds__(256, 2) back_kernel(const BackParams p) {
           const float sig = sigmoid(g), silu = g * sig;
           dot[i] = __builtin_fmaf(silu * up, z, dot[i]);
           const float dh = sh_weight[row] * z;
-          const float dg = dh * up * sig * __builtin_fmaf(g, sigmoid(-g), 1.0f), du = dh * silu;
+          // (the slope first: dh times up may pass fp32's range)
+          const float dg = dh * (up * (sig * __builtin_fmaf(g, sigmoid(-g), 1.0f))), du = dh * silu;
           float* dst = p.dpre + (int64_t)slot * 2 * K + k;
           dst[0] = dg;
           dst[K] = du;
