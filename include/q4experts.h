@@ -62,7 +62,8 @@ extern "C" {
  *   weights  float [T, top_k]: scale * s, divided by the sum of the chosen s
  *            if renormalize (however small they are); 0 where the id is -1
  * A NaN in a row, or a +inf under softmax, makes the row's weights NaN.
- * experts <= 1024, top_k <= 32, top_k <= experts / groups * top_groups.
+ * T < 2^24, experts <= 1024, top_k <= 32, top_k <= experts / groups *
+ * top_groups.
  */
 q4_status q4_route(const void *logits, int64_t ld, int32_t dtype, int64_t T,
                    int64_t experts, int64_t top_k, int32_t score,
@@ -130,7 +131,8 @@ size_t q4_experts_workspace_bytes(int32_t dtype, int64_t T, int64_t hidden,
  *   pre       as q4_experts gave it for the same x and ids
  *   dx        [T, hidden] of `dtype`, row pitch lddx
  *   dweights  float [T, top_k]; 0 for an empty slot
- * An id >= experts makes its token's dx and its own dweights NaN.
+ * An id >= experts makes its token's dx and its own dweights NaN.  Limits as
+ * q4_experts', of tiles 2^24 - 1.
  */
 q4_status q4_experts_backward(const void *dout, int64_t lddo, int32_t dtype,
                               int64_t T, int64_t hidden, int64_t width,
@@ -161,7 +163,7 @@ size_t q4_experts_backward_workspace_bytes(int32_t dtype, int64_t T,
  *            given all the same).  One >= vocab gives a NaN loss
  *   workspace  q4_head_cross_entropy_workspace_bytes(...) bytes, 16-byte
  *            aligned
- * vocab <= 2^30; a call of more than 2^24 - 1 tiles (64 or 128 rows, of at most
+ * M < 2^24, vocab <= 2^30; a call of more than 2^24 - 1 tiles (64 or 128 rows, of at most
  * 8192, by 128 columns) is refused, as by the gradient.
  */
 q4_status q4_head_cross_entropy(const void *x, int64_t ldx, int32_t dtype,
