@@ -163,8 +163,8 @@ size_t q4_experts_backward_workspace_bytes(int32_t dtype, int64_t T,
  *            given all the same).  One >= vocab gives a NaN loss
  *   workspace  q4_head_cross_entropy_workspace_bytes(...) bytes, 16-byte
  *            aligned
- * M < 2^24, vocab <= 2^30; a call of more than 2^24 - 1 tiles (64 or 128 rows, of at most
- * 8192, by 128 columns) is refused, as by the gradient.
+ * M < 2^24, vocab <= 2^30; a call of more than 2^24 - 1 tiles (64 or 128 rows,
+ * of at most 8192, by 128 columns) is refused, as by the gradient.
  */
 q4_status q4_head_cross_entropy(const void *x, int64_t ldx, int32_t dtype,
                                 int64_t M, int64_t vocab, int64_t K,
